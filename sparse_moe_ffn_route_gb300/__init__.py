@@ -470,3 +470,15 @@ def moe_noalloc_device_status(stream=None):
 
 def moe_status_string(status: int) -> str:
     return _lib.moe_status_string(status).decode()
+
+
+# ----------------------------------------------------------------------------- dense block
+from .block import (BoundCall, GluCfg, GluGrads, GluWeights, NormCfg, NormGrads, W4Cfg, W4Weights,  # noqa: E402,F401
+                    bind_block_norm_backward, bind_block_norm_forward, bind_glu_backward, bind_glu_forward,
+                    bind_w4_linear, block_norm_workspace, glu_cfg, glu_saved, glu_workspace,
+                    moe_block_norm_backward, moe_block_norm_forward, moe_block_norm_workspace_bytes,
+                    moe_glu_backward, moe_glu_forward, moe_glu_saved_bytes, moe_glu_workspace_bytes,
+                    moe_w4_linear, norm_cfg, w4_cfg, w4_quantize)
+from .block import EXPORTED as _BLOCK_EXPORTED  # noqa: E402
+
+EXPORTED += _BLOCK_EXPORTED

@@ -1,0 +1,56 @@
+// Internal contract between the dense block's C-ABI host code (block_abi.cu) and its
+// kernel translation units.
+#pragma once
+
+#include "../../include/moe_block.h"
+#include "internal.h"
+
+namespace moe {
+
+// The gated FFN's shapes and weights.
+struct GluParams {
+  const uint16_t *gate, *up, *down;   // bf16 [ff, d], [ff, d], [d, ff]
+  int d, ff;
+  int act;
+  float limit, alpha;
+};
+
+// What a training forward pass keeps: h row-major; g and u in blocks of 128 tokens x 4
+// columns, [block of tokens][ff / 4][128][4], so that the threads of a warp, which hold
+// one token row each, store and load whole lines.
+struct GluSaved {
+  uint16_t* h;     // bf16 [T, ff]
+  float* g;        // fp32, 128-token blocks
+  float* u;
+};
+
+// tcgen05 kernels (glu_gemm.cu).  Each clears or may set bits of *status.
+// h = act(x Wg^T, x Wu^T); g, u non-null: kept as GluSaved describes.
+cudaError_t launch_glu_gate_up(const GluParams& p, const uint16_t* x, int T, uint16_t* h, float* g, float* u,
+                               uint32_t* status, cudaStream_t s);
+// y = h Wd^T
+cudaError_t launch_glu_down(const GluParams& p, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
+                            cudaStream_t s);
+// dg, du [T, ff] from dy, the saved g and u
+cudaError_t launch_glu_dact(const GluParams& p, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
+                            uint16_t* du, uint32_t* status, cudaStream_t s);
+// dx, dWg, dWu, dWd, each where its pointer is non-null, in one launch
+cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
+                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
+                             uint16_t* dwd, uint32_t* status, cudaStream_t s);
+cudaError_t glu_set_wait_test(uint32_t polls, int withhold);
+
+// Few tokens (skinny.cu): the weights stream through warp MMAs, every 16 tokens.
+cudaError_t launch_skinny_bf16(const uint16_t* w0, const uint16_t* w1, int n_out, int n_in, const uint16_t* x, int T,
+                               const GluParams* act, uint16_t* y, uint32_t* clear_status, cudaStream_t s);
+cudaError_t launch_skinny_w4(const moe_w4_cfg_t& c, const moe_w4_weights_t& w, const uint16_t* x, int T, uint16_t* y,
+                             cudaStream_t s);
+
+// Norms (block_norm.cu).
+cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y,
+                                  uint16_t* a, cudaStream_t s);
+int block_norm_parts(int d, int T);   // rows of the weight gradients' partial sums
+cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, const uint16_t* dy,
+                                  const uint16_t* da, const moe_norm_grads_t& g, float* parts, cudaStream_t s);
+
+}  // namespace moe

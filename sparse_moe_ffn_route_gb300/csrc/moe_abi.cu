@@ -4,6 +4,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block.h"
 #include "internal.h"
 #include "permute_core.cuh"
 
@@ -790,6 +791,7 @@ int moe_test_set_wait_limit(uint32_t max_polls, int32_t withhold_first_load) {
   MOE_CUDA(ring_set_wait_test(max_polls, w));
   MOE_CUDA(fp4_stream_set_wait_test(max_polls, w));
   MOE_CUDA(decode_set_wait_test(max_polls, w));
+  MOE_CUDA(glu_set_wait_test(max_polls, w));
   return MOE_OK;
 }
 
