@@ -1,5 +1,5 @@
 // The dense gated FFN on the 5th-generation tensor cores: its two forward products and
-// the six of its backward pass, all D[128 x N] = A[128 x K] . B[N x K]^T tiles with fp32
+// the six of its backward pass, all D[M x N] = A[M x K] . B[N x K]^T tiles with fp32
 // accumulators in TMEM, fed by TMA through an mbarrier ring.
 //
 //   gate/up:  g = x Wg^T, u = x Wu^T in one tile (the B tile holds nf rows of each), so
@@ -17,9 +17,19 @@
 // 64 columns; the tensor core's descriptors name the form.  Rows and columns past an
 // edge are filled with zeros by the TMA unit, so d, ff and T need no padding.
 //
-// Warp roles of the persistent CTA: warp 0 TMA producer, warp 1 MMA issuer and owner of
-// TMEM (two accumulators of up to 256 columns, so that a tile's epilogue runs under the
-// next tile's MMAs), warps 2..5 epilogue.  Every wait is bounded (see tc::mbar_wait).
+// CG = 2: two CTAs of a cluster share one tile of 256 rows (cta_group::2).  Each holds its
+// 128 rows of A and half of the B tile, and the accumulators of its rows; the tensor cores
+// read the other half of B from the peer.  Against CG = 1 a chunk of 64 k moves 32 KiB
+// into each SM instead of 48 KiB for the same MMAs, which is what bounds CG = 1 (the same
+// tile at 256 columns: 96 bytes per clock and SM).  CG = 1 (128-row tiles) serves outputs
+// of few rows.
+//
+// Warp roles of the persistent CTA: warp 0 TMA producer; warp 1 owner of TMEM and, in the
+// first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
+// epilogue runs under the next tile's MMAs); warps 2..9 epilogue, two per TMEM lane
+// quarter on alternate column chunks; dact: warp 10 copies the saved g and u of the
+// coming chunks into a shared-memory ring, since their latency would otherwise be paid
+// at every chunk.  Every wait is bounded (see tc::mbar_wait).
 #include <cuda.h>
 
 #include <cstring>
@@ -34,24 +44,36 @@ namespace {
 
 constexpr int kBM = 128, kBK = 64, kMaxN = 256;
 constexpr int kTileA = kBM * kBK * 2;
-constexpr int kStageBytes = kTileA + kMaxN * kBK * 2;   // 48 KiB
-constexpr int kStages = 4;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-constexpr int kThreads = 192;
 constexpr int kMaxProblems = 4;
+constexpr int kEpiWarps = 8;
 
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
 
+// Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA), then, for
+// dact, kSlots slots of 16 columns of g and u (128 rows x 16 x 4 bytes each).
+template <int CG, int EPI>
+struct Lay {
+  static constexpr int kBRows = kMaxN / CG;
+  static constexpr int kStageBytes = kTileA + kBRows * kBK * 2;
+  static constexpr int kSlots = EPI == kEpiDact ? 4 : 0;
+  static constexpr int kRing = kSlots ? kSlots : 1;
+  static constexpr int kSlotBytes = 2 * 128 * 16 * 4;
+  static constexpr int kStages = (CG == 2 ? 6 : 4) - (EPI == kEpiDact ? (CG == 2 ? 2 : 1) : 0);
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSlots * kSlotBytes + 1024;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
+};
+
 // One product: D [M, N] over `segs` runs of `nkc` chunks of 64 k.  Run s multiplies
-// a[s] and b[s]; with `pair` (gate/up) every chunk instead takes N / 2 rows of b[0] and
-// N / 2 rows of b[1].
+// a[s] and b[s]; with `pair` (gate/up) the B tile instead takes tn / 2 rows of b[0] and
+// tn / 2 rows of b[1].
 struct Problem {
   CUtensorMap a[2], b[2];
   int M, N;             // rows and columns of the output (pair: columns of h)
   int nkc, segs, pair;
   int a_mn, b_mn;       // 1: MN-major
   int tn;               // columns of B per tile (MMA N)
-  int mt, nt;           // tiles
+  int mt, nt;           // tiles (of 128 CG rows)
+  int wide;             // output rows and base allow 32-byte stores
   uint16_t* out;        // bf16 [M, N]
 };
 
@@ -100,24 +122,149 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-// 16 fp32 -> 16 bf16 at dst (two 16-byte stores; cols: how many are in range, a multiple of 8).
-__device__ __forceinline__ void store_bf16x16(uint16_t* dst, const float (&v)[16], int cols) {
+// 16 fp32 -> 16 bf16 at dst; cols: how many are in range, a multiple of 8; wide: dst is
+// 32-byte aligned (one store per thread writes a whole sector).
+__device__ __forceinline__ void store_bf16x16(uint16_t* dst, const float (&v)[16], int cols, bool wide) {
   uint32_t q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  if (wide && cols > 8) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+                 "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                 : "memory");
+    return;
+  }
   if (cols > 0) reinterpret_cast<uint4*>(dst)[0] = make_uint4(q[0], q[1], q[2], q[3]);
   if (cols > 8) reinterpret_cast<uint4*>(dst)[1] = make_uint4(q[4], q[5], q[6], q[7]);
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_constant__ GemmParams g) {
+// 2 x 16 fp32 accumulator columns of this thread's row, at columns a and b.
+__device__ __forceinline__ void tmem_ld_2x16(uint32_t a, uint32_t b, float (&v)[16], float (&w)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a), "r"(b)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = __uint_as_float(r[i]);
+    w[i] = __uint_as_float(r[16 + i]);
+  }
+}
+
+// ---- the pair forms (PTX ISA, cta_group::2): operands and barriers of two CTAs
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The address of the same shared-memory location in the first CTA of the pair.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  if (CG == 1) {
+    tc::tma_load_2d(dst, map, c0, c1, bar);
+  } else {
+    // into this CTA's shared memory, counted on a barrier of the pair's first CTA
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 1) {
+    tc::umma_bf16(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Arrive on `bar` (CG 2: in both CTAs) once every MMA issued so far has completed.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if (CG == 1) {
+    tc::umma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  if (CG == 1)
+    tc::mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar)) : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst) {
+  if (CG == 1) {
+    tc::tmem_alloc(dst, 512);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dst) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr) {
+  if (CG == 1)
+    tc::tmem_dealloc(addr, 512);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+}
+
+// Plain copy of `bytes` (a multiple of 16) contiguous bytes into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+template <int CG, int EPI>
+__global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(const __grid_constant__ GemmParams g) {
+  using L = Lay<CG, EPI>;
+  constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ __align__(8) uint64_t sfull_bar[L::kRing], sempty_bar[L::kRing];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, consumed_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
   volatile int* abort = &abort_s;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -126,17 +273,22 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tc::smem_u32(&tfull_bar[b]), 1);
-      tc::mbar_init(tc::smem_u32(&tempty_bar[b]), 4);
+      tc::mbar_init(tc::smem_u32(&tempty_bar[b]), kEpiWarps * CG);
+    }
+    for (int s = 0; s < L::kSlots; ++s) {
+      tc::mbar_init(tc::smem_u32(&sfull_bar[s]), 1);
+      tc::mbar_init(tc::smem_u32(&sempty_bar[s]), kEpiWarps / 2);
     }
     tc::mbar_init(tc::smem_u32(&drain_bar), 1);
     abort_s = 0;
     consumed_s = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 1) tc::tmem_alloc(tc::smem_u32(&tmem_base_s), 512);
+  if (warp == 1) tmem_alloc<CG>(tc::smem_u32(&tmem_base_s));
   pdl_wait();
   tc::tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();   // the peer's barriers and TMEM are ready
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   if (g.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0u;
@@ -146,11 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
     if (tc::elect_one()) {
       int s = 0, issued = 0, withheld = -1;
       uint32_t ph = 0;
-      for (int t = blockIdx.x; t < g.tiles && !*abort; t += gridDim.x) {
+      for (int t = unit; t < g.tiles && !*abort; t += units) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
-        const int m0 = tl.m * kBM;
-        const uint32_t bytes = (uint32_t)kTileA + (uint32_t)p.tn * 128u;
+        const int m0 = (tl.m * CG + rank) * kBM;
+        const int half = p.tn >> 1;                          // pair: rows of gate, of up
+        const int brows = p.tn / CG;                         // rows of B in this CTA
+        const int n0 = p.pair ? tl.n * half : tl.n * p.tn + rank * brows;
+        const int boxes = p.b_mn ? (brows + 63) / 64 : 0;    // MN-major boxes of 64 columns
+        const uint32_t bytes = (uint32_t)kTileA + (p.b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u);
         for (int c = 0; c < p.nkc * p.segs; ++c) {
           if (!tc::mbar_wait(tc::smem_u32(&empty_bar[s]), ph ^ 1, abort, g.status)) break;
           if (*abort) break;   // a slot freed by an abort is not refilled
@@ -159,24 +315,27 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
           } else {
             const int seg = c >= p.nkc;
             const int k0 = (c - seg * p.nkc) * kBK;
-            const uint32_t fb = tc::smem_u32(&full_bar[s]);
+            const uint32_t own = tc::smem_u32(&full_bar[s]);
+            const uint32_t fb = CG == 2 ? in_leader(own) : own;
             const uint32_t sa = tc::smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
-            tc::mbar_arrive_expect_tx(fb, bytes);
+            if (rank == 0) tc::mbar_arrive_expect_tx(own, CG * bytes);   // the peer's loads count here too
             if (p.a_mn) {
-              tc::tma_load_2d(sa, &p.a[seg], m0, k0, fb);
-              tc::tma_load_2d(sa + 8192, &p.a[seg], m0 + 64, k0, fb);
+              load_tile<CG>(sa, &p.a[seg], m0, k0, fb);
+              load_tile<CG>(sa + 8192, &p.a[seg], m0 + 64, k0, fb);
             } else {
-              tc::tma_load_2d(sa, &p.a[seg], k0, m0, fb);
+              load_tile<CG>(sa, &p.a[seg], k0, m0, fb);
             }
             if (p.pair) {
-              const int nf = p.tn >> 1;
-              tc::tma_load_2d(sb, &p.b[0], k0, tl.n * nf, fb);
-              tc::tma_load_2d(sb + (uint32_t)nf * 128u, &p.b[1], k0, tl.n * nf, fb);
+              if (CG == 2) {
+                load_tile<CG>(sb, &p.b[rank], k0, n0, fb);
+              } else {
+                load_tile<CG>(sb, &p.b[0], k0, n0, fb);
+                load_tile<CG>(sb + (uint32_t)half * 128u, &p.b[1], k0, n0, fb);
+              }
             } else if (p.b_mn) {
-              for (int j = 0; j < p.tn / 64; ++j)
-                tc::tma_load_2d(sb + 8192u * j, &p.b[seg], tl.n * p.tn + 64 * j, k0, fb);
+              for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, &p.b[seg], n0 + 64 * j, k0, fb);
             } else {
-              tc::tma_load_2d(sb, &p.b[seg], k0, tl.n * p.tn, fb);
+              load_tile<CG>(sb, &p.b[seg], k0, n0, fb);
             }
             ++issued;
           }
@@ -186,8 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
           }
         }
       }
-      if (*abort) {
-        // Drain: wait (bounded, whatever the abort flag says) for the loads still in flight.
+      if (*abort && rank == 0) {
+        // Drain: wait (bounded, whatever the abort flag says) for the loads still in
+        // flight; the peer's are counted on the same barriers, and the cluster barrier
+        // at the end keeps it here meanwhile.
         int zero = 0;
         volatile int* never = &zero;
         for (int i = consumed_s; i < issued; ++i)
@@ -197,15 +358,15 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (tc::elect_one()) {
+    if (rank == 0 && tc::elect_one()) {
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 0;
       bool any = false;
-      for (int t = blockIdx.x; t < g.tiles && !*abort; t += gridDim.x) {
+      for (int t = unit; t < g.tiles && !*abort; t += units) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
         const uint32_t idesc =
-            tc::idesc_bf16_f32(kBM, p.tn) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
+            tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
         const uint32_t astep = p.a_mn ? 128u : 2u, bstep = p.b_mn ? 128u : 2u;   // 16 k, in 16-byte units
         if (!tc::mbar_wait(tc::smem_u32(&tempty_bar[b]), aph ^ 1, abort, g.status)) break;
         tc::tc_fence_after();
@@ -223,9 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
           const uint64_t ad = p.a_mn ? sdesc_mn_sw128(sa) : tc::sdesc_sw128(sa);
           const uint64_t bd = p.b_mn ? sdesc_mn_sw128(sb) : tc::sdesc_sw128(sb);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            tc::umma_bf16(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
-          tc::umma_commit(tc::smem_u32(&empty_bar[s]));
+          for (int j = 0; j < kBK / 16; ++j) mma<CG>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
+          commit<CG>(tc::smem_u32(&empty_bar[s]));
           any = true;
           if (++s == kStages) {
             s = 0;
@@ -233,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
           }
         }
         if (!ok) break;
-        tc::umma_commit(tc::smem_u32(&tfull_bar[b]));
+        commit<CG>(tc::smem_u32(&tfull_bar[b]));
         if (++b == 2) {
           b = 0;
           aph ^= 1;
@@ -241,77 +401,137 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
       }
       if (*abort && any) {
         // Let every MMA issued so far finish before TMEM is released.
-        tc::umma_commit(tc::smem_u32(&drain_bar));
+        commit<CG>(tc::smem_u32(&drain_bar));
         int zero = 0;
         volatile int* never = &zero;
         tc::mbar_wait(tc::smem_u32(&drain_bar), 0, never, g.status);
       }
     }
+  } else if (EPI == kEpiDact && warp == 2 + kEpiWarps) {
+    // ---------------------------------------------------------------- saved g, u
+    // 16 columns of the CTA's 128 rows are 8 KiB of g and 8 KiB of u, contiguous each.
+    if (tc::elect_one()) {
+      int slot = 0, filled = 0;
+      uint32_t ph = 0;
+      for (int t = unit; t < g.tiles && !*abort; t += units) {
+        const Tile tl = tile_at(g, t);
+        const Problem& p = g.p[tl.pi];
+        const int mb = tl.m * CG + rank;
+        const int n0 = tl.n * p.tn, cols = min(p.tn, p.N - n0);
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+          if (!tc::mbar_wait(tc::smem_u32(&sempty_bar[slot]), ph ^ 1, abort, g.status) || *abort) break;
+          const uint32_t fb = tc::smem_u32(&sfull_bar[slot]);
+          if (mb * kBM < p.M) {
+            const uint32_t n = (uint32_t)min(16, cols - c0) * 512u;
+            const size_t at = ((size_t)mb * p.N + n0 + c0) * 128;   // floats
+            const uint32_t dst = tc::smem_u32(smem + kStages * kStageBytes + slot * L::kSlotBytes);
+            tc::mbar_arrive_expect_tx(fb, 2 * n);
+            bulk_load(dst, g.g + at, n, fb);
+            bulk_load(dst + L::kSlotBytes / 2, g.u + at, n, fb);
+          } else {
+            tc::mbar_arrive(fb);   // a tile row block past the last token
+          }
+          ++filled;
+          if (++slot == L::kSlots) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (*abort) {
+        int zero = 0;
+        volatile int* never = &zero;
+        for (int i = filled > L::kSlots ? filled - L::kSlots : 0; i < filled; ++i)
+          tc::mbar_wait(tc::smem_u32(&sfull_bar[i % L::kRing]), (i / L::kRing) & 1, never, g.status);
+      }
+    }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;                 // TMEM lane quarter this warp may read
+    const int par = (warp - 2) >> 2;        // takes column chunks of this parity
     const int row = 32 * q + lane;
-    int b = 0;
+    int b = 0, sl = 0;                      // sl: dact, chunks seen (slot sl % kSlots)
     uint32_t aph = 0;
-    for (int t = blockIdx.x; t < g.tiles && !*abort; t += gridDim.x) {
+    for (int t = unit; t < g.tiles && !*abort; t += units) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.pi];
       if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * 256u;
-      const int m = tl.m * kBM + row;
-      const bool valid = m < p.M;
+      const int mb = tl.m * CG + rank;
+      const int m = mb * kBM + row;
+      const bool valid = m < p.M, wide = p.wide;
       const int tn = p.pair ? p.tn >> 1 : p.tn;
       const int n0 = tl.n * tn, cols = min(tn, p.N - n0);
       uint16_t* orow = p.out + (size_t)m * p.N + n0;
-      const size_t blk = ((size_t)tl.m * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        float v[16];
-        tc::tmem_ld16(taddr + (uint32_t)c0, v);
-        const int left = cols - c0;
-        if (EPI == kEpiGlu) {
-          float w[16];
-          tc::tmem_ld16(taddr + (uint32_t)(tn + c0), w);
+      if (EPI == kEpiGlu) {
+        const size_t blk = ((size_t)mb * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
+        for (int c0 = 16 * par; c0 < cols; c0 += 32) {
+          float v[16], w[16];
+          tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), v, w);
+          const int left = cols - c0;
           if (valid) {
             if (g.g) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (4 * i < left) {
                   const size_t at = blk + (size_t)(c0 / 4 + i) * 128;
-                  reinterpret_cast<float4*>(g.g)[at] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                  reinterpret_cast<float4*>(g.u)[at] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                  __stcs(reinterpret_cast<float4*>(g.g) + at, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                  __stcs(reinterpret_cast<float4*>(g.u) + at, make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
                 }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = glu_value(g.act, v[i], w[i]);
-            store_bf16x16(orow + c0, v, left);
+            store_bf16x16(orow + c0, v, left, wide);
           }
-        } else if (EPI == kEpiDact) {
+        }
+      } else if (EPI == kEpiDact) {
+        const int n_chunks = (cols + 15) / 16;
+        for (int j = 0; j < n_chunks; ++j) {
+          const int n = sl + j;
+          if ((n & 1) != par) continue;
+          const int slot = n % L::kRing, c0 = 16 * j;
+          float v[16], du[16];
+          tc::tmem_ld16(taddr + (uint32_t)c0, v);
+          if (!tc::mbar_wait(tc::smem_u32(&sfull_bar[slot]), (n / L::kRing) & 1, abort, g.status)) break;
+          const float4* gs = reinterpret_cast<const float4*>(smem + kStages * kStageBytes + slot * L::kSlotBytes) + row;
+          const float4* us = gs + L::kSlotBytes / 32;
+          const int left = cols - c0;
           if (valid) {
-            float du[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float4 gv = make_float4(0.f, 0.f, 0.f, 0.f), uv = gv;
               if (4 * i < left) {
-                const size_t at = blk + (size_t)(c0 / 4 + i) * 128;
-                gv = reinterpret_cast<const float4*>(g.g)[at];
-                uv = reinterpret_cast<const float4*>(g.u)[at];
+                gv = gs[128 * i];
+                uv = us[128 * i];
               }
               glu_grad(g.act, gv.x, uv.x, v[4 * i], v[4 * i], du[4 * i]);
               glu_grad(g.act, gv.y, uv.y, v[4 * i + 1], v[4 * i + 1], du[4 * i + 1]);
               glu_grad(g.act, gv.z, uv.z, v[4 * i + 2], v[4 * i + 2], du[4 * i + 2]);
               glu_grad(g.act, gv.w, uv.w, v[4 * i + 3], v[4 * i + 3], du[4 * i + 3]);
             }
-            store_bf16x16(orow + c0, v, left);
-            store_bf16x16(g.out2 + (size_t)m * p.N + n0 + c0, du, left);
           }
-        } else if (valid) {
-          store_bf16x16(orow + c0, v, left);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sempty_bar[slot]));
+          if (valid) {
+            store_bf16x16(orow + c0, v, left, wide);
+            store_bf16x16(g.out2 + (size_t)m * p.N + n0 + c0, du, left, wide);
+          }
+        }
+        sl += n_chunks;
+      } else {
+        for (int c0 = 32 * par; c0 < cols; c0 += 64) {
+          float v[16], w[16];
+          tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(c0 + 16), v, w);
+          if (valid) {
+            store_bf16x16(orow + c0, v, cols - c0, wide);
+            store_bf16x16(orow + c0 + 16, w, cols - c0 - 16, wide);
+          }
         }
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&tempty_bar[b]));
+      if (lane == 0) arrive_leader<CG>(tc::smem_u32(&tempty_bar[b]));
       if (++b == 2) {
         b = 0;
         aph ^= 1;
@@ -322,8 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1) glu_gemm_kernel(const __grid_cons
   pdl_trigger();
   tc::tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc<CG>(tmem);
 }
 
 // ---------------------------------------------------------------- host
@@ -334,35 +555,102 @@ bool map_bf16(CUtensorMap* m, const uint16_t* base, int rows, int cols, int box_
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// Columns of B per tile: the widest of 256, 128, 64 (32) whose tiles still give every SM
-// one.  `cols` output columns; a tile covers tn / per of them.
-int pick_tn(int mt, int cols, int per, int least) {
-  const int sms = sm_count();
-  int tn = kMaxN;
-  while (tn > least && (long long)mt * cdiv(cols, tn / per) < sms) tn >>= 1;
-  return tn;
-}
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-template <int EPI>
-cudaError_t launch(GemmParams& g, cudaStream_t s) {
+template <int CG, int EPI>
+cudaError_t prepare_kernel() {
   static bool done[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !done[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(glu_gemm_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
+  if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(glu_gemm_kernel<CG, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Lay<CG, EPI>::kSmemBytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+// SMs, and pairs of SMs that can hold a cluster of two at one time.
+int pair_count() {
+  static int n[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return sm_count() / 2;
+  if (n[dev]) return n[dev];
+  if (prepare_kernel<2, kEpiStore>() != cudaSuccess) return sm_count() / 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sm_count() / 2 * 2);
+  cfg.blockDim = dim3(Lay<2, kEpiStore>::kThreads);
+  cfg.dynamicSmemBytes = Lay<2, kEpiStore>::kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int c = 0;
+  if (cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore>, &cfg) != cudaSuccess || c < 1) c = sm_count() / 2;
+  return n[dev] = c;
+}
+
+template <int CG, int EPI>
+cudaError_t launch_cg(const GemmParams& g, cudaStream_t s) {
+  const cudaError_t e = prepare_kernel<CG, EPI>();
+  if (e != cudaSuccess) return e;
+  const int units = CG == 2 ? pair_count() : sm_count();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CG * (g.tiles < units ? g.tiles : units));
+  cfg.blockDim = dim3(Lay<CG, EPI>::kThreads);
+  cfg.dynamicSmemBytes = Lay<CG, EPI>::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<CG, EPI>, g);
+}
+
+template <int EPI>
+cudaError_t launch(GemmParams& g, int cg, cudaStream_t s) {
   g.tiles = 0;
   for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt;
-  const int sms = sm_count();
-  return launch_pdl(glu_gemm_kernel<EPI>, dim3(g.tiles < sms ? g.tiles : sms), dim3(kThreads), kSmemBytes, s, g);
+  return cg == 2 ? launch_cg<2, EPI>(g, s) : launch_cg<1, EPI>(g, s);
+}
+
+// Clocks of one chunk of 64 k with tn columns of B: the MMAs (2 per column for the 128
+// rows of an SM) or its operands' way into shared memory (about 64 bytes per clock).
+int chunk_clocks(int cg, int tn) {
+  const int mma = 2 * tn, feed = (kTileA + tn * 128 / cg) / 64;
+  return mma > feed ? mma : feed;
+}
+
+// The tile of one product [M, N] (per = 2: gate/up, N columns of each) alone on the GPU:
+// pairs or single CTAs, and the columns of B per tile, for which
+//   waves of tiles x (chunks x clocks per chunk + a tile's fixed cost)
+// is least.
+constexpr int kTileClocks = 2500;
+void pick_tile(int M, int N, int chunks, int per, int* cg, int* tn) {
+  long long best = -1;
+  for (int c = 1; c <= 2; ++c) {
+    const int units = c == 2 ? pair_count() : sm_count();
+    for (int n = 256; n >= 32; n -= 32) {
+      const long long tiles = (long long)cdiv(M, kBM * c) * cdiv(N, n / per);
+      const long long cost = (tiles + units - 1) / units * ((long long)chunks * chunk_clocks(c, n) + kTileClocks);
+      if (best < 0 || cost < best) {
+        best = cost;
+        *cg = c;
+        *tn = n;
+      }
+    }
+  }
 }
 
 // D [M, N] = sum over segments of A_s B_s^T, k of length K in each.  a_mn / b_mn: the
 // operand is stored [K, M] / [K, N].
-bool set_problem(Problem& p, int M, int N, int K, const uint16_t* a0, const uint16_t* a1, bool a_mn,
+bool set_problem(Problem& p, int cg, int tn, int M, int N, int K, const uint16_t* a0, const uint16_t* a1, bool a_mn,
                  const uint16_t* b0, const uint16_t* b1, bool b_mn, uint16_t* out) {
   p.M = M;
   p.N = N;
@@ -371,15 +659,16 @@ bool set_problem(Problem& p, int M, int N, int K, const uint16_t* a0, const uint
   p.pair = 0;
   p.a_mn = a_mn;
   p.b_mn = b_mn;
-  p.mt = cdiv(M, kBM);
-  p.tn = pick_tn(p.mt, N, 1, 64);
-  p.nt = cdiv(N, p.tn);
+  p.mt = cdiv(M, kBM * cg);
+  p.tn = tn;
+  p.nt = cdiv(N, tn);
+  p.wide = N % 16 == 0 && aligned32(out);
   p.out = out;
   const uint16_t* a[2] = {a0, a1};
   const uint16_t* b[2] = {b0, b1};
   for (int i = 0; i < p.segs; ++i) {
     if (!(a_mn ? map_bf16(&p.a[i], a[i], K, M, 64) : map_bf16(&p.a[i], a[i], M, K, kBM))) return false;
-    if (!(b_mn ? map_bf16(&p.b[i], b[i], K, N, 64) : map_bf16(&p.b[i], b[i], N, K, p.tn))) return false;
+    if (!(b_mn ? map_bf16(&p.b[i], b[i], K, N, 64) : map_bf16(&p.b[i], b[i], N, K, tn / cg))) return false;
   }
   return true;
 }
@@ -397,9 +686,11 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   p.nkc = cdiv(w.d, kBK);
   p.segs = 1;
   p.pair = 1;
-  p.mt = cdiv(T, kBM);
-  p.tn = pick_tn(p.mt, w.ff, 2, 32);
+  int cg;
+  pick_tile(T, w.ff, p.nkc, 2, &cg, &p.tn);
+  p.mt = cdiv(T, kBM * cg);
   p.nt = cdiv(w.ff, p.tn / 2);
+  p.wide = w.ff % 16 == 0 && aligned32(h);
   p.out = h;
   if (!map_bf16(&p.a[0], x, T, w.d, kBM) || !map_bf16(&p.b[0], w.gate, w.ff, w.d, p.tn / 2) ||
       !map_bf16(&p.b[1], w.up, w.ff, w.d, p.tn / 2))
@@ -409,7 +700,7 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   g.u = su;
   g.status = status;
   g.clear_status = 1;
-  return launch<kEpiGlu>(g, s);
+  return launch<kEpiGlu>(g, cg, s);
 }
 
 cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
@@ -417,9 +708,11 @@ cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.n_problems = 1;
-  if (!set_problem(g.p[0], T, w.d, w.ff, h, nullptr, false, w.down, nullptr, false, y)) return cudaErrorInvalidValue;
+  int cg, tn;
+  pick_tile(T, w.d, cdiv(w.ff, kBK), 1, &cg, &tn);
+  if (!set_problem(g.p[0], cg, tn, T, w.d, w.ff, h, nullptr, false, w.down, nullptr, false, y)) return cudaErrorInvalidValue;
   g.status = status;
-  return launch<kEpiStore>(g, s);
+  return launch<kEpiStore>(g, cg, s);
 }
 
 cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
@@ -427,14 +720,17 @@ cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.n_problems = 1;
-  if (!set_problem(g.p[0], T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg)) return cudaErrorInvalidValue;
+  int cg, tn;
+  pick_tile(T, w.ff, cdiv(w.d, kBK), 1, &cg, &tn);
+  if (!set_problem(g.p[0], cg, tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg)) return cudaErrorInvalidValue;
+  g.p[0].wide = g.p[0].wide && aligned32(du);
   g.act = GluAct{w.act, w.limit, w.alpha};
   g.g = sv.g;
   g.u = sv.u;
   g.out2 = du;
   g.status = status;
   g.clear_status = 1;
-  return launch<kEpiDact>(g, s);
+  return launch<kEpiDact>(g, cg, s);
 }
 
 cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
@@ -443,15 +739,21 @@ cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, const uint16
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   bool ok = true;
-  // the weights' gradients first: their sums over the tokens are the longest tiles
-  if (dwg) ok = ok && set_problem(g.p[g.n_problems++], w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
-  if (dwu) ok = ok && set_problem(g.p[g.n_problems++], w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
-  if (dwd) ok = ok && set_problem(g.p[g.n_problems++], w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd);
-  if (dx) ok = ok && set_problem(g.p[g.n_problems++], T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
+  // the longest tiles first: dx sums over 2 ff, the weights' gradients over T
+  const int cg = w.d > kBM && w.ff > kBM && T > kBM ? 2 : 1, tn = kMaxN;
+  const bool dx_first = 2 * w.ff > T;
+  auto add_dx = [&] {
+    if (dx) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
+  };
+  if (dx_first) add_dx();
+  if (dwg) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
+  if (dwu) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
+  if (dwd) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd);
+  if (!dx_first) add_dx();
   if (!ok) return cudaErrorInvalidValue;
   if (!g.n_problems) return cudaSuccess;
   g.status = status;
-  return launch<kEpiStore>(g, s);
+  return launch<kEpiStore>(g, cg, s);
 }
 
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold) { return tc::set_wait_test(polls, withhold); }
