@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t sfull_bar[L::kRing], sempty_bar[L::kRing];
   __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s, consumed_s;
+  __shared__ int abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
     }
     tc::mbar_init(tc::smem_u32(&drain_bar), 1);
     abort_s = 0;
-    consumed_s = 0;
     tc::fence_barrier_init();
   }
   if (warp == 1) tmem_alloc<CG>(tc::smem_u32(&tmem_base_s));
@@ -295,65 +294,67 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
+    // Everything that a chunk needs is in registers: with the parameters read per chunk
+    // this thread took 527 clocks a chunk and the MMAs (512) waited for it.
     if (tc::elect_one()) {
-      int s = 0, issued = 0, withheld = -1;
+      int s = 0, issued = 0, withheld = tc::withheld_load(0, blockIdx.x == 0) ? 0 : -1;
       uint32_t ph = 0;
+      const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
+      const uint32_t lead0 = CG == 2 ? in_leader(full0) : full0, stage0 = tc::smem_u32(smem);
       for (int t = unit; t < g.tiles && !*abort; t += units) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
         const int m0 = (tl.m * CG + rank) * kBM;
+        const bool a_mn = p.a_mn, b_mn = p.b_mn, two_b = CG == 1 && p.pair;
         const int half = p.tn >> 1;                          // pair: rows of gate, of up
         const int brows = p.tn / CG;                         // rows of B in this CTA
         const int n0 = p.pair ? tl.n * half : tl.n * p.tn + rank * brows;
-        const int boxes = p.b_mn ? (brows + 63) / 64 : 0;    // MN-major boxes of 64 columns
-        const uint32_t bytes = (uint32_t)kTileA + (p.b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u);
-        for (int c = 0; c < p.nkc * p.segs; ++c) {
-          if (!tc::mbar_wait(tc::smem_u32(&empty_bar[s]), ph ^ 1, abort, g.status)) break;
-          if (*abort) break;   // a slot freed by an abort is not refilled
-          if (tc::withheld_load(issued, blockIdx.x == 0)) {
-            withheld = issued++;
-          } else {
-            const int seg = c >= p.nkc;
-            const int k0 = (c - seg * p.nkc) * kBK;
-            const uint32_t own = tc::smem_u32(&full_bar[s]);
-            const uint32_t fb = CG == 2 ? in_leader(own) : own;
-            const uint32_t sa = tc::smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
-            if (rank == 0) tc::mbar_arrive_expect_tx(own, CG * bytes);   // the peer's loads count here too
-            if (p.a_mn) {
-              load_tile<CG>(sa, &p.a[seg], m0, k0, fb);
-              load_tile<CG>(sa + 8192, &p.a[seg], m0 + 64, k0, fb);
-            } else {
-              load_tile<CG>(sa, &p.a[seg], k0, m0, fb);
+        const int boxes = b_mn ? (brows + 63) / 64 : 0;      // MN-major boxes of 64 columns
+        const uint32_t bytes = CG * ((uint32_t)kTileA + (b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u));
+        const int nkc = p.nkc, segs = p.segs;
+        bool ok = true;
+        for (int seg = 0; seg < segs && ok; ++seg) {
+          const CUtensorMap* ma = &p.a[seg];
+          const CUtensorMap* mb = p.pair ? &p.b[CG == 2 ? rank : 0] : &p.b[seg];
+          const CUtensorMap* mb1 = &p.b[1];
+          for (int c = 0, k0 = 0; c < nkc; ++c, k0 += kBK) {
+            if (!tc::mbar_wait(empty0 + 8u * s, ph ^ 1, abort, g.status)) {
+              ok = false;
+              break;
             }
-            if (p.pair) {
-              if (CG == 2) {
-                load_tile<CG>(sb, &p.b[rank], k0, n0, fb);
+            if (issued != withheld) {
+              const uint32_t fb = lead0 + 8u * s, sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + kTileA;
+              if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8u * s, bytes);   // the peer's loads count here too
+              if (a_mn) {
+                load_tile<CG>(sa, ma, m0, k0, fb);
+                load_tile<CG>(sa + 8192, ma, m0 + 64, k0, fb);
               } else {
-                load_tile<CG>(sb, &p.b[0], k0, n0, fb);
-                load_tile<CG>(sb + (uint32_t)half * 128u, &p.b[1], k0, n0, fb);
+                load_tile<CG>(sa, ma, k0, m0, fb);
               }
-            } else if (p.b_mn) {
-              for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, &p.b[seg], n0 + 64 * j, k0, fb);
-            } else {
-              load_tile<CG>(sb, &p.b[seg], k0, n0, fb);
+              if (b_mn) {
+                for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, mb, n0 + 64 * j, k0, fb);
+              } else {
+                load_tile<CG>(sb, mb, k0, n0, fb);
+                if (two_b) load_tile<CG>(sb + (uint32_t)half * 128u, mb1, k0, n0, fb);
+              }
             }
             ++issued;
-          }
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1;
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
         }
+        if (!ok) break;
       }
       if (*abort && rank == 0) {
-        // Drain: wait (bounded, whatever the abort flag says) for the loads still in
-        // flight; the peer's are counted on the same barriers, and the cluster barrier
-        // at the end keeps it here meanwhile.
+        // Drain: wait (bounded, whatever the abort flag says) for the last load of each
+        // stage; the peer's are counted on the same barriers, and the cluster barrier at
+        // the end keeps it here meanwhile.
         int zero = 0;
         volatile int* never = &zero;
-        for (int i = consumed_s; i < issued; ++i)
-          if (i != withheld)
-            tc::mbar_wait(tc::smem_u32(&full_bar[i % kStages]), (i / kStages) & 1, never, g.status);
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          if (i != withheld) tc::mbar_wait(full0 + 8u * (i % kStages), (i / kStages) & 1, never, g.status);
       }
     }
   } else if (warp == 1) {
@@ -362,30 +363,31 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 0;
       bool any = false;
+      const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
+      const uint32_t stage0 = tc::smem_u32(smem);
       for (int t = unit; t < g.tiles && !*abort; t += units) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
-        const uint32_t idesc =
-            tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
-        const uint32_t astep = p.a_mn ? 128u : 2u, bstep = p.b_mn ? 128u : 2u;   // 16 k, in 16-byte units
+        const bool a_mn = p.a_mn, b_mn = p.b_mn;
+        const uint32_t idesc = tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+        const uint32_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;   // 16 k, in 16-byte units
+        const uint64_t ad0 = a_mn ? sdesc_mn_sw128(stage0) : tc::sdesc_sw128(stage0);
+        const uint64_t bd0 = b_mn ? sdesc_mn_sw128(stage0 + kTileA) : tc::sdesc_sw128(stage0 + kTileA);
         if (!tc::mbar_wait(tc::smem_u32(&tempty_bar[b]), aph ^ 1, abort, g.status)) break;
         tc::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)b * 256u;
         bool ok = true;
         const int chunks = p.nkc * p.segs;
         for (int c = 0; c < chunks; ++c) {
-          if (!tc::mbar_wait(tc::smem_u32(&full_bar[s]), ph, abort, g.status)) {
+          if (!tc::mbar_wait(full0 + 8u * s, ph, abort, g.status)) {
             ok = false;
             break;
           }
-          consumed_s = consumed_s + 1;
           tc::tc_fence_after();
-          const uint32_t sa = tc::smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
-          const uint64_t ad = p.a_mn ? sdesc_mn_sw128(sa) : tc::sdesc_sw128(sa);
-          const uint64_t bd = p.b_mn ? sdesc_mn_sw128(sb) : tc::sdesc_sw128(sb);
+          const uint64_t ad = ad0 + (uint32_t)s * (kStageBytes >> 4), bd = bd0 + (uint32_t)s * (kStageBytes >> 4);
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j) mma<CG>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
-          commit<CG>(tc::smem_u32(&empty_bar[s]));
+          commit<CG>(empty0 + 8u * s);
           any = true;
           if (++s == kStages) {
             s = 0;
