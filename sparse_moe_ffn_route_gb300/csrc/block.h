@@ -41,8 +41,12 @@ cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, const uint16
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold);
 
 // Few tokens (skinny.cu): the weights stream through warp MMAs, every 16 tokens.
-cudaError_t launch_skinny_bf16(const uint16_t* w0, const uint16_t* w1, int n_out, int n_in, const uint16_t* x, int T,
-                               const GluParams* act, uint16_t* y, uint32_t* clear_status, cudaStream_t s);
+// x_lo, y_lo: the low halves of a two-part x or h (at most 8 tokens); a two-part h carries
+// what rounding h to bf16 would lose into the down product.  early: the launch before it on
+// the stream was this function's (the weights may be read before its results are there).
+cudaError_t launch_skinny_bf16(const uint16_t* w0, const uint16_t* w1, int n_out, int n_in, const uint16_t* x,
+                               const uint16_t* x_lo, int T, const GluParams* act, uint16_t* y, uint16_t* y_lo,
+                               uint32_t* clear_status, bool early, cudaStream_t s);
 cudaError_t launch_skinny_w4(const moe_w4_cfg_t& c, const moe_w4_weights_t& w, const uint16_t* x, int T, uint16_t* y,
                              cudaStream_t s);
 

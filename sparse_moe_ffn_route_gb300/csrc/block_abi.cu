@@ -130,8 +130,11 @@ int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const mo
   uint16_t* yo = static_cast<uint16_t*>(y);
   if (!saved && T <= kSkinnyTokens) {
     uint16_t* h = reinterpret_cast<uint16_t*>(base + L.h);
-    BLOCK_CUDA(launch_skinny_bf16(p.gate, p.up, p.ff, p.d, xi, T, &p, h, status, s));
-    BLOCK_CUDA(launch_skinny_bf16(p.down, nullptr, p.d, p.ff, h, T, nullptr, yo, nullptr, s));
+    // Few products per output leave h's rounding to bf16 visible beside y's own (1.6 times
+    // y's error alone at one token and ff 512), so h then keeps its low half as well.
+    uint16_t* lo = T <= 8 ? reinterpret_cast<uint16_t*>(base + L.du) : nullptr;
+    BLOCK_CUDA(launch_skinny_bf16(p.gate, p.up, p.ff, p.d, xi, nullptr, T, &p, h, lo, status, false, s));
+    BLOCK_CUDA(launch_skinny_bf16(p.down, nullptr, p.d, p.ff, h, lo, T, nullptr, yo, nullptr, nullptr, true, s));
     return MOE_OK;
   }
   GluSaved sv{reinterpret_cast<uint16_t*>(base + L.h), nullptr, nullptr};

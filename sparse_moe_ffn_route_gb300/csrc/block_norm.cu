@@ -3,11 +3,15 @@
 // gradients of the same.
 //
 // Bound by memory: forward reads x, z and writes y, a (8 bytes per element), backward
-// reads x, z, dy, da and writes dx, dz (12 bytes).  One CTA holds one row at a time in
-// registers, 8 elements (one 16-byte vector) per thread and step, so every tensor passes
-// memory once; the row sums cross the CTA through shared memory (forward: sum z^2, then
-// sum y^2; backward: sum z^2, then sum y^2 and sum da pre_w y together, then
-// sum D post_w z, from which both dgate and dz follow).
+// reads x, z, dy, da and writes dx, dz (12 bytes).  One CTA works on one row at a time, 8
+// elements (one 16-byte vector) per thread and step, so every tensor passes memory once.
+// Each thread copies its own vectors of the next rows into shared memory ahead of time
+// (cp.async: the rows' latency stays off the chain of sums, and needs no registers and no
+// barrier, since a thread reads only what it copied).  The row sums cross the CTA through
+// shared memory (forward: sum z^2, then sum y^2; backward: sum z^2, then sum y^2 and
+// sum da pre_w y together, then sum D post_w z, from which both dgate and dz follow).
+// The sums of y are taken from y itself and not expanded into sums of x and z, which
+// would cost one exchange less but cancel where the branch takes back the residual.
 //
 // Backward: with rz = 1 / sqrt(mean z^2 + eps), ry alike for y, c the branch's factor,
 //   D  = dy + ry (da pre_w - y ry^2 mean(da pre_w y))        (gradient of y)
@@ -25,7 +29,8 @@ namespace {
 constexpr int kMaxWarps = 16;
 
 // Sum of N values over the CTA, in every thread, in a fixed order.  `buf` holds
-// N * kMaxWarps floats; consecutive calls alternate between two buffers.
+// N * kMaxWarps floats; a row's sums use buffers of their own, and rows alternate between
+// two sets (a warp a row ahead waits at that row's first barrier for the last reader).
 template <int N>
 __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -39,8 +44,12 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    v[i] = 0.f;
-    for (int w = 0; w < nw; ++w) v[i] += buf[i * kMaxWarps + w];
+    float s = 0.f;
+    for (int w = 0; w < nw; w += 4) {   // slots past the last warp hold zeros
+      const float4 q = *reinterpret_cast<const float4*>(buf + i * kMaxWarps + w);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+    v[i] = s;
   }
 }
 
@@ -70,214 +79,272 @@ struct NormArgs {
   float *dgate, *part;   // part: [gridDim.x][2][d] (dpost_w, dpre_w), or null
 };
 
-__device__ __forceinline__ uint4 ld8(const uint16_t* p, size_t at) { return *reinterpret_cast<const uint4*>(p + at); }
+__device__ __forceinline__ uint4 ld8(const uint16_t* p, int at) { return *reinterpret_cast<const uint4*>(p + at); }
 
-// V vectors of 8 elements per thread: element 8 (threadIdx.x + i blockDim.x).
-template <int V>
-__global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const NormArgs g) {
-  __shared__ float buf[2][kMaxWarps];
-  pdl_wait();
-  const float inv_d = 1.f / (float)g.d;
-  for (int t = blockIdx.x; t < g.T; t += gridDim.x) {
-    const size_t base = (size_t)t * g.d;
-    float y[V][8];
-    if (g.z) {
-      float z[V][8], ss[1] = {0.f};
+// This thread's vectors of a row, and the copies of the rows ahead: DEPTH slots of NA arrays.
+// Vector i holds elements 8 (threadIdx.x + i blockDim.x) .. + 7 of the row.
+template <int NA, int V, int DEPTH>
+struct Ahead {
+  uint32_t base;            // shared address of this thread's first vector
+  const uint4* mine;
+  int n;                    // threads
+  __device__ __forceinline__ Ahead(uint4* smem)
+      : base((uint32_t)__cvta_generic_to_shared(smem + threadIdx.x)), mine(smem + threadIdx.x), n((int)blockDim.x) {}
+  __device__ __forceinline__ int elem(int i) const { return 8 * ((int)threadIdx.x + i * n); }
+  // starts the copies of row t (none past the last row or for a missing array)
+  __device__ __forceinline__ void start(int slot, const uint16_t* const (&p)[NA], int t, int T, int d) const {
+    if (t < T) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 8 * (threadIdx.x + i * blockDim.x);
-        uint4 xq = make_uint4(0u, 0u, 0u, 0u), zq = xq;
-        if (e < g.d) {
-          xq = ld8(g.x, base + e);
-          zq = ld8(g.z, base + e);
+      for (int i = 0; i < V; ++i)
+        if (elem(i) < d) {
+          const size_t off = (size_t)t * d + elem(i);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            if (p[a])
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + 16u * (uint32_t)(((slot * NA + a) * V + i) * n)),
+                           "l"(p[a] + off)
+                           : "memory");
         }
-        unpack8(xq, y[i]);
-        unpack8(zq, z[i]);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+  __device__ __forceinline__ uint4 get(int slot, int a, int i) const { return mine[((slot * NA + a) * V + i) * n]; }
+};
+
+// Z: there is a branch; POST: with a norm; PRE: with the next block's norm (a).
+template <int V, int DEPTH, bool Z, bool POST, bool PRE>
+__global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __grid_constant__ NormArgs g) {
+  extern __shared__ uint4 rows[];
+  __shared__ __align__(16) float buf[2][2][kMaxWarps];
+  for (int i = threadIdx.x; i < 4 * kMaxWarps; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  pdl_wait();
+  __syncthreads();
+  const int d = g.d, T = g.T;
+  const float inv_d = 1.f / (float)d, eps = g.eps, rs = g.rs;
+  const Ahead<2, V, DEPTH> ahead(rows);
+  const uint16_t* const src[2] = {g.x, Z ? g.z : nullptr};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] += z[i][j] * z[i][j];
-      }
+  for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
+  int slot = 0, par = 0;
+  for (int t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
+    const size_t base = (size_t)t * d;
+    float y[V][8];
+    ahead.wait();
+    if (Z) {
       float c = g.bs;
       if (g.gate) c *= 1.f / (1.f + expf(-g.gate[t]));
-      if (g.post_w) {
-        cta_sum(ss, buf[0]);
-        c *= 1.f / sqrtf(ss[0] * inv_d + g.eps);
+      if (POST) {
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (ahead.elem(i) < d) {
+            float z[8];
+            unpack8(ahead.get(slot, 1, i), z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss[0] += z[j] * z[j];
+          }
+        cta_sum(ss, buf[par][0]);
+        c *= 1.f / sqrtf(ss[0] * inv_d + eps);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 8 * (threadIdx.x + i * blockDim.x);
-        if (e < g.d) {
-          float w[8];
-          if (g.post_w) unpack8(ld8(g.post_w, e), w);
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) {
+          float z[8];
+          unpack8(ahead.get(slot, 0, i), y[i]);
+          unpack8(ahead.get(slot, 1, i), z);
+          if (POST) {
+            float w[8];
+            unpack8(ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[i][j] = g.rs * y[i][j] + c * (g.post_w ? z[i][j] * w[j] : z[i][j]);
-          *reinterpret_cast<uint4*>(g.y + base + e) = pack8(y[i]);
+            for (int j = 0; j < 8; ++j) z[j] *= w[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[i][j] = rs * y[i][j] + c * z[j];
+          *reinterpret_cast<uint4*>(g.y + base + ahead.elem(i)) = pack8(y[i]);
         }
-      }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 8 * (threadIdx.x + i * blockDim.x);
-        unpack8(e < g.d ? ld8(g.x, base + e) : make_uint4(0u, 0u, 0u, 0u), y[i]);
-      }
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) unpack8(ahead.get(slot, 0, i), y[i]);
     }
-    if (g.pre_w) {
+    ahead.start(slot, src, t + DEPTH * (int)gridDim.x, T, d);
+    if (++slot == DEPTH) slot = 0;
+    if (PRE) {
       float ss[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] += y[i][j] * y[i][j];
-      cta_sum(ss, buf[1]);
-      const float r = 1.f / sqrtf(ss[0] * inv_d + g.eps);
+          for (int j = 0; j < 8; ++j) ss[0] += y[i][j] * y[i][j];
+      cta_sum(ss, buf[par][1]);
+      const float r = 1.f / sqrtf(ss[0] * inv_d + eps);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 8 * (threadIdx.x + i * blockDim.x);
-        if (e < g.d) {
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) {
           float w[8];
-          unpack8(ld8(g.pre_w, e), w);
+          unpack8(ld8(g.pre_w, ahead.elem(i)), w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[i][j] *= r * w[j];
-          *reinterpret_cast<uint4*>(g.a + base + e) = pack8(y[i]);
+          *reinterpret_cast<uint4*>(g.a + base + ahead.elem(i)) = pack8(y[i]);
         }
-      }
     }
-    // the buffers of this row's sums are not rewritten before every thread has read them:
-    // each sum's own barrier lies between (with one sum a row, this one)
-    if (!(g.z && g.post_w && g.pre_w)) __syncthreads();
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   pdl_trigger();
 }
 
-template <int V>
-__global__ void __launch_bounds__(kMaxWarps * 32) block_norm_bwd_kernel(const NormArgs g) {
-  __shared__ float buf[3][2 * kMaxWarps];
+// Z, POST: as above; DA: da is given (else a's gradient is zero).
+template <int V, int DEPTH, bool Z, bool POST, bool DA>
+__global__ void __launch_bounds__(kMaxWarps * 32) block_norm_bwd_kernel(const __grid_constant__ NormArgs g) {
+  extern __shared__ uint4 rows[];
+  __shared__ __align__(16) float buf[2][4][kMaxWarps];
+  for (int i = threadIdx.x; i < 8 * kMaxWarps; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
   pdl_wait();
-  const float inv_d = 1.f / (float)g.d;
+  __syncthreads();
+  const int d = g.d, T = g.T;
+  const float inv_d = 1.f / (float)d, eps = g.eps, rs = Z ? g.rs : 1.f;
+  const bool has_dy = g.dy != nullptr;
   float dpost[V][8] = {}, dpre[V][8] = {};
-  for (int t = blockIdx.x; t < g.T; t += gridDim.x) {
-    const size_t base = (size_t)t * g.d;
-    float y[V][8], z[V][8], D[V][8], da[V][8];
-    float sz[1] = {0.f};
+  const Ahead<4, V, DEPTH> ahead(rows);
+  const uint16_t* const src[4] = {DA ? g.x : nullptr, Z ? g.z : nullptr, g.dy, DA ? g.da : nullptr};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = 8 * (threadIdx.x + i * blockDim.x);
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      const bool in = e < g.d;
-      const uint4 xq = in ? ld8(g.x, base + e) : zero;
-      const uint4 zq = in && g.z ? ld8(g.z, base + e) : zero;
-      const uint4 dq = in && g.dy ? ld8(g.dy, base + e) : zero;
-      const uint4 aq = in && g.da ? ld8(g.da, base + e) : zero;
-      unpack8(xq, y[i]);
-      unpack8(zq, z[i]);
-      unpack8(dq, D[i]);
-      unpack8(aq, da[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sz[0] += z[i][j] * z[i][j];
-    }
+  for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
+  int slot = 0, par = 0;
+  for (int t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
+    const size_t base = (size_t)t * d;
+    float y[V][8], D[V][8];
     float c = g.bs, s = 1.f, rz = 1.f;
     if (g.gate) {
       s = 1.f / (1.f + expf(-g.gate[t]));
       c *= s;
     }
-    if (g.post_w) {
-      cta_sum(sz, buf[0]);
-      rz = 1.f / sqrtf(sz[0] * inv_d + g.eps);
-    }
-    float sy[2] = {0.f, 0.f};   // sum y^2, sum da pre_w y
+    ahead.wait();
+    if (POST) {
+      float sz[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = 8 * (threadIdx.x + i * blockDim.x);
-      if (e < g.d) {
-        float w[8];
-        if (g.z) {
-          if (g.post_w) unpack8(ld8(g.post_w, e), w);
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) {
+          float z[8];
+          unpack8(ahead.get(slot, 1, i), z);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[i][j] = g.rs * y[i][j] + c * rz * (g.post_w ? z[i][j] * w[j] : z[i][j]);
+          for (int j = 0; j < 8; ++j) sz[0] += z[j] * z[j];
         }
-        if (g.da) {
-          unpack8(ld8(g.pre_w, e), w);
+      cta_sum(sz, buf[par][0]);
+      rz = 1.f / sqrtf(sz[0] * inv_d + eps);
+    }
+    const float cr = c * rz;
+    float ry = 0.f, k = 0.f;
+    if (DA) {
+      float sy[2] = {0.f, 0.f};   // sum y^2, sum da pre_w y
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) {
+          float w[8], v[8];
+          unpack8(ahead.get(slot, 0, i), y[i]);
+          if (Z) {
+            unpack8(ahead.get(slot, 1, i), v);
+            if (POST) {
+              unpack8(ld8(g.post_w, ahead.elem(i)), w);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] *= w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[i][j] = rs * y[i][j] + cr * v[j];
+          }
+          unpack8(ahead.get(slot, 3, i), v);
+          unpack8(ld8(g.pre_w, ahead.elem(i)), w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
+            D[i][j] = v[j] * w[j];   // the gradient through a, before its row terms
             sy[0] += y[i][j] * y[i][j];
-            sy[1] += da[i][j] * w[j] * y[i][j];
+            sy[1] += D[i][j] * y[i][j];
           }
         }
-      }
-    }
-    float ry = 0.f, k = 0.f;
-    if (g.da) {
-      cta_sum(sy, buf[1]);
-      ry = 1.f / sqrtf(sy[0] * inv_d + g.eps);
+      cta_sum(sy, buf[par][1]);
+      ry = 1.f / sqrtf(sy[0] * inv_d + eps);
       k = ry * ry * sy[1] * inv_d;
     }
     float sw[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = 8 * (threadIdx.x + i * blockDim.x);
-      if (e < g.d) {
-        float w[8];
-        if (g.da) {
-          unpack8(ld8(g.pre_w, e), w);
+    for (int i = 0; i < V; ++i)
+      if (ahead.elem(i) < d) {
+        float v[8];
+        if (DA) {
+          unpack8(ahead.get(slot, 3, i), v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            D[i][j] += ry * (da[i][j] * w[j] - y[i][j] * k);
-            dpre[i][j] += da[i][j] * y[i][j] * ry;
+            D[i][j] = ry * (D[i][j] - y[i][j] * k);
+            dpre[i][j] += v[j] * (y[i][j] * ry);
           }
+          if (has_dy) {
+            unpack8(ahead.get(slot, 2, i), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) D[i][j] += v[j];
+          }
+        } else {
+          unpack8(ahead.get(slot, 2, i), D[i]);
         }
         if (g.dx) {
-          float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (g.z ? g.rs : 1.f) * D[i][j];
-          *reinterpret_cast<uint4*>(g.dx + base + e) = pack8(o);
+          for (int j = 0; j < 8; ++j) v[j] = rs * D[i][j];
+          *reinterpret_cast<uint4*>(g.dx + base + ahead.elem(i)) = pack8(v);
         }
-        if (g.z) {
-          if (g.post_w) unpack8(ld8(g.post_w, e), w);
+        if (Z) {
+          unpack8(ahead.get(slot, 1, i), v);
+          if (POST) {
+            float w[8];
+            unpack8(ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (g.post_w) {
-              dpost[i][j] += c * D[i][j] * z[i][j] * rz;
+            for (int j = 0; j < 8; ++j) {
+              dpost[i][j] += cr * (D[i][j] * v[j]);
               D[i][j] *= w[j];
             }
-            sw[0] += D[i][j] * z[i][j];
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sw[0] += D[i][j] * v[j];
         }
       }
-    }
-    if (g.z && (g.dz || g.dgate)) {
+    if (Z && (g.dz || g.dgate)) {
       float kz = 0.f;
-      if (g.post_w || g.dgate) {
-        cta_sum(sw, buf[2]);
-        if (g.post_w) kz = rz * rz * sw[0] * inv_d;
+      if (POST || g.dgate) {
+        cta_sum(sw, buf[par][3]);
+        if (POST) kz = rz * rz * sw[0] * inv_d;
         if (g.dgate && threadIdx.x == 0) g.dgate[t] = g.bs * s * (1.f - s) * rz * sw[0];
       }
       if (g.dz) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = 8 * (threadIdx.x + i * blockDim.x);
-          if (e < g.d) {
+        for (int i = 0; i < V; ++i)
+          if (ahead.elem(i) < d) {
+            if (POST) {
+              float v[8];
+              unpack8(ahead.get(slot, 1, i), v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) D[i][j] = c * rz * (D[i][j] - z[i][j] * kz);
-            *reinterpret_cast<uint4*>(g.dz + base + e) = pack8(D[i]);
+              for (int j = 0; j < 8; ++j) D[i][j] = D[i][j] - v[j] * kz;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) D[i][j] *= cr;
+            *reinterpret_cast<uint4*>(g.dz + base + ahead.elem(i)) = pack8(D[i]);
           }
-        }
       }
     }
-    __syncthreads();   // the sums' buffers are free again
+    ahead.start(slot, src, t + DEPTH * (int)gridDim.x, T, d);
+    if (++slot == DEPTH) slot = 0;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (g.part) {
-    float* p = g.part + (size_t)blockIdx.x * 2 * g.d;
+    float* p = g.part + (size_t)blockIdx.x * 2 * d;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = 8 * (threadIdx.x + i * blockDim.x);
-      if (e < g.d) {
+    for (int i = 0; i < V; ++i)
+      if (ahead.elem(i) < d) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float(&v)[8] = h ? dpre[i] : dpost[i];
-          float4* o = reinterpret_cast<float4*>(p + (size_t)h * g.d + e);
+          float4* o = reinterpret_cast<float4*>(p + (size_t)h * d + ahead.elem(i));
           o[0] = make_float4(v[0], v[1], v[2], v[3]);
           o[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
-    }
   }
   pdl_trigger();
 }
@@ -303,13 +370,28 @@ __global__ void __launch_bounds__(256) block_norm_reduce_kernel(const float* par
   }
 }
 
-// Threads and vectors per thread of a row of d: up to 512 threads, V 1, 2 or 4.
-int pick_v(int d, int* threads) {
-  const int vecs = d / 8;
-  int v = 1;
-  while (v < 4 && vecs > v * 256) v <<= 1;
-  *threads = ((vecs + v - 1) / v + 31) / 32 * 32;
-  return v;
+// The launch shape of a row of d: threads, vectors per thread (1 up to 2048 elements, 2 up
+// to 8192, else 4), rows ahead, CTAs.  Rows ahead as deep as leaves an SM several CTAs.
+struct Shape {
+  int v, threads, smem, ctas;
+};
+
+template <int NA, int V, int DEPTH, typename K>
+Shape shape_of(K kernel, int d, int T) {
+  Shape h;
+  h.v = V;
+  h.threads = ((d / 8 + V - 1) / V + 31) / 32 * 32;
+  h.smem = DEPTH * NA * V * h.threads * 16;
+  if (h.smem > 46 * 1024)   // with the static shared memory, past the default 48 KiB
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h.smem);
+  const int sms = sm_count();
+  int per_sm = 1;
+  if (T > sms &&
+      (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, h.threads, h.smem) != cudaSuccess || per_sm < 1))
+    per_sm = 1;
+  const int most = sms * per_sm;
+  h.ctas = T < most ? T : most;
+  return h;
 }
 
 NormArgs make_args(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T) {
@@ -327,6 +409,40 @@ NormArgs make_args(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T) 
   return g;
 }
 
+template <int V, int DEPTH, bool Z, bool POST, bool PRE>
+cudaError_t run_fwd(const NormArgs& g, cudaStream_t s) {
+  auto* kernel = block_norm_fwd_kernel<V, DEPTH, Z, POST, PRE>;
+  const Shape h = shape_of<2, V, DEPTH>(kernel, g.d, g.T);
+  return launch_pdl(kernel, dim3(h.ctas), dim3(h.threads), h.smem, s, g);
+}
+
+template <int V, int DEPTH>
+cudaError_t pick_fwd(const NormArgs& g, cudaStream_t s) {
+  if (!g.z) return run_fwd<V, DEPTH, false, false, true>(g, s);
+  if (g.post_w) return g.pre_w ? run_fwd<V, DEPTH, true, true, true>(g, s) : run_fwd<V, DEPTH, true, true, false>(g, s);
+  return g.pre_w ? run_fwd<V, DEPTH, true, false, true>(g, s) : run_fwd<V, DEPTH, true, false, false>(g, s);
+}
+
+// The backward kernel's partial sums are one row per CTA; their number must not depend on
+// more than d and T, since the caller sized the workspace by it.
+constexpr int kBwdPerSm = 4;
+
+template <int V, int DEPTH, bool Z, bool POST, bool DA>
+cudaError_t run_bwd(const NormArgs& g, int* ctas, cudaStream_t s) {
+  auto* kernel = block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>;
+  const Shape h = shape_of<4, V, DEPTH>(kernel, g.d, g.T);
+  *ctas = h.ctas < *ctas ? h.ctas : *ctas;
+  return launch_pdl(kernel, dim3(*ctas), dim3(h.threads), h.smem, s, g);
+}
+
+template <int V, int DEPTH>
+cudaError_t pick_bwd(const NormArgs& g, int* ctas, cudaStream_t s) {
+  if (!g.z) return run_bwd<V, DEPTH, false, false, true>(g, ctas, s);
+  if (g.post_w)
+    return g.da ? run_bwd<V, DEPTH, true, true, true>(g, ctas, s) : run_bwd<V, DEPTH, true, true, false>(g, ctas, s);
+  return g.da ? run_bwd<V, DEPTH, true, false, true>(g, ctas, s) : run_bwd<V, DEPTH, true, false, false>(g, ctas, s);
+}
+
 }  // namespace
 
 cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y,
@@ -334,19 +450,14 @@ cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   NormArgs g = make_args(c, in, T);
   g.y = y;
   g.a = a;
-  int threads;
-  const int v = pick_v(g.d, &threads);
-  const int most = sm_count() * (2048 / threads);
-  const dim3 grid(T < most ? T : most), block(threads);
-  if (v == 1) return launch_pdl(block_norm_fwd_kernel<1>, grid, block, 0, s, g);
-  if (v == 2) return launch_pdl(block_norm_fwd_kernel<2>, grid, block, 0, s, g);
-  return launch_pdl(block_norm_fwd_kernel<4>, grid, block, 0, s, g);
+  if (g.d <= 2048) return pick_fwd<1, 3>(g, s);
+  if (g.d <= 8192) return pick_fwd<2, 2>(g, s);
+  return pick_fwd<4, 1>(g, s);
 }
 
 int block_norm_parts(int d, int T) {
-  int threads;
-  pick_v(d, &threads);
-  const int most = sm_count() * (1024 / threads > 1 ? 1024 / threads : 1);
+  (void)d;
+  const int most = kBwdPerSm * sm_count();
   return T < most ? T : most;
 }
 
@@ -359,13 +470,10 @@ cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   g.dz = static_cast<uint16_t*>(o.dbranch);
   g.dgate = o.dgate;
   g.part = o.dpost_w || o.dpre_w ? parts : nullptr;
-  int threads;
-  const int v = pick_v(g.d, &threads);
-  const int n = block_norm_parts(g.d, T);
-  const dim3 grid(n), block(threads);
-  cudaError_t e = v == 1   ? launch_pdl(block_norm_bwd_kernel<1>, grid, block, 0, s, g)
-                  : v == 2 ? launch_pdl(block_norm_bwd_kernel<2>, grid, block, 0, s, g)
-                           : launch_pdl(block_norm_bwd_kernel<4>, grid, block, 0, s, g);
+  int n = block_norm_parts(g.d, T);
+  const cudaError_t e = g.d <= 2048   ? pick_bwd<1, 3>(g, &n, s)
+                        : g.d <= 8192 ? pick_bwd<2, 2>(g, &n, s)
+                                      : pick_bwd<4, 1>(g, &n, s);
   if (e != cudaSuccess || !g.part) return e;
   return launch_pdl(block_norm_reduce_kernel, dim3((g.d + 31) / 32, 2), dim3(256), 0, s, static_cast<const float*>(parts),
                     n, g.d, o.dpost_w, o.dpre_w);

@@ -12,28 +12,36 @@ struct GluAct {
   float limit, alpha;
 };
 
-__device__ __forceinline__ float sigmoid_f32(float v) { return 1.f / (1.f + __expf(-v)); }
+// exp and the quotient by their fast forms (a few 2^-23 off, far below the bf16 rounding
+// that follows); an infinite exp gives 0.
+__device__ __forceinline__ float sigmoid_f32(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
+template <bool CLAMPED>
 __device__ __forceinline__ float glu_value(const GluAct& a, float g, float u) {
-  if (a.act == MOE_ACT_SWIGLU) return g * sigmoid_f32(g) * u;
+  if (!CLAMPED) return g * sigmoid_f32(g) * u;
   g = g > a.limit ? a.limit : g;
   u = u > a.limit ? a.limit : (u < -a.limit ? -a.limit : u);
   return (u + 1.f) * g * sigmoid_f32(a.alpha * g);
 }
 
+__device__ __forceinline__ float glu_value(const GluAct& a, float g, float u) {
+  return a.act == MOE_ACT_SWIGLU ? glu_value<false>(a, g, u) : glu_value<true>(a, g, u);
+}
+
 // dg = dh dh/dg, du = dh dh/du; a clamp passes the gradient up to its border, inclusive.
+template <bool CLAMPED>
 __device__ __forceinline__ void glu_grad(const GluAct& a, float g, float u, float dh, float& dg, float& du) {
-  if (a.act == MOE_ACT_SWIGLU) {
-    const float s = sigmoid_f32(g);
-    du = dh * g * s;
-    dg = dh * u * (s + g * s * (1.f - s));
+  if (!CLAMPED) {
+    const float s = sigmoid_f32(g), gs = g * s;
+    du = dh * gs;
+    dg = dh * u * (s + gs * (1.f - s));
     return;
   }
   const float gc = g > a.limit ? a.limit : g;
   const float uc = u > a.limit ? a.limit : (u < -a.limit ? -a.limit : u);
-  const float s = sigmoid_f32(a.alpha * gc);
-  du = (u > a.limit || u < -a.limit) ? 0.f : dh * gc * s;
-  dg = g > a.limit ? 0.f : dh * (uc + 1.f) * (s + a.alpha * gc * s * (1.f - s));
+  const float s = sigmoid_f32(a.alpha * gc), gs = gc * s;
+  du = (u > a.limit || u < -a.limit) ? 0.f : dh * gs;
+  dg = g > a.limit ? 0.f : dh * (uc + 1.f) * (s + a.alpha * gs * (1.f - s));
 }
 
 }  // namespace moe

@@ -113,7 +113,7 @@ def glu_inputs(T, d, ff, act, seed=1):
     return x, w, rnd(gen, T, d)
 
 
-SHAPES = [(1, 8, 8), (1, 2048, 512), (2, 40, 24), (7, 64, 64), (8, 264, 136), (16, 2880, 328), (17, 64, 2880),
+SHAPES = [(1, 8, 8), (8, 96, 12288), (10, 13544, 72), (16, 72, 8000), (3, 6152, 4864), (1, 2048, 512), (2, 40, 24), (7, 64, 64), (8, 264, 136), (16, 2880, 328), (17, 64, 2880),
           (33, 136, 520), (64, 512, 72), (128, 256, 256), (129, 264, 1000), (300, 520, 392), (777, 1024, 512),
           (1500, 72, 2056)]
 
@@ -236,6 +236,41 @@ def test_glu_clamped_nan_passes():
     for sv in (None, moe.glu_saved(moe.glu_cfg(d, ff, act=1), 4)):
         y = moe.moe_glu_forward(moe.glu_cfg(d, ff, act=1), x, w, saved=sv)
         assert torch.isnan(y[2]).all() and torch.isfinite(y[[0, 1, 3]]).all()
+
+
+@pytest.mark.parametrize("T,d", [(1, 2880), (130, 2880), (64, 8192)])
+def test_glu_clamp_border_takes_the_exact_side(T, d):
+    """Gate and up values within 1e-7 .. 1e-4 of the clamp's border, nearer than a truncating
+    sum of d products resolves: the gradient passes exactly where the 64-bit value is inside."""
+    gen = gen_for(T, d, 11)
+    ff = 128
+    x = rnd(gen, T, d)
+    t = T // 2                      # the token whose values are placed
+    x[t, :4] = torch.tensor([2.0 ** -4, 2.0 ** -11, 2.0 ** -18, 2.0 ** -25])
+    w = {n: rnd(gen, ff, d, scale=0.3 * d ** -0.5) for n in ("gate", "up")}
+    off = torch.logspace(-7, -4, ff // 2, dtype=torch.float64, device="cuda")
+    target = LIMIT + torch.cat((off, -off))
+    for n in w:
+        m = w[n]
+        # a first part of the sum close to the target, then ever finer corrections
+        m[:, 4:] = (m[:, 4:].double() + (target - x[t, 4:].double() @ m[:, 4:].double().T)[:, None] * x[t, 4:].double()
+                    / x[t, 4:].double().square().sum()).bfloat16()
+        m[:, :4] = 0
+        for j in range(4):
+            m[:, j] = ((target - m.double() @ x[t].double()) / x[t, j].double()).bfloat16()
+    value = {n: w[n].double() @ x[t].double() for n in w}
+    assert all(((v - LIMIT).abs() < 2e-4).all() for v in value.values())
+    inside = {n: value[n].float().double() <= LIMIT for n in w}
+    assert all(i.any() and not i.all() for i in inside.values())
+    cfg = moe.glu_cfg(d, ff, act=moe.ACT_CLAMPED_GLU)
+    weights = moe.GluWeights(w["gate"], w["up"], rnd(gen, d, ff, scale=ff ** -0.5))
+    saved = moe.glu_saved(cfg, T)
+    moe.moe_glu_forward(cfg, x, weights, saved=saved)
+    dy = torch.zeros_like(x)        # only the placed token has a gradient
+    dy[t] = rnd(gen, d)
+    _, g = moe.moe_glu_backward(cfg, x, weights, saved, dy)
+    assert torch.equal(g.gate.abs().amax(1) > 0, inside["gate"])
+    assert torch.equal(g.up.abs().amax(1) > 0, inside["up"])
 
 
 def test_glu_repeats_bit_for_bit_and_in_a_graph():
@@ -481,7 +516,8 @@ def w4_64(x, w, group):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("T,k,n,group", [
     (1, 128, 1, 128), (1, 32, 16, 32), (3, 96, 17, 32), (8, 192, 40, 64), (5, 2048, 1000, 128), (9, 4096, 77, 64),
-    (16, 8192, 130, 32), (16, 128 * 9, 2500, 128), (17, 320, 33, 32), (40, 576, 50, 64)])
+    (16, 8192, 130, 32), (16, 128 * 9, 2500, 128), (17, 320, 33, 32), (40, 576, 50, 64), (7, 13824, 70, 64),
+    (12, 14336, 40, 128), (16, 4096, 6000, 64)])
 def test_w4_linear(T, k, n, group, zeros):
     x, w = w4_inputs(T, k, n, group, zeros)
     want, e = w4_64(x, w, group)
