@@ -106,6 +106,14 @@ def _one_device(x: torch.Tensor, *others) -> None:
             raise ValueError(f"tensors on {x.device} and {t.device}")
 
 
+def _current_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The same handle without the Stream object around it, 0.1 us instead of 2, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class BoundCall:
     """A library call with its arguments marshalled once.  Each call enqueues the same work
     on the same buffers (their contents are read when it runs) on the stream given to
@@ -116,14 +124,15 @@ class BoundCall:
 
     def __init__(self, where, args, out, keep, device, stream):
         self._fn, self._where = getattr(_lib, where), where
-        self._args, self._out, self._keep, self._device = args, out, keep, device
+        self._args, self._out, self._keep = args, out, keep
+        self._device = device.index if _raw_stream is not None else device
         self._stream = None if stream is None else (
             stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
     def __call__(self):
         stream = self._stream
         if stream is None:
-            stream = torch.cuda.current_stream(self._device).cuda_stream
+            stream = (_raw_stream or _current_stream)(self._device)
         status = self._fn(*self._args, stream)
         if status != MOE_OK:
             raise MoeError(status, self._where)

@@ -7,6 +7,19 @@
 
 namespace moe {
 
+// Lets KERNEL use up to `bytes` of dynamic shared memory; asked of the driver once per
+// device (`bytes` is the same at every call).
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
 // The gated FFN's shapes and weights.
 struct GluParams {
   const uint16_t *gate, *up, *down;   // bf16 [ff, d], [ff, d], [d, ff]
@@ -31,13 +44,12 @@ cudaError_t launch_glu_gate_up(const GluParams& p, const uint16_t* x, int T, uin
 // y = h Wd^T
 cudaError_t launch_glu_down(const GluParams& p, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
                             cudaStream_t s);
-// dg, du [T, ff] from dy, the saved g and u
+// dg, du [T, ff] from dy and the saved g and u; and, where dwd is non-null, dWd
 cudaError_t launch_glu_dact(const GluParams& p, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint32_t* status, cudaStream_t s);
-// dx, dWg, dWu, dWd, each where its pointer is non-null, in one launch
-cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
-                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
-                             uint16_t* dwd, uint32_t* status, cudaStream_t s);
+                            uint16_t* du, uint16_t* dwd, uint32_t* status, cudaStream_t s);
+// dx, dWg, dWu, each where its pointer is non-null, in one launch
+cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, int T, const uint16_t* dg, const uint16_t* du,
+                             uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint32_t* status, cudaStream_t s);
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold);
 
 // Few tokens (skinny.cu): the weights stream through warp MMAs, every 16 tokens.
@@ -53,7 +65,7 @@ cudaError_t launch_skinny_w4(const moe_w4_cfg_t& c, const moe_w4_weights_t& w, c
 // Norms (block_norm.cu).
 cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y,
                                   uint16_t* a, cudaStream_t s);
-int block_norm_parts(int d, int T);   // rows of the weight gradients' partial sums
+int block_norm_parts(int T);   // rows of the weight gradients' partial sums
 cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, const uint16_t* dy,
                                   const uint16_t* da, const moe_norm_grads_t& g, float* parts, cudaStream_t s);
 

@@ -173,10 +173,9 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
   uint16_t* du = reinterpret_cast<uint16_t*>(base + L.du);
   const GluSaved sv = saved_at(const_cast<void*>(saved), saved_layout(*cfg, T));
   const uint16_t* dyi = static_cast<const uint16_t*>(dy);
-  BLOCK_CUDA(launch_glu_dact(p, dyi, T, sv, dg, du, status, s));
-  BLOCK_CUDA(launch_glu_grads(p, static_cast<const uint16_t*>(x), dyi, T, sv, dg, du, static_cast<uint16_t*>(dx),
-                              static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up),
-                              static_cast<uint16_t*>(dw.down), status, s));
+  BLOCK_CUDA(launch_glu_dact(p, dyi, T, sv, dg, du, static_cast<uint16_t*>(dw.down), status, s));
+  BLOCK_CUDA(launch_glu_grads(p, static_cast<const uint16_t*>(x), T, dg, du, static_cast<uint16_t*>(dx),
+                              static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up), status, s));
   return MOE_OK;
 }
 
@@ -196,7 +195,7 @@ int moe_block_norm_forward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* i
 
 size_t moe_block_norm_workspace_bytes(const moe_norm_cfg_t* cfg, int32_t T) {
   if (check_norm(cfg) != MOE_OK || T < 0) return 0;
-  return 256 + (size_t)block_norm_parts(cfg->d_model, T) * 2 * cfg->d_model * 4;
+  return 256 + (size_t)block_norm_parts(T) * 2 * cfg->d_model * 4;
 }
 
 int moe_block_norm_backward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* in, int32_t T, const void* dy,

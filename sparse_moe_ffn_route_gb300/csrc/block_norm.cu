@@ -3,8 +3,8 @@
 // gradients of the same.
 //
 // Bound by memory: forward reads x, z and writes y, a (8 bytes per element), backward
-// reads x, z, dy, da and writes dx, dz (12 bytes).  One CTA works on one row at a time, 8
-// elements (one 16-byte vector) per thread and step, so every tensor passes memory once.
+// reads x, z, dy, da and writes dx, dz (12 bytes).  A group of threads (forward: a CTA)
+// works on one row at a time, held in registers, so every tensor passes memory once.
 // Each thread copies its own vectors of the next rows into shared memory ahead of time
 // (cp.async: the rows' latency stays off the chain of sums, and needs no registers and no
 // barrier, since a thread reads only what it copied).  The row sums cross the CTA through
@@ -18,8 +18,12 @@
 //   dx = residual_scale D;   W = D post_w;   S = sum W z
 //   dgate = branch_scale s (1 - s) rz S;   dz = c rz (W - z rz^2 S / d)
 //   dpost_w += c D z rz;   dpre_w += da y ry
-// A CTA keeps its columns' weight gradients in registers over all its rows and writes one
-// row of partial sums; a second kernel adds the partial rows in order.
+// One CTA per SM holds several groups of threads, each on rows of its own (named barriers),
+// with 16 elements per thread and row: the fixed work of a row (exchanges, roots) is paid
+// by fewer warps than at 8 elements (4400 instructions per row of 2048 then, of which half
+// were that).  The next row's sum z^2 shares the exchange of this row's S.  A thread keeps
+// its columns' weight gradients in registers over all its rows; the groups add theirs up
+// and the CTA writes one row of partial sums, which a second kernel adds in order.
 #include "block.h"
 #include "common.cuh"
 
@@ -53,17 +57,61 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(u[i]);
-    v[2 * i + 1] = bf16_hi(u[i]);
-  }
+// rsqrtf is 2 units in the last place off at most, sigmoid a few: far below what the sums
+// that go in have lost.
+__device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(sum * inv_d + eps); }
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+// Two fp32 values that one instruction works on (fma.rn.f32x2 and its kin): the kernels
+// are near the issue rate, and this halves their arithmetic.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float both(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  return lo + hi;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ void unpack8(const uint4& q, F2 (&v)[4]) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2(bf16_lo(u[i]), bf16_hi(u[i]));
+}
+
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    split(v[i], lo, hi);
+    u[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 struct NormArgs {
@@ -81,16 +129,16 @@ struct NormArgs {
 
 __device__ __forceinline__ uint4 ld8(const uint16_t* p, int at) { return *reinterpret_cast<const uint4*>(p + at); }
 
-// This thread's vectors of a row, and the copies of the rows ahead: DEPTH slots of NA arrays.
-// Vector i holds elements 8 (threadIdx.x + i blockDim.x) .. + 7 of the row.
+// A thread's vectors of a row (vector i of thread tid of n: elements 8 (tid + i n) .. + 7) and
+// the copies of the rows ahead: DEPTH slots of NA arrays.
 template <int NA, int V, int DEPTH>
 struct Ahead {
   uint32_t base;            // shared address of this thread's first vector
   const uint4* mine;
-  int n;                    // threads
-  __device__ __forceinline__ Ahead(uint4* smem)
-      : base((uint32_t)__cvta_generic_to_shared(smem + threadIdx.x)), mine(smem + threadIdx.x), n((int)blockDim.x) {}
-  __device__ __forceinline__ int elem(int i) const { return 8 * ((int)threadIdx.x + i * n); }
+  int tid, n;
+  __device__ __forceinline__ Ahead(uint4* smem, int tid_, int n_)
+      : base((uint32_t)__cvta_generic_to_shared(smem + tid_)), mine(smem + tid_), tid(tid_), n(n_) {}
+  __device__ __forceinline__ int elem(int i) const { return 8 * (tid + i * n); }
   // starts the copies of row t (none past the last row or for a missing array)
   __device__ __forceinline__ void start(int slot, const uint16_t* const (&p)[NA], int t, int T, int d) const {
     if (t < T) {
@@ -108,7 +156,9 @@ struct Ahead {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+  // all but the last LEFT rows asked for are there
+  template <int LEFT>
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
   __device__ __forceinline__ uint4 get(int slot, int a, int i) const { return mine[((slot * NA + a) * V + i) * n]; }
 };
 
@@ -121,46 +171,49 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
   pdl_wait();
   __syncthreads();
   const int d = g.d, T = g.T;
-  const float inv_d = 1.f / (float)d, eps = g.eps, rs = g.rs;
-  const Ahead<2, V, DEPTH> ahead(rows);
+  const float inv_d = 1.f / (float)d, eps = g.eps;
+  const F2 rs = f2(g.rs);
+  const Ahead<2, V, DEPTH> ahead(rows, threadIdx.x, blockDim.x);
   const uint16_t* const src[2] = {g.x, Z ? g.z : nullptr};
 #pragma unroll
   for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
   int slot = 0, par = 0;
   for (int t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
     const size_t base = (size_t)t * d;
-    float y[V][8];
-    ahead.wait();
+    F2 y[V][4];
+    ahead.template wait<DEPTH - 1>();
     if (Z) {
       float c = g.bs;
-      if (g.gate) c *= 1.f / (1.f + expf(-g.gate[t]));
+      if (g.gate) c *= sigmoid(g.gate[t]);
       if (POST) {
-        float ss[1] = {0.f};
+        F2 sum = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (ahead.elem(i) < d) {
-            float z[8];
+            F2 z[4];
             unpack8(ahead.get(slot, 1, i), z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss[0] += z[j] * z[j];
+            for (int j = 0; j < 4; ++j) sum = fma2(z[j], z[j], sum);
           }
+        float ss[1] = {both(sum)};
         cta_sum(ss, buf[par][0]);
-        c *= 1.f / sqrtf(ss[0] * inv_d + eps);
+        c *= inv_rms(ss[0], inv_d, eps);
       }
+      const F2 c2 = f2(c);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d) {
-          float z[8];
+          F2 z[4];
           unpack8(ahead.get(slot, 0, i), y[i]);
           unpack8(ahead.get(slot, 1, i), z);
           if (POST) {
-            float w[8];
+            F2 w[4];
             unpack8(ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] *= w[j];
+            for (int j = 0; j < 4; ++j) z[j] = mul2(z[j], w[j]);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[i][j] = rs * y[i][j] + c * z[j];
+          for (int j = 0; j < 4; ++j) y[i][j] = fma2(c2, z[j], mul2(rs, y[i][j]));
           *reinterpret_cast<uint4*>(g.y + base + ahead.elem(i)) = pack8(y[i]);
         }
     } else {
@@ -171,21 +224,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
     ahead.start(slot, src, t + DEPTH * (int)gridDim.x, T, d);
     if (++slot == DEPTH) slot = 0;
     if (PRE) {
-      float ss[1] = {0.f};
+      F2 sum = f2(0.f);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss[0] += y[i][j] * y[i][j];
+          for (int j = 0; j < 4; ++j) sum = fma2(y[i][j], y[i][j], sum);
+      float ss[1] = {both(sum)};
       cta_sum(ss, buf[par][1]);
-      const float r = 1.f / sqrtf(ss[0] * inv_d + eps);
+      const F2 r = f2(inv_rms(ss[0], inv_d, eps));
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d) {
-          float w[8];
+          F2 w[4];
           unpack8(ld8(g.pre_w, ahead.elem(i)), w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[i][j] *= r * w[j];
+          for (int j = 0; j < 4; ++j) y[i][j] = mul2(y[i][j], mul2(r, w[j]));
           *reinterpret_cast<uint4*>(g.a + base + ahead.elem(i)) = pack8(y[i]);
         }
     }
@@ -194,157 +248,220 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
   pdl_trigger();
 }
 
-// Z, POST: as above; DA: da is given (else a's gradient is zero).
+// Sum of N values over a group of n threads (whole warps) in every thread, in a fixed order;
+// `buf` and its turns as in cta_sum.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int tid, int n, int barrier) {
+  const int warp = tid >> 5, lane = tid & 31, nw = n >> 5;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (nw == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[i * kMaxWarps + warp] = v[i];
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(n) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = 0.f;
+    for (int w = 0; w < nw; w += 4) {   // slots past the last warp hold zeros
+      const float4 q = *reinterpret_cast<const float4*>(buf + i * kMaxWarps + w);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+    v[i] = s;
+  }
+}
+
+// Z, POST: as above; DA: da is given (else a's gradient is zero).  gt: threads of a group.
 template <int V, int DEPTH, bool Z, bool POST, bool DA>
-__global__ void __launch_bounds__(kMaxWarps * 32) block_norm_bwd_kernel(const __grid_constant__ NormArgs g) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
   extern __shared__ uint4 rows[];
-  __shared__ __align__(16) float buf[2][4][kMaxWarps];
-  for (int i = threadIdx.x; i < 8 * kMaxWarps; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  __shared__ __align__(16) float sums[kMaxWarps][2][2][2 * kMaxWarps];   // group, row parity, exchange
+  const int group = threadIdx.x / gt, groups = blockDim.x / gt, tid = threadIdx.x - group * gt;
+  for (int i = threadIdx.x; i < groups * 8 * kMaxWarps; i += blockDim.x) (&sums[0][0][0][0])[i] = 0.f;
   pdl_wait();
   __syncthreads();
-  const int d = g.d, T = g.T;
-  const float inv_d = 1.f / (float)d, eps = g.eps, rs = Z ? g.rs : 1.f;
+  const int d = g.d, T = g.T, stride = gridDim.x * groups;
+  const float inv_d = 1.f / (float)d, eps = g.eps;
+  const F2 rs = f2(Z ? g.rs : 1.f);
   const bool has_dy = g.dy != nullptr;
-  float dpost[V][8] = {}, dpre[V][8] = {};
-  const Ahead<4, V, DEPTH> ahead(rows);
-  const uint16_t* const src[4] = {DA ? g.x : nullptr, Z ? g.z : nullptr, g.dy, DA ? g.da : nullptr};
+  F2 dpost[V][4], dpre[V][4];
 #pragma unroll
-  for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
+  for (int i = 0; i < 4 * V; ++i) dpost[i >> 2][i & 3] = dpre[i >> 2][i & 3] = f2(0.f);
+  const Ahead<4, V, DEPTH> ahead(rows + (size_t)group * DEPTH * 4 * V * gt, tid, gt);
+  const uint16_t* const src[4] = {DA ? g.x : nullptr, Z ? g.z : nullptr, g.dy, DA ? g.da : nullptr};
+  int t = blockIdx.x + gridDim.x * group;
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, t + s * stride, T, d);
+  F2 z[V][4];
+  // z of the row in `slot` and its sum of squares
+  auto take_z = [&](int slot, float& out) {
+    F2 sum = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ahead.elem(i) < d) {
+        unpack8(ahead.get(slot, 1, i), z[i]);
+        if (POST) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum = fma2(z[i][j], z[i][j], sum);
+        }
+      }
+    out = both(sum);
+  };
   int slot = 0, par = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
+  float sz = 0.f;   // sum z^2 of the row
+  if (t < T && Z) {
+    float first[1] = {0.f};
+    ahead.template wait<DEPTH - 1>();
+    take_z(0, first[0]);
+    if (POST) group_sum(first, sums[group][1][1], tid, gt, 1 + group);
+    sz = first[0];
+  }
+  for (; t < T; t += stride, par ^= 1) {
     const size_t base = (size_t)t * d;
-    float y[V][8], D[V][8];
-    float c = g.bs, s = 1.f, rz = 1.f;
+    F2 y[V][4], D[V][4];
+    float c = g.bs, s = 1.f;
     if (g.gate) {
-      s = 1.f / (1.f + expf(-g.gate[t]));
+      s = sigmoid(g.gate[t]);
       c *= s;
     }
-    ahead.wait();
-    if (POST) {
-      float sz[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (ahead.elem(i) < d) {
-          float z[8];
-          unpack8(ahead.get(slot, 1, i), z);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sz[0] += z[j] * z[j];
-        }
-      cta_sum(sz, buf[par][0]);
-      rz = 1.f / sqrtf(sz[0] * inv_d + eps);
-    }
-    const float cr = c * rz;
-    float ry = 0.f, k = 0.f;
+    const float rz = POST ? inv_rms(sz, inv_d, eps) : 1.f;
+    const F2 cr = f2(c * rz);
+    if (!Z) ahead.template wait<DEPTH - 1>();
+    F2 ry = f2(0.f), k = ry;   // 1 / rms(y), and -ry times the mean term of D
     if (DA) {
-      float sy[2] = {0.f, 0.f};   // sum y^2, sum da pre_w y
+      F2 yy = f2(0.f), qy = yy;   // sum y^2, sum da pre_w y
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d) {
-          float w[8], v[8];
+          F2 w[4], v[4];
           unpack8(ahead.get(slot, 0, i), y[i]);
           if (Z) {
-            unpack8(ahead.get(slot, 1, i), v);
-            if (POST) {
-              unpack8(ld8(g.post_w, ahead.elem(i)), w);
+            if (POST) unpack8(ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] *= w[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[i][j] = rs * y[i][j] + cr * v[j];
+            for (int j = 0; j < 4; ++j) y[i][j] = fma2(cr, POST ? mul2(z[i][j], w[j]) : z[i][j], mul2(rs, y[i][j]));
           }
           unpack8(ahead.get(slot, 3, i), v);
           unpack8(ld8(g.pre_w, ahead.elem(i)), w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            D[i][j] = v[j] * w[j];   // the gradient through a, before its row terms
-            sy[0] += y[i][j] * y[i][j];
-            sy[1] += D[i][j] * y[i][j];
+          for (int j = 0; j < 4; ++j) {
+            D[i][j] = mul2(v[j], w[j]);   // the gradient through a, before its row terms
+            yy = fma2(y[i][j], y[i][j], yy);
+            qy = fma2(D[i][j], y[i][j], qy);
           }
         }
-      cta_sum(sy, buf[par][1]);
-      ry = 1.f / sqrtf(sy[0] * inv_d + eps);
-      k = ry * ry * sy[1] * inv_d;
+      float sy[2] = {both(yy), both(qy)};
+      group_sum(sy, sums[group][par][0], tid, gt, 1 + group);
+      const float r = inv_rms(sy[0], inv_d, eps);
+      ry = f2(r);
+      k = f2(-(r * r * sy[1] * inv_d));
     }
-    float sw[1] = {0.f};
+    F2 dot = f2(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (ahead.elem(i) < d) {
-        float v[8];
+        F2 v[4];
         if (DA) {
           unpack8(ahead.get(slot, 3, i), v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            D[i][j] = ry * (D[i][j] - y[i][j] * k);
-            dpre[i][j] += v[j] * (y[i][j] * ry);
+          for (int j = 0; j < 4; ++j) {
+            dpre[i][j] = fma2(v[j], mul2(y[i][j], ry), dpre[i][j]);
+            D[i][j] = fma2(k, y[i][j], D[i][j]);
           }
           if (has_dy) {
             unpack8(ahead.get(slot, 2, i), v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) D[i][j] += v[j];
+            for (int j = 0; j < 4; ++j) D[i][j] = fma2(ry, D[i][j], v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) D[i][j] = mul2(ry, D[i][j]);
           }
         } else {
           unpack8(ahead.get(slot, 2, i), D[i]);
         }
         if (g.dx) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = rs * D[i][j];
+          for (int j = 0; j < 4; ++j) v[j] = mul2(rs, D[i][j]);
           *reinterpret_cast<uint4*>(g.dx + base + ahead.elem(i)) = pack8(v);
         }
         if (Z) {
-          unpack8(ahead.get(slot, 1, i), v);
           if (POST) {
-            float w[8];
+            F2 w[4];
             unpack8(ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              dpost[i][j] += cr * (D[i][j] * v[j]);
-              D[i][j] *= w[j];
+            for (int j = 0; j < 4; ++j) {
+              dpost[i][j] = fma2(cr, mul2(D[i][j], z[i][j]), dpost[i][j]);
+              D[i][j] = mul2(D[i][j], w[j]);
             }
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sw[0] += D[i][j] * v[j];
+          for (int j = 0; j < 4; ++j) dot = fma2(D[i][j], z[i][j], dot);
+          if (g.dz && POST) {   // z is in y's place until S is known
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[i][j] = z[i][j];
+          }
         }
       }
-    if (Z && (g.dz || g.dgate)) {
-      float kz = 0.f;
-      if (POST || g.dgate) {
-        cta_sum(sw, buf[par][3]);
-        if (POST) kz = rz * rz * sw[0] * inv_d;
-        if (g.dgate && threadIdx.x == 0) g.dgate[t] = g.bs * s * (1.f - s) * rz * sw[0];
-      }
+    // this row's copies are read; z of the next row is there with all but the DEPTH - 1
+    // rows asked for last
+    ahead.start(slot, src, t + DEPTH * stride, T, d);
+    if (++slot == DEPTH) slot = 0;
+    if (Z) {
+      ahead.template wait<DEPTH - 1>();
+      float sw[2] = {both(dot), 0.f};     // S, sum z^2 of the next row
+      if (t + stride < T) take_z(slot, sw[1]);
+      if (POST || g.dgate) group_sum(sw, sums[group][par][1], tid, gt, 1 + group);
+      sz = sw[1];
+      const F2 kz = f2(POST ? -(rz * rz * sw[0] * inv_d) : 0.f);
+      if (g.dgate && tid == 0) g.dgate[t] = g.bs * s * (1.f - s) * rz * sw[0];
       if (g.dz) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (ahead.elem(i) < d) {
-            if (POST) {
-              float v[8];
-              unpack8(ahead.get(slot, 1, i), v);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) D[i][j] = D[i][j] - v[j] * kz;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) D[i][j] *= cr;
+            for (int j = 0; j < 4; ++j) D[i][j] = mul2(cr, POST ? fma2(kz, y[i][j], D[i][j]) : D[i][j]);
             *reinterpret_cast<uint4*>(g.dz + base + ahead.elem(i)) = pack8(D[i]);
           }
       }
     }
-    ahead.start(slot, src, t + DEPTH * (int)gridDim.x, T, d);
-    if (++slot == DEPTH) slot = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (g.part) {
-    float* p = g.part + (size_t)blockIdx.x * 2 * d;
+    // the groups' sums, added in order by the first group
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(rows);   // [group][2][d]
+    if (group) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (ahead.elem(i) < d) {
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float(&v)[8] = h ? dpre[i] : dpost[i];
-          float4* o = reinterpret_cast<float4*>(p + (size_t)h * d + ahead.elem(i));
-          o[0] = make_float4(v[0], v[1], v[2], v[3]);
-          o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
+          for (int h = 0; h < 2; ++h) {
+            F2* o = reinterpret_cast<F2*>(acc + ((size_t)group * 2 + h) * d + ahead.elem(i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = h ? dpre[i][j] : dpost[i][j];
+          }
+    }
+    __syncthreads();
+    if (!group) {
+      float* p = g.part + (size_t)blockIdx.x * 2 * d;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            F2(&v)[4] = h ? dpre[i] : dpost[i];
+            for (int q = 1; q < groups; ++q) {
+              const F2* a = reinterpret_cast<const F2*>(acc + ((size_t)q * 2 + h) * d + ahead.elem(i));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = add2(v[j], a[j]);
+            }
+            F2* o = reinterpret_cast<F2*>(p + (size_t)h * d + ahead.elem(i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = v[j];
+          }
+    }
   }
   pdl_trigger();
 }
@@ -370,30 +487,6 @@ __global__ void __launch_bounds__(256) block_norm_reduce_kernel(const float* par
   }
 }
 
-// The launch shape of a row of d: threads, vectors per thread (1 up to 2048 elements, 2 up
-// to 8192, else 4), rows ahead, CTAs.  Rows ahead as deep as leaves an SM several CTAs.
-struct Shape {
-  int v, threads, smem, ctas;
-};
-
-template <int NA, int V, int DEPTH, typename K>
-Shape shape_of(K kernel, int d, int T) {
-  Shape h;
-  h.v = V;
-  h.threads = ((d / 8 + V - 1) / V + 31) / 32 * 32;
-  h.smem = DEPTH * NA * V * h.threads * 16;
-  if (h.smem > 46 * 1024)   // with the static shared memory, past the default 48 KiB
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h.smem);
-  const int sms = sm_count();
-  int per_sm = 1;
-  if (T > sms &&
-      (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, h.threads, h.smem) != cudaSuccess || per_sm < 1))
-    per_sm = 1;
-  const int most = sms * per_sm;
-  h.ctas = T < most ? T : most;
-  return h;
-}
-
 NormArgs make_args(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T) {
   NormArgs g{};
   g.x = static_cast<const uint16_t*>(in.x);
@@ -411,9 +504,18 @@ NormArgs make_args(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T) 
 
 template <int V, int DEPTH, bool Z, bool POST, bool PRE>
 cudaError_t run_fwd(const NormArgs& g, cudaStream_t s) {
-  auto* kernel = block_norm_fwd_kernel<V, DEPTH, Z, POST, PRE>;
-  const Shape h = shape_of<2, V, DEPTH>(kernel, g.d, g.T);
-  return launch_pdl(kernel, dim3(h.ctas), dim3(h.threads), h.smem, s, g);
+  constexpr auto* kernel = block_norm_fwd_kernel<V, DEPTH, Z, POST, PRE>;
+  const int threads = ((g.d / 8 + V - 1) / V + 31) / 32 * 32, smem = DEPTH * 2 * V * threads * 16;
+  cudaError_t e = allow_smem<kernel>(DEPTH * 2 * V * kMaxWarps * 32 * 16);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  int per_sm = 1;
+  if (g.T > sms) {   // as many CTAs as the GPU holds
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int most = sms * (per_sm > 0 ? per_sm : 1);
+  return launch_pdl(kernel, dim3(g.T < most ? g.T : most), dim3(threads), smem, s, g);
 }
 
 template <int V, int DEPTH>
@@ -423,24 +525,22 @@ cudaError_t pick_fwd(const NormArgs& g, cudaStream_t s) {
   return g.pre_w ? run_fwd<V, DEPTH, true, false, true>(g, s) : run_fwd<V, DEPTH, true, false, false>(g, s);
 }
 
-// The backward kernel's partial sums are one row per CTA; their number must not depend on
-// more than d and T, since the caller sized the workspace by it.
-constexpr int kBwdPerSm = 4;
-
 template <int V, int DEPTH, bool Z, bool POST, bool DA>
-cudaError_t run_bwd(const NormArgs& g, int* ctas, cudaStream_t s) {
+cudaError_t run_bwd(const NormArgs& g, int ctas, cudaStream_t s) {
   auto* kernel = block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>;
-  const Shape h = shape_of<4, V, DEPTH>(kernel, g.d, g.T);
-  *ctas = h.ctas < *ctas ? h.ctas : *ctas;
-  return launch_pdl(kernel, dim3(*ctas), dim3(h.threads), h.smem, s, g);
+  const int gt = ((g.d / 8 + V - 1) / V + 31) / 32 * 32, threads = kMaxWarps * 32 / gt * gt;
+  const int smem = DEPTH * 4 * V * threads * 16;
+  const cudaError_t e = allow_smem<block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>>(DEPTH * 4 * V * kMaxWarps * 32 * 16);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(ctas), dim3(threads), smem, s, g, gt);
 }
 
 template <int V, int DEPTH>
-cudaError_t pick_bwd(const NormArgs& g, int* ctas, cudaStream_t s) {
-  if (!g.z) return run_bwd<V, DEPTH, false, false, true>(g, ctas, s);
+cudaError_t pick_bwd(const NormArgs& g, int n, cudaStream_t s) {
+  if (!g.z) return run_bwd<V, DEPTH, false, false, true>(g, n, s);
   if (g.post_w)
-    return g.da ? run_bwd<V, DEPTH, true, true, true>(g, ctas, s) : run_bwd<V, DEPTH, true, true, false>(g, ctas, s);
-  return g.da ? run_bwd<V, DEPTH, true, false, true>(g, ctas, s) : run_bwd<V, DEPTH, true, false, false>(g, ctas, s);
+    return g.da ? run_bwd<V, DEPTH, true, true, true>(g, n, s) : run_bwd<V, DEPTH, true, true, false>(g, n, s);
+  return g.da ? run_bwd<V, DEPTH, true, false, true>(g, n, s) : run_bwd<V, DEPTH, true, false, false>(g, n, s);
 }
 
 }  // namespace
@@ -455,9 +555,8 @@ cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   return pick_fwd<4, 1>(g, s);
 }
 
-int block_norm_parts(int d, int T) {
-  (void)d;
-  const int most = kBwdPerSm * sm_count();
+int block_norm_parts(int T) {
+  const int most = sm_count();
   return T < most ? T : most;
 }
 
@@ -470,10 +569,8 @@ cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   g.dz = static_cast<uint16_t*>(o.dbranch);
   g.dgate = o.dgate;
   g.part = o.dpost_w || o.dpre_w ? parts : nullptr;
-  int n = block_norm_parts(g.d, T);
-  const cudaError_t e = g.d <= 2048   ? pick_bwd<1, 3>(g, &n, s)
-                        : g.d <= 8192 ? pick_bwd<2, 2>(g, &n, s)
-                                      : pick_bwd<4, 1>(g, &n, s);
+  const int n = block_norm_parts(T);
+  const cudaError_t e = g.d <= 8192 ? pick_bwd<2, 3>(g, n, s) : pick_bwd<4, 1>(g, n, s);
   if (e != cudaSuccess || !g.part) return e;
   return launch_pdl(block_norm_reduce_kernel, dim3((g.d + 31) / 32, 2), dim3(256), 0, s, static_cast<const float*>(parts),
                     n, g.d, o.dpost_w, o.dpre_w);

@@ -7,9 +7,10 @@
 //   down:     y = h Wd^T
 //   dact:     dh = dy Wd, whose epilogue turns it into dg and du with the saved g and u
 //             (dh never reaches memory and is never rounded)
-//   grads:    dx = dg Wg + du Wu (one sum over two runs of k), dWg = dg^T x,
-//             dWu = du^T x, dWd = dy^T h, all in one launch so that the tiles of the
-//             small products fill the SMs that the large ones leave
+//             (dWd = dy^T h rides along in that launch)
+//   grads:    dx = dg Wg + du Wu (one sum over two runs of k), dWg = dg^T x and
+//             dWu = du^T x in one launch, so that the tiles of the small products fill the
+//             SMs that the large ones leave
 //
 // An operand's k runs along its rows ("K-major": x Wg^T) or down its columns
 // ("MN-major": both operands of dg^T x).  Both are read as they lie: a K-major tile is
@@ -32,7 +33,9 @@
 // at every chunk.  Every wait is bounded (see tc::mbar_wait).
 #include <cuda.h>
 
+#include <algorithm>
 #include <cstring>
+#include <utility>
 
 #include "block.h"
 #include "common.cuh"
@@ -47,6 +50,7 @@ constexpr int kTileA = kBM * kBK * 2;
 constexpr int kMaxProblems = 4;
 constexpr int kEpiWarps = 8;
 
+// The epilogue of a launch's first product (any others: kEpiStore).
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
 
 // Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA), then, for
@@ -77,9 +81,14 @@ struct Problem {
   uint16_t* out;        // bf16 [M, N]
 };
 
+// Launches of several products list each unit's tiles (see list_tiles); the others give unit
+// u the tiles u, u + units, ...
+constexpr int kMaxListed = 2048, kMaxUnits = 160;
+
 struct GemmParams {
   Problem p[kMaxProblems];
-  int n_problems, tiles;
+  int n_problems, tiles, listed;
+  uint16_t first[kMaxUnits + 1], list[kMaxListed];
   GluAct act;
   float *g, *u;         // saved (kEpiGlu: written when non-null; kEpiDact: read)
   uint16_t* out2;       // kEpiDact: du (out: dg)
@@ -113,6 +122,16 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& g, int t) {
   tl.n = r / rows;
   tl.m = m0 + (r - tl.n * rows);
   return tl;
+}
+
+// The i-th tile of a unit, or -1.
+__device__ __forceinline__ int nth_tile(const GemmParams& g, int unit, int units, int i) {
+  if (g.listed) {
+    i += g.first[unit];
+    return i < g.first[unit + 1] ? g.list[i] : -1;
+  }
+  const long long t = unit + (long long)units * i;
+  return t < g.tiles ? (int)t : -1;
 }
 
 // Descriptor of an MN-major tile of 128-byte-swizzled boxes [64 k][64 mn]: 8 k rows are
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
       uint32_t ph = 0;
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
       const uint32_t lead0 = CG == 2 ? in_leader(full0) : full0, stage0 = tc::smem_u32(smem);
-      for (int t = unit; t < g.tiles && !*abort; t += units) {
+      for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
         const int m0 = (tl.m * CG + rank) * kBM;
@@ -422,7 +441,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
       bool any = false;
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
       const uint32_t stage0 = tc::smem_u32(smem);
-      for (int t = unit; t < g.tiles && !*abort; t += units) {
+      for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
         const bool a_mn = p.a_mn, b_mn = p.b_mn;
@@ -472,9 +491,10 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
     if (tc::elect_one()) {
       int slot = 0, filled = 0;
       uint32_t ph = 0;
-      for (int t = unit; t < g.tiles && !*abort; t += units) {
+      for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
+        if (tl.pi) continue;
         const int mb = tl.m * CG + rank;
         const int n0 = tl.n * p.tn, cols = min(p.tn, p.N - n0);
         for (int c0 = 0; c0 < cols; c0 += 16) {
@@ -512,7 +532,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
     const bool clamped = g.act.act == MOE_ACT_CLAMPED_GLU;
     int b = 0, sl = 0;                      // sl: dact, chunks seen (slot sl % kSlots)
     uint32_t aph = 0;
-    for (int t = unit; t < g.tiles && !*abort; t += units) {
+    for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.pi];
       if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
@@ -565,7 +585,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
             store_bf16x16(orow + c0, v, left, wide);
           }
         }
-      } else if (EPI == kEpiDact) {
+      } else if (EPI == kEpiDact && tl.pi == 0) {
         const int n_chunks = (cols + 15) / 16;
         for (int j = 0; j < n_chunks; ++j) {
           const int n = sl + j;
@@ -638,14 +658,7 @@ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) ==
 
 template <int CG, int EPI>
 cudaError_t prepare_kernel() {
-  static bool done[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(glu_gemm_kernel<CG, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Lay<CG, EPI>::kSmemBytes);
-  if (e == cudaSuccess) done[dev] = true;
-  return e;
+  return allow_smem<glu_gemm_kernel<CG, EPI>>(Lay<CG, EPI>::kSmemBytes);
 }
 
 // SMs, and pairs of SMs that can hold a cluster of two at one time.
@@ -692,13 +705,6 @@ cudaError_t launch_cg(const GemmParams& g, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<CG, EPI>, g);
 }
 
-template <int EPI>
-cudaError_t launch(GemmParams& g, int cg, cudaStream_t s) {
-  g.tiles = 0;
-  for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt;
-  return cg == 2 ? launch_cg<2, EPI>(g, s) : launch_cg<1, EPI>(g, s);
-}
-
 // Clocks of one chunk of 64 k with tn columns of B: the MMAs (2 per column for the 128
 // rows of an SM) or its operands' way into shared memory (about 64 bytes per clock).
 int chunk_clocks(int cg, int tn) {
@@ -725,6 +731,64 @@ void pick_tile(int M, int N, int chunks, int per, int* cg, int* tn) {
       }
     }
   }
+}
+
+// Clocks of a tile: its chunks, and what its epilogue adds to the next tile's start.
+long long tile_clocks(const Problem& p, int cg) {
+  return (long long)p.nkc * p.segs * chunk_clocks(cg, p.tn) + kTileClocks;
+}
+
+// Gives the tiles of several products, the longest first, each to the unit that is done
+// first; returns the clocks until the last is done.  With more tiles than the list holds
+// (then there are many per unit) they go round in turn.
+long long list_tiles(GemmParams& g, int cg) {
+  const int units = cg == 2 ? pair_count() : sm_count();
+  g.tiles = 0;
+  for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt;
+  g.listed = g.n_problems > 1 && g.tiles <= kMaxListed && units <= kMaxUnits;
+  if (!g.listed) return 0;
+  int order[kMaxProblems], start[kMaxProblems], n = 0;
+  for (int i = 0; i < g.n_problems; ++i) {
+    order[i] = i;
+    start[i] = n;
+    n += g.p[i].mt * g.p[i].nt;
+  }
+  std::sort(order, order + g.n_problems, [&](int a, int b) { return tile_clocks(g.p[a], cg) > tile_clocks(g.p[b], cg); });
+  // a heap of (clocks so far, unit); who took which tile
+  std::pair<long long, int> heap[kMaxUnits];
+  for (int u = 0; u < units; ++u) heap[u] = {0, -u};   // equal loads: the lowest unit first
+  auto later = [](const std::pair<long long, int>& a, const std::pair<long long, int>& b) {
+    return a.first != b.first ? a.first > b.first : a.second < b.second;
+  };
+  std::make_heap(heap, heap + units, later);
+  uint16_t taken_by[kMaxListed], count[kMaxUnits] = {};
+  long long end = 0;
+  for (int i = 0; i < g.n_problems; ++i) {
+    const Problem& p = g.p[order[i]];
+    const long long c = tile_clocks(p, cg);
+    for (int t = 0; t < p.mt * p.nt; ++t) {
+      std::pop_heap(heap, heap + units, later);
+      auto& least = heap[units - 1];
+      least.first += c;
+      if (least.first > end) end = least.first;
+      taken_by[start[order[i]] + t] = (uint16_t)(-least.second);
+      ++count[-least.second];
+      std::push_heap(heap, heap + units, later);
+    }
+  }
+  g.first[0] = 0;
+  for (int u = 0; u < units; ++u) g.first[u + 1] = (uint16_t)(g.first[u] + count[u]);
+  uint16_t at[kMaxUnits];
+  std::copy(g.first, g.first + units, at);
+  for (int i = 0; i < g.n_problems; ++i)   // a unit's tiles in the order it took them
+    for (int t = start[order[i]], e = t + g.p[order[i]].mt * g.p[order[i]].nt; t < e; ++t) g.list[at[taken_by[t]]++] = (uint16_t)t;
+  return end;
+}
+
+template <int EPI>
+cudaError_t launch(GemmParams& g, int cg, cudaStream_t s) {
+  list_tiles(g, cg);
+  return cg == 2 ? launch_cg<2, EPI>(g, s) : launch_cg<1, EPI>(g, s);
 }
 
 // D [M, N] = sum over segments of A_s B_s^T, k of length K in each.  a_mn / b_mn: the
@@ -802,14 +866,17 @@ cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16
 }
 
 cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint32_t* status, cudaStream_t s) {
+                            uint16_t* du, uint16_t* dwd, uint32_t* status, cudaStream_t s) {
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
-  g.n_problems = 1;
   int cg, tn;
   pick_tile(T, w.ff, cdiv(w.d, kBK), 1, &cg, &tn);
-  if (!set_problem(g.p[0], cg, tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg)) return cudaErrorInvalidValue;
+  if (!set_problem(g.p[g.n_problems++], cg, tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg))
+    return cudaErrorInvalidValue;
   g.p[0].wide = g.p[0].wide && aligned32(du);
+  // dWd = dy^T h waits for nothing that this launch computes: its tiles fill up the SMs
+  if (dwd && !set_problem(g.p[g.n_problems++], cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd))
+    return cudaErrorInvalidValue;
   g.act = GluAct{w.act, w.limit, w.alpha};
   g.g = sv.g;
   g.u = sv.u;
@@ -819,23 +886,15 @@ cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const
   return launch<kEpiDact>(g, cg, s);
 }
 
-cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
-                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
-                             uint16_t* dwd, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, int T, const uint16_t* dg, const uint16_t* du,
+                             uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint32_t* status, cudaStream_t s) {
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   bool ok = true;
-  // the longest tiles first: dx sums over 2 ff, the weights' gradients over T
-  const int cg = w.d > kBM && w.ff > kBM && T > kBM ? 2 : 1, tn = kMaxN;
-  const bool dx_first = 2 * w.ff > T;
-  auto add_dx = [&] {
-    if (dx) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
-  };
-  if (dx_first) add_dx();
-  if (dwg) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
-  if (dwu) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
-  if (dwd) ok = ok && set_problem(g.p[g.n_problems++], cg, tn, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd);
-  if (!dx_first) add_dx();
+  const int cg = w.d > kBM && w.ff > kBM && T > kBM ? 2 : 1;
+  if (dx) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
+  if (dwg) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
+  if (dwu) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
   if (!ok) return cudaErrorInvalidValue;
   if (!g.n_problems) return cudaSuccess;
   g.status = status;

@@ -453,10 +453,9 @@ cudaError_t launch_one(const F& f, int n_out, const Tokens& tk, const GluAct& ac
   const int most = (Mem<NC>::kPhaseBytes / (8 * NC) - 256) / (F::kStep * 2) / kWarps * kWarps;
   c.phase_steps = c.steps <= most ? (c.steps + c.ws - 1) / c.ws * c.ws : most;
   const int smem = Mem<NC>::kRingBytes + 8 * NC * (c.phase_steps * F::kStep * 2 / 128 * 128 + 128 + F::kPad);
-  auto* kernel = skinny_kernel<F, GLU, NC>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<skinny_kernel<F, GLU, NC>>(227 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(ctas, passes), dim3(kWarps * 32), smem, s, f, n_out, tk, c, act, y, y_lo, clear_status,
+  return launch_pdl(skinny_kernel<F, GLU, NC>, dim3(ctas, passes), dim3(kWarps * 32), smem, s, f, n_out, tk, c, act, y, y_lo, clear_status,
                     early);
 }
 
