@@ -44,12 +44,14 @@ cudaError_t launch_glu_gate_up(const GluParams& p, const uint16_t* x, int T, uin
 // y = h Wd^T
 cudaError_t launch_glu_down(const GluParams& p, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
                             cudaStream_t s);
-// dg, du [T, ff] from dy and the saved g and u; and, where dwd is non-null, dWd
+// dg, du [T, ff] from dy and the saved g and u; and dWd, if dwd is non-null and the launch
+// can take it along (*with_down)
 cudaError_t launch_glu_dact(const GluParams& p, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint16_t* dwd, uint32_t* status, cudaStream_t s);
-// dx, dWg, dWu, each where its pointer is non-null, in one launch
-cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, int T, const uint16_t* dg, const uint16_t* du,
-                             uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint32_t* status, cudaStream_t s);
+                            uint16_t* du, uint16_t* dwd, bool* with_down, uint32_t* status, cudaStream_t s);
+// dx, dWg, dWu, dWd, each where its pointer is non-null
+cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
+                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
+                             uint16_t* dwd, uint32_t* status, cudaStream_t s);
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold);
 
 // Few tokens (skinny.cu): the weights stream through warp MMAs, every 16 tokens.

@@ -173,9 +173,12 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
   uint16_t* du = reinterpret_cast<uint16_t*>(base + L.du);
   const GluSaved sv = saved_at(const_cast<void*>(saved), saved_layout(*cfg, T));
   const uint16_t* dyi = static_cast<const uint16_t*>(dy);
-  BLOCK_CUDA(launch_glu_dact(p, dyi, T, sv, dg, du, static_cast<uint16_t*>(dw.down), status, s));
-  BLOCK_CUDA(launch_glu_grads(p, static_cast<const uint16_t*>(x), T, dg, du, static_cast<uint16_t*>(dx),
-                              static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up), status, s));
+  bool with_down = false;
+  uint16_t* dwd = static_cast<uint16_t*>(dw.down);
+  BLOCK_CUDA(launch_glu_dact(p, dyi, T, sv, dg, du, dwd, &with_down, status, s));
+  BLOCK_CUDA(launch_glu_grads(p, static_cast<const uint16_t*>(x), dyi, T, sv, dg, du, static_cast<uint16_t*>(dx),
+                              static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up),
+                              with_down ? nullptr : dwd, status, s));
   return MOE_OK;
 }
 

@@ -25,6 +25,10 @@
 // tile at 256 columns: 96 bytes per clock and SM).  CG = 1 (128-row tiles) serves outputs
 // of few rows.
 //
+// SPLIT: when the tiles are too few for the SMs (few tokens), the 2, 4 or 8 CTAs of a
+// cluster take consecutive parts of one tile's k; each leaves its partial tile in shared
+// memory, and each adds up and finishes its share of the columns over the CTAs, in order.
+//
 // Warp roles of the persistent CTA: warp 0 TMA producer; warp 1 owner of TMEM and, in the
 // first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
 // epilogue runs under the next tile's MMAs); warps 2..9 epilogue, two per TMEM lane
@@ -53,17 +57,18 @@ constexpr int kEpiWarps = 8;
 // The epilogue of a launch's first product (any others: kEpiStore).
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
 
-// Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA), then, for
-// dact, kSlots slots of 16 columns of g and u (128 rows x 16 x 4 bytes each).
-template <int CG, int EPI>
+constexpr int kMaxStages = 10;
+
+// Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA, as many as the
+// launch's widest tile has, so that narrow tiles get more stages), then, for dact, kSlots
+// slots of 16 columns of g and u (128 rows x 16 x 4 bytes each).
+template <int EPI>
 struct Lay {
-  static constexpr int kBRows = kMaxN / CG;
-  static constexpr int kStageBytes = kTileA + kBRows * kBK * 2;
   static constexpr int kSlots = EPI == kEpiDact ? 4 : 0;
   static constexpr int kRing = kSlots ? kSlots : 1;
   static constexpr int kSlotBytes = 2 * 128 * 16 * 4;
-  static constexpr int kStages = (CG == 2 ? 6 : 4) - (EPI == kEpiDact ? (CG == 2 ? 2 : 1) : 0);
-  static constexpr int kSmemBytes = kStages * kStageBytes + kSlots * kSlotBytes + 1024;
+  static constexpr int kStageSpace = 225 * 1024 - kSlots * kSlotBytes;
+  static constexpr int kSmemBytes = kStageSpace + kSlots * kSlotBytes + 1024;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
 };
 
@@ -88,6 +93,7 @@ constexpr int kMaxListed = 2048, kMaxUnits = 160;
 struct GemmParams {
   Problem p[kMaxProblems];
   int n_problems, tiles, listed;
+  int stages, stage_bytes;   // of the ring
   uint16_t first[kMaxUnits + 1], list[kMaxListed];
   GluAct act;
   float *g, *u;         // saved (kEpiGlu: written when non-null; kEpiDact: read)
@@ -327,20 +333,89 @@ __device__ __forceinline__ void settle(float& v, bool near, const uint16_t* x, c
   }
 }
 
-template <int CG, int EPI>
-__global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(const __grid_constant__ GemmParams g) {
-  using L = Lay<CG, EPI>;
-  constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes;
+// The address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+// 8 finished columns of one row of a split tile: the sums v (gate/up: v gate, w up).
+template <int EPI>
+__device__ __forceinline__ void finish8(const GemmParams& g, const Problem& p, int mb, int row, int n, float (&v)[8],
+                                        float (&w)[8]) {
+  const bool clamped = g.act.act == MOE_ACT_CLAMPED_GLU;
+  const int m = mb * kBM + row, lane = row & 31;
+  const bool valid = m < p.M;
+  const size_t blk = ((size_t)mb * (p.N / 4) + n / 4) * 128 + row;   // saved g, u: float4 index
+  if (EPI == kEpiGlu) {
+    if (clamped && g.g) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const size_t f = (size_t)(n + i) * g.d;
+        settle(v[i], valid && fabsf(v[i] - g.act.limit) <= g.tau, g.x, g.wg + f, g.d, m - lane, lane);
+        settle(w[i], valid && fabsf(fabsf(w[i]) - g.act.limit) <= g.tau, g.x, g.wu + f, g.d, m - lane, lane);
+      }
+    }
+    if (!valid) return;
+    if (g.g) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        reinterpret_cast<float4*>(g.g)[blk + 128 * i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        reinterpret_cast<float4*>(g.u)[blk + 128 * i] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = glu_value(g.act, v[i], w[i]);
+  } else if (EPI == kEpiDact) {
+    if (!valid) return;
+    float gv[8], uv[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<float4*>(gv + 4 * i) = reinterpret_cast<const float4*>(g.g)[blk + 128 * i];
+      *reinterpret_cast<float4*>(uv + 4 * i) = reinterpret_cast<const float4*>(g.u)[blk + 128 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (clamped) glu_grad<true>(g.act, gv[i], uv[i], v[i], v[i], w[i]);
+      else glu_grad<false>(g.act, gv[i], uv[i], v[i], v[i], w[i]);
+    }
+    *reinterpret_cast<uint4*>(g.out2 + (size_t)m * p.N + n) =
+        make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+  }
+  if (valid)
+    *reinterpret_cast<uint4*>(p.out + (size_t)m * p.N + n) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+template <int CG, int EPI, bool SPLIT>
+__global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const __grid_constant__ GemmParams g) {
+  using L = Lay<EPI>;
+  const int kStages = g.stages, kStageBytes = g.stage_bytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
-  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t sfull_bar[L::kRing], sempty_bar[L::kRing];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  // SPLIT: a cluster is a unit with one tile, of which this CTA takes part `part`
+  const int parts = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / (CG * parts), units = gridDim.x / (CG * parts);
   volatile int* abort = &abort_s;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -389,11 +464,13 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
         const uint32_t bytes = CG * ((uint32_t)kTileA + (b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u));
         const int nkc = p.nkc, segs = p.segs;
         bool ok = true;
+        const int from = nkc * segs * part / parts, to = nkc * segs * (part + 1) / parts;   // SPLIT: of its chunks
         for (int seg = 0; seg < segs && ok; ++seg) {
           const CUtensorMap* ma = &p.a[seg];
           const CUtensorMap* mb = p.pair ? &p.b[CG == 2 ? rank : 0] : &p.b[seg];
           const CUtensorMap* mb1 = &p.b[1];
-          for (int c = 0, k0 = 0; c < nkc; ++c, k0 += kBK) {
+          const int c0 = max(from - seg * nkc, 0), c1 = min(to - seg * nkc, nkc);
+          for (int c = c0, k0 = c0 * kBK; c < c1; ++c, k0 += kBK) {
             if (!tc::mbar_wait(empty0 + 8u * s, ph ^ 1, abort, g.status)) {
               ok = false;
               break;
@@ -453,7 +530,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
         tc::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)b * 256u;
         bool ok = true;
-        const int chunks = p.nkc * p.segs;
+        const int all = p.nkc * p.segs, chunks = all * (part + 1) / parts - all * part / parts;
         for (int c = 0; c < chunks; ++c) {
           if (!tc::mbar_wait(full0 + 8u * s, ph, abort, g.status)) {
             ok = false;
@@ -488,7 +565,7 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
   } else if (EPI == kEpiDact && warp == 2 + kEpiWarps) {
     // ---------------------------------------------------------------- saved g, u
     // 16 columns of the CTA's 128 rows are 8 KiB of g and 8 KiB of u, contiguous each.
-    if (tc::elect_one()) {
+    if (!SPLIT && tc::elect_one()) {
       int slot = 0, filled = 0;
       uint32_t ph = 0;
       for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
@@ -544,7 +621,16 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
       const int tn = p.pair ? p.tn >> 1 : p.tn;
       const int n0 = tl.n * tn, cols = min(tn, p.N - n0);
       uint16_t* orow = p.out + (size_t)m * p.N + n0;
-      if (EPI == kEpiGlu) {
+      if (SPLIT) {
+        // the partial tile, over the ring: [column][row]
+        float* st = reinterpret_cast<float*>(smem) + row;
+        for (int c0 = 16 * par; c0 < p.tn; c0 += 32) {
+          float v[16];
+          tc::tmem_ld16(taddr + (uint32_t)c0, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st[(c0 + i) * kBM] = v[i];
+        }
+      } else if (EPI == kEpiGlu) {
         const size_t blk = ((size_t)mb * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
         for (int c0 = 16 * par; c0 < cols; c0 += 32) {
           float v[16], w[16];
@@ -638,10 +724,34 @@ __global__ void __launch_bounds__(Lay<CG, EPI>::kThreads, 1) glu_gemm_kernel(con
     }
   }
 
+  if (SPLIT) {
+    cluster_sync();   // every part lies in its CTA's shared memory
+    if (warp >= 2 && warp < 2 + kEpiWarps) {
+      const int q = warp & 3, par = (warp - 2) >> 2, row = 32 * q + lane;
+      const Tile tl = tile_at(g, unit);
+      const Problem& p = g.p[tl.pi];
+      const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn;
+      const uint32_t st = tc::smem_u32(smem) + 4u * (uint32_t)row;
+      const int u0 = tn / 8 * part / parts, u1 = tn / 8 * (part + 1) / parts;   // its 8-column shares
+      for (int u = u0 + par; u < u1; u += 2) {
+        if (n0 + 8 * u >= p.N) break;
+        float v[8] = {}, w[8] = {};
+        for (int r = 0; r < parts; ++r) {
+          const uint32_t at = in_cta(st, (uint32_t)r) + (uint32_t)(8 * u * kBM * 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += ld_cluster(at + (uint32_t)(i * kBM * 4));
+          if (EPI == kEpiGlu)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] += ld_cluster(at + (uint32_t)((tn + i) * kBM * 4));
+        }
+        finish8<EPI>(g, p, tl.m, row, n0 + 8 * u, v, w);
+      }
+    }
+  }
   pdl_trigger();
   tc::tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
+  if (CG == 2 || SPLIT) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
   tc::tc_fence_after();
   if (warp == 1) tmem_dealloc<CG>(tmem);
 }
@@ -656,81 +766,104 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-template <int CG, int EPI>
+template <int CG, int EPI, bool SPLIT>
 cudaError_t prepare_kernel() {
-  return allow_smem<glu_gemm_kernel<CG, EPI>>(Lay<CG, EPI>::kSmemBytes);
+  return allow_smem<glu_gemm_kernel<CG, EPI, SPLIT>>(Lay<EPI>::kSmemBytes);
 }
 
-// SMs, and pairs of SMs that can hold a cluster of two at one time.
-int pair_count() {
-  static int n[64] = {};
+// How many clusters of n CTAs (one CTA per SM) the GPU holds at one time.
+int cluster_count(int n) {
+  static int count[64][9] = {};
+  const int sms = sm_count();
+  if (n == 1) return sms;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return sm_count() / 2;
-  if (n[dev]) return n[dev];
-  if (prepare_kernel<2, kEpiStore>() != cudaSuccess) return sm_count() / 2;
+  if (dev < 0 || dev >= 64) return sms / n;
+  if (count[dev][n]) return count[dev][n];
+  if (prepare_kernel<2, kEpiStore, false>() != cudaSuccess) return sms / n;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = (unsigned)n;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count() / 2 * 2);
-  cfg.blockDim = dim3(Lay<2, kEpiStore>::kThreads);
-  cfg.dynamicSmemBytes = Lay<2, kEpiStore>::kSmemBytes;
+  cfg.gridDim = dim3(sms / n * n);
+  cfg.blockDim = dim3(Lay<kEpiStore>::kThreads);
+  cfg.dynamicSmemBytes = Lay<kEpiStore>::kSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int c = 0;
-  if (cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore>, &cfg) != cudaSuccess || c < 1) c = sm_count() / 2;
-  return n[dev] = c;
+  if (cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore, false>, &cfg) != cudaSuccess || c < 1) c = sms / n;
+  return count[dev][n] = c;
 }
 
-template <int CG, int EPI>
-cudaError_t launch_cg(const GemmParams& g, cudaStream_t s) {
-  const cudaError_t e = prepare_kernel<CG, EPI>();
+// How a launch runs: single CTAs or pairs (cg), or clusters of `parts` CTAs that split k.
+struct Way {
+  int cg, parts, tn;
+};
+
+template <int CG, int EPI, bool SPLIT>
+cudaError_t launch_as(const GemmParams& g, const Way& w, cudaStream_t s) {
+  const cudaError_t e = prepare_kernel<CG, EPI, SPLIT>();
   if (e != cudaSuccess) return e;
-  const int units = CG == 2 ? pair_count() : sm_count();
+  const int size = CG * w.parts;   // CTAs of a unit
+  const int units = SPLIT ? g.tiles : cluster_count(size);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = (unsigned)size;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CG * (g.tiles < units ? g.tiles : units));
-  cfg.blockDim = dim3(Lay<CG, EPI>::kThreads);
-  cfg.dynamicSmemBytes = Lay<CG, EPI>::kSmemBytes;
+  cfg.gridDim = dim3(size * (g.tiles < units ? g.tiles : units));
+  cfg.blockDim = dim3(Lay<EPI>::kThreads);
+  cfg.dynamicSmemBytes = Lay<EPI>::kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<CG, EPI>, g);
+  cfg.numAttrs = size > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<CG, EPI, SPLIT>, g);
+}
+
+int stage_bytes(int cg, int tn, bool b_mn) {
+  return kTileA + (b_mn ? cdiv(tn / cg, 64) * 8192 : tn / cg * 128);
+}
+
+int stages_for(int bytes, int space) {
+  const int n = space / bytes;
+  return n < kMaxStages ? n : kMaxStages;
 }
 
 // Clocks of one chunk of 64 k with tn columns of B: the MMAs (2 per column for the 128
-// rows of an SM) or its operands' way into shared memory (about 64 bytes per clock).
+// rows of an SM), its operands' way into shared memory (about 64 bytes per clock), or a
+// load's latency (about 2400 clocks while memory is busy) over the stages in flight.
 int chunk_clocks(int cg, int tn) {
   const int mma = 2 * tn, feed = (kTileA + tn * 128 / cg) / 64;
-  return mma > feed ? mma : feed;
+  const int wait = 2400 / stages_for(stage_bytes(cg, tn, false), Lay<kEpiStore>::kStageSpace);
+  return std::max(mma, std::max(feed, wait));
 }
 
-// The tile of one product [M, N] (per = 2: gate/up, N columns of each) alone on the GPU:
-// pairs or single CTAs, and the columns of B per tile, for which
-//   waves of tiles x (chunks x clocks per chunk + a tile's fixed cost)
-// is least.
+// The way to run one product [M, N] (per = 2: gate/up, N columns of each) alone on the GPU
+// for which
+//   waves of tiles x (chunks of a unit x clocks per chunk + a tile's fixed cost)
+// is least.  A part of a split tile pays about 2500 clocks more for the exchange.
 constexpr int kTileClocks = 2500;
-void pick_tile(int M, int N, int chunks, int per, int* cg, int* tn) {
-  long long best = -1;
-  for (int c = 1; c <= 2; ++c) {
-    const int units = c == 2 ? pair_count() : sm_count();
-    for (int n = 256; n >= 32; n -= 32) {
-      const long long tiles = (long long)cdiv(M, kBM * c) * cdiv(N, n / per);
-      const long long cost = (tiles + units - 1) / units * ((long long)chunks * chunk_clocks(c, n) + kTileClocks);
-      if (best < 0 || cost < best) {
-        best = cost;
-        *cg = c;
-        *tn = n;
-      }
+Way pick_way(int M, int N, int chunks, int per) {
+  Way best{1, 1, 256};
+  long long least = -1;
+  auto consider = [&](int cg, int parts, int tn) {
+    const int units = cluster_count(cg * parts);
+    const long long tiles = (long long)cdiv(M, kBM * cg) * cdiv(N, tn / per);
+    const long long cost = (tiles + units - 1) / units *
+                           ((long long)cdiv(chunks, parts) * chunk_clocks(cg, tn) + kTileClocks + (parts > 1 ? 2500 : 0));
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = Way{cg, parts, tn};
     }
-  }
+  };
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int tn = 256; tn >= 32; tn -= 32) consider(cg, 1, tn);
+  for (int parts = 2; parts <= 8 && parts <= chunks; parts <<= 1)
+    for (int tn = 256; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(1, parts, tn);
+  return best;
 }
 
 // Clocks of a tile: its chunks, and what its epilogue adds to the next tile's start.
@@ -739,14 +872,14 @@ long long tile_clocks(const Problem& p, int cg) {
 }
 
 // Gives the tiles of several products, the longest first, each to the unit that is done
-// first; returns the clocks until the last is done.  With more tiles than the list holds
-// (then there are many per unit) they go round in turn.
-long long list_tiles(GemmParams& g, int cg) {
-  const int units = cg == 2 ? pair_count() : sm_count();
+// first.  With more tiles than the list holds (then there are many per unit) they go round
+// in turn.
+void list_tiles(GemmParams& g, int cg) {
+  const int units = cluster_count(cg);
   g.tiles = 0;
   for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt;
   g.listed = g.n_problems > 1 && g.tiles <= kMaxListed && units <= kMaxUnits;
-  if (!g.listed) return 0;
+  if (!g.listed) return;
   int order[kMaxProblems], start[kMaxProblems], n = 0;
   for (int i = 0; i < g.n_problems; ++i) {
     order[i] = i;
@@ -762,7 +895,6 @@ long long list_tiles(GemmParams& g, int cg) {
   };
   std::make_heap(heap, heap + units, later);
   uint16_t taken_by[kMaxListed], count[kMaxUnits] = {};
-  long long end = 0;
   for (int i = 0; i < g.n_problems; ++i) {
     const Problem& p = g.p[order[i]];
     const long long c = tile_clocks(p, cg);
@@ -770,7 +902,6 @@ long long list_tiles(GemmParams& g, int cg) {
       std::pop_heap(heap, heap + units, later);
       auto& least = heap[units - 1];
       least.first += c;
-      if (least.first > end) end = least.first;
       taken_by[start[order[i]] + t] = (uint16_t)(-least.second);
       ++count[-least.second];
       std::push_heap(heap, heap + units, later);
@@ -782,13 +913,17 @@ long long list_tiles(GemmParams& g, int cg) {
   std::copy(g.first, g.first + units, at);
   for (int i = 0; i < g.n_problems; ++i)   // a unit's tiles in the order it took them
     for (int t = start[order[i]], e = t + g.p[order[i]].mt * g.p[order[i]].nt; t < e; ++t) g.list[at[taken_by[t]]++] = (uint16_t)t;
-  return end;
 }
 
 template <int EPI>
-cudaError_t launch(GemmParams& g, int cg, cudaStream_t s) {
-  list_tiles(g, cg);
-  return cg == 2 ? launch_cg<2, EPI>(g, s) : launch_cg<1, EPI>(g, s);
+cudaError_t launch(GemmParams& g, const Way& w, cudaStream_t s) {
+  g.stage_bytes = 0;
+  for (int i = 0; i < g.n_problems; ++i) g.stage_bytes = std::max(g.stage_bytes, stage_bytes(w.cg, g.p[i].tn, g.p[i].b_mn));
+  g.stage_bytes = (g.stage_bytes + 1023) / 1024 * 1024;
+  g.stages = stages_for(g.stage_bytes, Lay<EPI>::kStageSpace);
+  list_tiles(g, w.cg);
+  if (w.parts > 1) return launch_as<1, EPI, true>(g, w, s);
+  return w.cg == 2 ? launch_as<2, EPI, false>(g, w, s) : launch_as<1, EPI, false>(g, w, s);
 }
 
 // D [M, N] = sum over segments of A_s B_s^T, k of length K in each.  a_mn / b_mn: the
@@ -829,9 +964,9 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   p.nkc = cdiv(w.d, kBK);
   p.segs = 1;
   p.pair = 1;
-  int cg;
-  pick_tile(T, w.ff, p.nkc, 2, &cg, &p.tn);
-  p.mt = cdiv(T, kBM * cg);
+  const Way way = pick_way(T, w.ff, p.nkc, 2);
+  p.tn = way.tn;
+  p.mt = cdiv(T, kBM * way.cg);
   p.nt = cdiv(w.ff, p.tn / 2);
   p.wide = w.ff % 16 == 0 && aligned32(h);
   p.out = h;
@@ -850,7 +985,7 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   g.tau = w.limit * (float)(w.d / 16 + 8) * 0x1p-23f;
   g.status = status;
   g.clear_status = 1;
-  return launch<kEpiGlu>(g, cg, s);
+  return launch<kEpiGlu>(g, way, s);
 }
 
 cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
@@ -858,47 +993,61 @@ cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.n_problems = 1;
-  int cg, tn;
-  pick_tile(T, w.d, cdiv(w.ff, kBK), 1, &cg, &tn);
-  if (!set_problem(g.p[0], cg, tn, T, w.d, w.ff, h, nullptr, false, w.down, nullptr, false, y)) return cudaErrorInvalidValue;
+  const Way way = pick_way(T, w.d, cdiv(w.ff, kBK), 1);
+  if (!set_problem(g.p[0], way.cg, way.tn, T, w.d, w.ff, h, nullptr, false, w.down, nullptr, false, y)) return cudaErrorInvalidValue;
   g.status = status;
-  return launch<kEpiStore>(g, cg, s);
+  return launch<kEpiStore>(g, way, s);
 }
 
 cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint16_t* dwd, uint32_t* status, cudaStream_t s) {
+                            uint16_t* du, uint16_t* dwd, bool* with_down, uint32_t* status, cudaStream_t s) {
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
-  int cg, tn;
-  pick_tile(T, w.ff, cdiv(w.d, kBK), 1, &cg, &tn);
-  if (!set_problem(g.p[g.n_problems++], cg, tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg))
+  const Way way = pick_way(T, w.ff, cdiv(w.d, kBK), 1);
+  if (!set_problem(g.p[g.n_problems++], way.cg, way.tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg))
     return cudaErrorInvalidValue;
   g.p[0].wide = g.p[0].wide && aligned32(du);
-  // dWd = dy^T h waits for nothing that this launch computes: its tiles fill up the SMs
-  if (dwd && !set_problem(g.p[g.n_problems++], cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd))
-    return cudaErrorInvalidValue;
   g.act = GluAct{w.act, w.limit, w.alpha};
   g.g = sv.g;
   g.u = sv.u;
   g.out2 = du;
   g.status = status;
   g.clear_status = 1;
-  return launch<kEpiDact>(g, cg, s);
+  // dWd = dy^T h waits for nothing that this launch computes: its tiles fill up the SMs
+  // (a launch that splits k has none of its own)
+  *with_down = dwd && way.parts == 1;
+  if (*with_down &&
+      !set_problem(g.p[g.n_problems++], way.cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd))
+    return cudaErrorInvalidValue;
+  return launch<kEpiDact>(g, way, s);
 }
 
-cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, int T, const uint16_t* dg, const uint16_t* du,
-                             uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
+                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
+                             uint16_t* dwd, uint32_t* status, cudaStream_t s) {
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
+  g.status = status;
+  if (dx) {   // a long sum over few tiles splits it, in a launch of its own
+    const Way way = pick_way(T, w.d, 2 * cdiv(w.ff, kBK), 1);
+    if (way.parts > 1) {
+      if (!set_problem(g.p[g.n_problems++], way.cg, way.tn, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx))
+        return cudaErrorInvalidValue;
+      const cudaError_t e = launch<kEpiStore>(g, way, s);
+      if (e != cudaSuccess) return e;
+      g.n_problems = 0;
+      dx = nullptr;
+    }
+  }
   bool ok = true;
-  const int cg = w.d > kBM && w.ff > kBM && T > kBM ? 2 : 1;
+  const int cg = w.d > kBM && w.ff > kBM && (!dx || T > kBM) ? 2 : 1;
   if (dx) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
   if (dwg) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
   if (dwu) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
+  if (dwd) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd);
   if (!ok) return cudaErrorInvalidValue;
   if (!g.n_problems) return cudaSuccess;
-  g.status = status;
-  return launch<kEpiStore>(g, cg, s);
+  return launch<kEpiStore>(g, Way{cg, 1, kMaxN}, s);
 }
 
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold) { return tc::set_wait_test(polls, withhold); }

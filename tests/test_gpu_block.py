@@ -115,7 +115,7 @@ def glu_inputs(T, d, ff, act, seed=1):
 
 SHAPES = [(1, 8, 8), (8, 96, 12288), (10, 13544, 72), (16, 72, 8000), (3, 6152, 4864), (1, 2048, 512), (2, 40, 24), (7, 64, 64), (8, 264, 136), (16, 2880, 328), (17, 64, 2880),
           (33, 136, 520), (64, 512, 72), (128, 256, 256), (129, 264, 1000), (300, 520, 392), (777, 1024, 512),
-          (1500, 72, 2056)]
+          (1500, 72, 2056), (20, 4096, 2048), (100, 2056, 4096), (250, 4104, 264)]
 
 
 @pytest.mark.parametrize("act", [moe.ACT_SWIGLU, moe.ACT_CLAMPED_GLU])
