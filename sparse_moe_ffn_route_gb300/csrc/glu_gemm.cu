@@ -80,6 +80,7 @@ struct Problem {
   int M, N;             // rows and columns of the output (pair: columns of h)
   int nkc, segs, pair;
   int a_mn, b_mn;       // 1: MN-major
+  int a_blocks, b_blocks;   // MN-major, 1: maps of [block of 64][k][64], one load per chunk
   int tn;               // columns of B per tile (MMA N)
   int mt, nt;           // tiles (of 128 CG rows)
   int wide;             // output rows and base allow 32-byte stores
@@ -220,6 +221,23 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
   }
+}
+
+// The same for a box of [blocks of 64 columns][64 k][64 columns]: k0, first block.
+template <int CG>
+__device__ __forceinline__ void load_blocks(uint32_t dst, const CUtensorMap* map, int k0, int block, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k0), "r"(block), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k0), "r"(block), "r"(bar)
+        : "memory");
 }
 
 template <int CG>
@@ -457,6 +475,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         const Problem& p = g.p[tl.pi];
         const int m0 = (tl.m * CG + rank) * kBM;
         const bool a_mn = p.a_mn, b_mn = p.b_mn, two_b = CG == 1 && p.pair;
+        const bool a_blocks = p.a_blocks, b_blocks = p.b_blocks;
         const int half = p.tn >> 1;                          // pair: rows of gate, of up
         const int brows = p.tn / CG;                         // rows of B in this CTA
         const int n0 = p.pair ? tl.n * half : tl.n * p.tn + rank * brows;
@@ -478,13 +497,17 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
             if (issued != withheld) {
               const uint32_t fb = lead0 + 8u * s, sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + kTileA;
               if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8u * s, bytes);   // the peer's loads count here too
-              if (a_mn) {
+              if (a_blocks) {
+                load_blocks<CG>(sa, ma, k0, m0 >> 6, fb);
+              } else if (a_mn) {
                 load_tile<CG>(sa, ma, m0, k0, fb);
                 load_tile<CG>(sa + 8192, ma, m0 + 64, k0, fb);
               } else {
                 load_tile<CG>(sa, ma, k0, m0, fb);
               }
-              if (b_mn) {
+              if (b_blocks) {
+                load_blocks<CG>(sb, mb, k0, n0 >> 6, fb);
+              } else if (b_mn) {
                 for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, mb, n0 + 64 * j, k0, fb);
               } else {
                 load_tile<CG>(sb, mb, k0, n0, fb);
@@ -764,6 +787,33 @@ bool map_bf16(CUtensorMap* m, const uint16_t* base, int rows, int cols, int box_
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// A matrix [k, cols], cols a multiple of 64, seen as [cols / 64][k][64]: an MN-major tile of
+// `blocks` x 64 columns and 64 k is one box.  (With a ragged last block its rows would run
+// into the next row of the matrix, and past its end: those go by boxes of the plain map.)
+bool map_blocks(CUtensorMap* m, const uint16_t* base, int k, int cols, int blocks) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn || !base) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)k, (cuuint64_t)(cols / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+  const cuuint32_t box[3] = {64, kBK, (cuuint32_t)blocks}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 template <int CG, int EPI, bool SPLIT>
@@ -944,9 +994,18 @@ bool set_problem(Problem& p, int cg, int tn, int M, int N, int K, const uint16_t
   p.out = out;
   const uint16_t* a[2] = {a0, a1};
   const uint16_t* b[2] = {b0, b1};
+  const int brows = tn / cg;
+  p.a_blocks = a_mn && M % 64 == 0;
+  p.b_blocks = b_mn && N % 64 == 0 && brows % 64 == 0;
   for (int i = 0; i < p.segs; ++i) {
-    if (!(a_mn ? map_bf16(&p.a[i], a[i], K, M, 64) : map_bf16(&p.a[i], a[i], M, K, kBM))) return false;
-    if (!(b_mn ? map_bf16(&p.b[i], b[i], K, N, 64) : map_bf16(&p.b[i], b[i], N, K, tn / cg))) return false;
+    if (!(p.a_blocks ? map_blocks(&p.a[i], a[i], K, M, 2)
+          : a_mn     ? map_bf16(&p.a[i], a[i], K, M, 64)
+                     : map_bf16(&p.a[i], a[i], M, K, kBM)))
+      return false;
+    if (!(p.b_blocks ? map_blocks(&p.b[i], b[i], K, N, brows / 64)
+          : b_mn     ? map_bf16(&p.b[i], b[i], K, N, 64)
+                     : map_bf16(&p.b[i], b[i], N, K, brows)))
+      return false;
   }
   return true;
 }
