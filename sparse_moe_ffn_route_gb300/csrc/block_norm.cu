@@ -273,15 +273,53 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int tid, in
   }
 }
 
+// Threads of a CTA of the backward kernel, at most (768 with 80 registers each: 81 us instead
+// of 53 at 8192 x 2048; rows ahead 3 instead of 2: 57 us).
+constexpr int kBwdThreads = 512;
+
+// The two weights in fp32 in shared memory: the halves of a vector of 8 apart, so that a
+// warp's reads of 16 bytes per thread meet no bank twice.
+struct Weights {
+  float4* w;
+  int n;      // vectors of 8
+  __device__ __forceinline__ void fill(int which, const uint16_t* src) const {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      F2 v[4];
+      unpack8(ld8(src, 8 * i), v);
+      F2* lo = reinterpret_cast<F2*>(w + (2 * which) * n + i);
+      F2* hi = reinterpret_cast<F2*>(w + (2 * which + 1) * n + i);
+      lo[0] = v[0];
+      lo[1] = v[1];
+      hi[0] = v[2];
+      hi[1] = v[3];
+    }
+  }
+  __device__ __forceinline__ void get(int which, int vec, F2 (&v)[4]) const {
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(w + (2 * which) * n + vec);
+    const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(w + (2 * which + 1) * n + vec);
+    v[0].v = lo.x;
+    v[1].v = lo.y;
+    v[2].v = hi.x;
+    v[3].v = hi.y;
+  }
+};
+
 // Z, POST: as above; DA: da is given (else a's gradient is zero).  gt: threads of a group.
 template <int V, int DEPTH, bool Z, bool POST, bool DA>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
 block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
   extern __shared__ uint4 rows[];
-  __shared__ __align__(16) float sums[kMaxWarps][2][2][2 * kMaxWarps];   // group, row parity, exchange
+  // group, row parity, exchange: two values per warp of the group
+  __shared__ __align__(16) float sums[kBwdThreads / 32][2][2][2 * kMaxWarps];
+  constexpr bool kShared = V <= 2;   // the weights in shared memory, after the rows
+  const Weights weights{reinterpret_cast<float4*>(rows + (size_t)blockDim.x * DEPTH * 4 * V), g.d / 8};
   const int group = threadIdx.x / gt, groups = blockDim.x / gt, tid = threadIdx.x - group * gt;
   for (int i = threadIdx.x; i < groups * 8 * kMaxWarps; i += blockDim.x) (&sums[0][0][0][0])[i] = 0.f;
   pdl_wait();
+  if (kShared) {
+    if (POST) weights.fill(0, g.post_w);
+    if (DA) weights.fill(1, g.pre_w);
+  }
   __syncthreads();
   const int d = g.d, T = g.T, stride = gridDim.x * groups;
   const float inv_d = 1.f / (float)d, eps = g.eps;
@@ -295,37 +333,42 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
   int t = blockIdx.x + gridDim.x * group;
 #pragma unroll
   for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, t + s * stride, T, d);
-  F2 z[V][4];
-  // z of the row in `slot` and its sum of squares
-  auto take_z = [&](int slot, float& out) {
+  auto weight = [&](int which, int i, F2 (&w)[4]) {
+    if (kShared) weights.get(which, ahead.elem(i) >> 3, w);
+    else unpack8(ld8(which ? g.pre_w : g.post_w, ahead.elem(i)), w);
+  };
+  // sum z^2 of the row in `slot`
+  auto sum_z = [&](int slot) {
     F2 sum = f2(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (ahead.elem(i) < d) {
-        unpack8(ahead.get(slot, 1, i), z[i]);
-        if (POST) {
+        F2 z[4];
+        unpack8(ahead.get(slot, 1, i), z);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum = fma2(z[i][j], z[i][j], sum);
-        }
+        for (int j = 0; j < 4; ++j) sum = fma2(z[j], z[j], sum);
       }
-    out = both(sum);
+    return both(sum);
   };
   int slot = 0, par = 0;
+  float gate = g.gate && t < T ? g.gate[t] : 0.f;
   float sz = 0.f;   // sum z^2 of the row
   if (t < T && Z) {
-    float first[1] = {0.f};
     ahead.template wait<DEPTH - 1>();
-    take_z(0, first[0]);
-    if (POST) group_sum(first, sums[group][1][1], tid, gt, 1 + group);
-    sz = first[0];
+    if (POST) {
+      float first[1] = {sum_z(0)};
+      group_sum(first, sums[group][1][1], tid, gt, 1 + group);
+      sz = first[0];
+    }
   }
   for (; t < T; t += stride, par ^= 1) {
     const size_t base = (size_t)t * d;
     F2 y[V][4], D[V][4];
     float c = g.bs, s = 1.f;
     if (g.gate) {
-      s = sigmoid(g.gate[t]);
+      s = sigmoid(gate);
       c *= s;
+      if (t + stride < T) gate = g.gate[t + stride];   // the next row's, ahead of its use
     }
     const float rz = POST ? inv_rms(sz, inv_d, eps) : 1.f;
     const F2 cr = f2(c * rz);
@@ -339,12 +382,13 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
           F2 w[4], v[4];
           unpack8(ahead.get(slot, 0, i), y[i]);
           if (Z) {
-            if (POST) unpack8(ld8(g.post_w, ahead.elem(i)), w);
+            unpack8(ahead.get(slot, 1, i), v);
+            if (POST) weight(0, i, w);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = fma2(cr, POST ? mul2(z[i][j], w[j]) : z[i][j], mul2(rs, y[i][j]));
+            for (int j = 0; j < 4; ++j) y[i][j] = fma2(cr, POST ? mul2(v[j], w[j]) : v[j], mul2(rs, y[i][j]));
           }
           unpack8(ahead.get(slot, 3, i), v);
-          unpack8(ld8(g.pre_w, ahead.elem(i)), w);
+          weight(1, i, w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             D[i][j] = mul2(v[j], w[j]);   // the gradient through a, before its row terms
@@ -387,20 +431,21 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
           *reinterpret_cast<uint4*>(g.dx + base + ahead.elem(i)) = pack8(v);
         }
         if (Z) {
+          F2 z[4];
+          unpack8(ahead.get(slot, 1, i), z);
           if (POST) {
             F2 w[4];
-            unpack8(ld8(g.post_w, ahead.elem(i)), w);
+            weight(0, i, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              dpost[i][j] = fma2(cr, mul2(D[i][j], z[i][j]), dpost[i][j]);
+              dpost[i][j] = fma2(cr, mul2(D[i][j], z[j]), dpost[i][j]);
               D[i][j] = mul2(D[i][j], w[j]);
             }
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dot = fma2(D[i][j], z[i][j], dot);
-          if (g.dz && POST) {   // z is in y's place until S is known
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = z[i][j];
+          for (int j = 0; j < 4; ++j) {
+            dot = fma2(D[i][j], z[j], dot);
+            if (POST) y[i][j] = z[j];   // z waits in y's place until S is known
           }
         }
       }
@@ -411,7 +456,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
     if (Z) {
       ahead.template wait<DEPTH - 1>();
       float sw[2] = {both(dot), 0.f};     // S, sum z^2 of the next row
-      if (t + stride < T) take_z(slot, sw[1]);
+      if (POST && t + stride < T) sw[1] = sum_z(slot);
       if (POST || g.dgate) group_sum(sw, sums[group][par][1], tid, gt, 1 + group);
       sz = sw[1];
       const F2 kz = f2(POST ? -(rz * rz * sw[0] * inv_d) : 0.f);
@@ -528,9 +573,11 @@ cudaError_t pick_fwd(const NormArgs& g, cudaStream_t s) {
 template <int V, int DEPTH, bool Z, bool POST, bool DA>
 cudaError_t run_bwd(const NormArgs& g, int ctas, cudaStream_t s) {
   auto* kernel = block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>;
-  const int gt = ((g.d / 8 + V - 1) / V + 31) / 32 * 32, threads = kMaxWarps * 32 / gt * gt;
-  const int smem = DEPTH * 4 * V * threads * 16;
-  const cudaError_t e = allow_smem<block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>>(DEPTH * 4 * V * kMaxWarps * 32 * 16);
+  const int gt = ((g.d / 8 + V - 1) / V + 31) / 32 * 32, threads = kBwdThreads / gt * gt;
+  constexpr int kWeightBytes = V <= 2 ? 8192 * 2 * 4 : 0;   // of the longest row
+  const int smem = DEPTH * 4 * V * threads * 16 + (V <= 2 ? g.d * 2 * 4 : 0);
+  const cudaError_t e = allow_smem<block_norm_bwd_kernel<V, DEPTH, Z, POST, DA>>(DEPTH * 4 * V * kBwdThreads * 16 +
+                                                                                         kWeightBytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(ctas), dim3(threads), smem, s, g, gt);
 }
@@ -570,7 +617,7 @@ cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   g.dgate = o.dgate;
   g.part = o.dpost_w || o.dpre_w ? parts : nullptr;
   const int n = block_norm_parts(T);
-  const cudaError_t e = g.d <= 8192 ? pick_bwd<2, 3>(g, n, s) : pick_bwd<4, 1>(g, n, s);
+  const cudaError_t e = g.d <= 8192 ? pick_bwd<2, 2>(g, n, s) : pick_bwd<4, 1>(g, n, s);
   if (e != cudaSuccess || !g.part) return e;
   return launch_pdl(block_norm_reduce_kernel, dim3((g.d + 31) / 32, 2), dim3(256), 0, s, static_cast<const float*>(parts),
                     n, g.d, o.dpost_w, o.dpre_w);
