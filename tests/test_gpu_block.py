@@ -303,6 +303,34 @@ def test_glu_repeats_bit_for_bit_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,d,ff", [(64, 2048, 256), (300, 256, 2048), (700, 512, 1024)])
+def test_glu_wait_gives_up_reports_timeout_and_recovers(T, d, ff):
+    """A load that is never issued (the test hook) runs the bounded waits out: the call reports
+    MOE_ERR_TIMEOUT, and the next one is right.  Split tiles, pairs and many tiles."""
+    x, w, dy = glu_inputs(T, d, ff, 0)
+    cfg = moe.glu_cfg(d, ff)
+    ws, saved = moe.glu_workspace(cfg, T), moe.glu_saved(cfg, T)
+    want = glu64(x, w.gate, w.up, w.down, dy, 0)
+    for backward in (False, True):
+        moe.moe_glu_forward(cfg, x, w, saved=saved, ws=ws)
+        assert moe.moe_device_status(ws)[0] == moe.MOE_OK
+        try:
+            moe.moe_test_set_wait_limit(1 << 14, True)
+            if backward:
+                moe.moe_glu_backward(cfg, x, w, saved, dy, ws=ws)
+            else:
+                moe.moe_glu_forward(cfg, x, w, ws=ws)
+            status, bits = moe.moe_device_status(ws)
+        finally:
+            moe.moe_test_set_wait_limit(moe.DEFAULT_WAIT_POLLS, False)
+        assert status == -7 and bits & (1 << 8), (status, bits)
+    y = moe.moe_glu_forward(cfg, x, w, saved=saved, ws=ws)
+    dx, g = moe.moe_glu_backward(cfg, x, w, saved, dy, ws=ws)
+    assert moe.moe_device_status(ws)[0] == moe.MOE_OK
+    for name, t in (("y", y), ("dx", dx), ("gate", g.gate), ("up", g.up), ("down", g.down)):
+        close(t, *want[name], name)
+
+
 # ----------------------------------------------------------------------------- norms
 EPS = 1e-6
 
