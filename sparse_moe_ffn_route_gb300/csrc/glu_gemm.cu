@@ -358,10 +358,29 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Not volatile: loads of several CTAs' shared memory go out together.
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
+}
+
+// sum over the `parts` CTAs of the cluster, in order, of 8 columns of a partial tile at
+// `at`: the loads of two CTAs at a time are in flight together.
+__device__ __forceinline__ void sum_parts(uint32_t at, int parts, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  for (int r = 0; r < parts; r += 2) {   // parts is even
+    float a[8], b[8];
+    const uint32_t pa = in_cta(at, (uint32_t)r), pb = in_cta(at, (uint32_t)r + 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = ld_cluster(pa + (uint32_t)(i * kBM * 4));
+      b[i] = ld_cluster(pb + (uint32_t)(i * kBM * 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (v[i] + a[i]) + b[i];
+  }
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -453,13 +472,14 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     tc::fence_barrier_init();
   }
   if (warp == 1) tmem_alloc<CG>(tc::smem_u32(&tmem_base_s));
-  pdl_wait();
   tc::tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();   // the peer's barriers and TMEM are ready
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  if (g.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0u;
+  // Each role waits for the kernel before this one only where it first touches global
+  // memory: the barriers, TMEM and the first tile's parameters (cold reads of the constant
+  // bank: about 1 us) are then ready.
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -483,6 +503,10 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         const uint32_t bytes = CG * ((uint32_t)kTileA + (b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u));
         const int nkc = p.nkc, segs = p.segs;
         bool ok = true;
+        if (nth == 0) {
+          pdl_wait();
+          if (g.clear_status && blockIdx.x == 0) *g.status = 0u;
+        }
         const int from = nkc * segs * part / parts, to = nkc * segs * (part + 1) / parts;   // SPLIT: of its chunks
         for (int seg = 0; seg < segs && ok; ++seg) {
           const CUtensorMap* ma = &p.a[seg];
@@ -594,6 +618,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
         const Tile tl = tile_at(g, t);
         const Problem& p = g.p[tl.pi];
+        if (nth == 0) pdl_wait();
         if (tl.pi) continue;
         const int mb = tl.m * CG + rank;
         const int n0 = tl.n * p.tn, cols = min(p.tn, p.N - n0);
@@ -635,8 +660,6 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.pi];
-      if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
-      tc::tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * 256u;
       const int mb = tl.m * CG + rank;
       const int m = mb * kBM + row;
@@ -644,6 +667,9 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       const int tn = p.pair ? p.tn >> 1 : p.tn;
       const int n0 = tl.n * tn, cols = min(tn, p.N - n0);
       uint16_t* orow = p.out + (size_t)m * p.N + n0;
+      if (nth == 0) pdl_wait();
+      if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
+      tc::tc_fence_after();
       if (SPLIT) {
         // the partial tile, over the ring: [column][row]
         float* st = reinterpret_cast<float*>(smem) + row;
@@ -758,15 +784,9 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       const int u0 = tn / 8 * part / parts, u1 = tn / 8 * (part + 1) / parts;   // its 8-column shares
       for (int u = u0 + par; u < u1; u += 2) {
         if (n0 + 8 * u >= p.N) break;
-        float v[8] = {}, w[8] = {};
-        for (int r = 0; r < parts; ++r) {
-          const uint32_t at = in_cta(st, (uint32_t)r) + (uint32_t)(8 * u * kBM * 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += ld_cluster(at + (uint32_t)(i * kBM * 4));
-          if (EPI == kEpiGlu)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] += ld_cluster(at + (uint32_t)((tn + i) * kBM * 4));
-        }
+        float v[8], w[8];
+        sum_parts(st + (uint32_t)(8 * u * kBM * 4), parts, v);
+        if (EPI == kEpiGlu) sum_parts(st + (uint32_t)((tn + 8 * u) * kBM * 4), parts, w);
         finish8<EPI>(g, p, tl.m, row, n0 + 8 * u, v, w);
       }
     }
