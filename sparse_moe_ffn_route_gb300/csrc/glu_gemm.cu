@@ -26,8 +26,9 @@
 // of few rows.
 //
 // SPLIT: when the tiles are too few for the SMs (few tokens), the 2, 4 or 8 CTAs of a
-// cluster take consecutive parts of one tile's k; each leaves its partial tile in shared
-// memory, and each adds up and finishes its share of the columns over the CTAs, in order.
+// cluster take consecutive parts of one tile's k.  Each CTA finishes a share of the columns:
+// the others write their partial sums of these into its shared memory, and it adds them up
+// in order (reading them from the others instead cost up to 5 us of round trips).
 //
 // Warp roles of the persistent CTA: warp 0 TMA producer; warp 1 owner of TMEM and, in the
 // first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
@@ -358,30 +359,12 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Not volatile: loads of several CTAs' shared memory go out together.
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// sum over the `parts` CTAs of the cluster, in order, of 8 columns of a partial tile at
-// `at`: the loads of two CTAs at a time are in flight together.
-__device__ __forceinline__ void sum_parts(uint32_t at, int parts, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  for (int r = 0; r < parts; r += 2) {   // parts is even
-    float a[8], b[8];
-    const uint32_t pa = in_cta(at, (uint32_t)r), pb = in_cta(at, (uint32_t)r + 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i] = ld_cluster(pa + (uint32_t)(i * kBM * 4));
-      b[i] = ld_cluster(pb + (uint32_t)(i * kBM * 4));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (v[i] + a[i]) + b[i];
-  }
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
@@ -475,6 +458,8 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   tc::tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();   // the peer's barriers and TMEM are ready
+  if (SPLIT) cluster_arrive();   // this CTA runs: the others may write to it
+  bool all_run = false;
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   // Each role waits for the kernel before this one only where it first touches global
@@ -671,14 +656,25 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       if (SPLIT) {
-        // the partial tile, over the ring: [column][row]
-        float* st = reinterpret_cast<float*>(smem) + row;
-        for (int c0 = 16 * par; c0 < p.tn; c0 += 32) {
-          float v[16];
-          tc::tmem_ld16(taddr + (uint32_t)c0, v);
+        // every 8 columns to the CTA that finishes them: [its share][part][8 (pair: 16)][row]
+        cluster_wait();
+        all_run = true;
+        const uint32_t ex = tc::smem_u32(smem) + (uint32_t)(kStages * kStageBytes + 4 * row);
+        const int shares = tn / 8, each = EPI == kEpiGlu ? 16 : 8;
+        if (m - lane < p.M)   // of a row block past the last row nothing is needed
+          for (int c0 = 16 * par; c0 < p.tn; c0 += 32) {
+            float v[16];
+            tc::tmem_ld16(taddr + (uint32_t)c0, v);
+            const int up = EPI == kEpiGlu && c0 >= tn, c = up ? c0 - tn : c0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) st[(c0 + i) * kBM] = v[i];
-        }
+            for (int k = 0; k < 2; ++k) {
+              const int u = c / 8 + k, owner = ((u + 1) * parts - 1) / shares, nth_of = u - shares * owner / parts;
+              const uint32_t to =
+                  in_cta(ex + (uint32_t)(((nth_of * parts + part) * each + 8 * up) * kBM * 4), (uint32_t)owner);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) st_cluster(to + (uint32_t)(i * kBM * 4), v[8 * k + i]);
+            }
+          }
       } else if (EPI == kEpiGlu) {
         const size_t blk = ((size_t)mb * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
         for (int c0 = 16 * par; c0 < cols; c0 += 32) {
@@ -774,19 +770,26 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   }
 
   if (SPLIT) {
-    cluster_sync();   // every part lies in its CTA's shared memory
+    if (!all_run) cluster_wait();
+    cluster_sync();   // every part has arrived
     if (warp >= 2 && warp < 2 + kEpiWarps) {
       const int q = warp & 3, par = (warp - 2) >> 2, row = 32 * q + lane;
       const Tile tl = tile_at(g, unit);
       const Problem& p = g.p[tl.pi];
-      const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn;
-      const uint32_t st = tc::smem_u32(smem) + 4u * (uint32_t)row;
-      const int u0 = tn / 8 * part / parts, u1 = tn / 8 * (part + 1) / parts;   // its 8-column shares
+      const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn, shares = tn / 8, each = EPI == kEpiGlu ? 16 : 8;
+      const float* ex = reinterpret_cast<const float*>(smem + kStages * kStageBytes) + row;
+      const int u0 = shares * part / parts, u1 = shares * (part + 1) / parts;
       for (int u = u0 + par; u < u1; u += 2) {
-        if (n0 + 8 * u >= p.N) break;
-        float v[8], w[8];
-        sum_parts(st + (uint32_t)(8 * u * kBM * 4), parts, v);
-        if (EPI == kEpiGlu) sum_parts(st + (uint32_t)((tn + 8 * u) * kBM * 4), parts, w);
+        if (n0 + 8 * u >= p.N || tl.m * kBM + 32 * q >= p.M) break;
+        float v[8] = {}, w[8] = {};
+        for (int r = 0; r < parts; ++r) {
+          const float* x = ex + ((u - u0) * parts + r) * each * kBM;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] += x[i * kBM];
+            if (EPI == kEpiGlu) w[i] += x[(8 + i) * kBM];
+          }
+        }
         finish8<EPI>(g, p, tl.m, row, n0 + 8 * u, v, w);
       }
     }
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   pdl_trigger();
   tc::tc_fence_before();
   __syncthreads();
-  if (CG == 2 || SPLIT) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
+  if (CG == 2) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
   tc::tc_fence_after();
   if (warp == 1) tmem_dealloc<CG>(tmem);
 }
@@ -932,7 +935,8 @@ Way pick_way(int M, int N, int chunks, int per) {
   for (int cg = 1; cg <= 2; ++cg)
     for (int tn = 256; tn >= 32; tn -= 32) consider(cg, 1, tn);
   for (int parts = 2; parts <= 8 && parts <= chunks; parts <<= 1)
-    for (int tn = 256; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(1, parts, tn);
+    // up to 128 columns: the exchange's space leaves the ring three stages at least
+    for (int tn = 128; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(1, parts, tn);
   return best;
 }
 
@@ -990,7 +994,8 @@ cudaError_t launch(GemmParams& g, const Way& w, cudaStream_t s) {
   g.stage_bytes = 0;
   for (int i = 0; i < g.n_problems; ++i) g.stage_bytes = std::max(g.stage_bytes, stage_bytes(w.cg, g.p[i].tn, g.p[i].b_mn));
   g.stage_bytes = (g.stage_bytes + 1023) / 1024 * 1024;
-  g.stages = stages_for(g.stage_bytes, Lay<EPI>::kStageSpace);
+  // a split tile's exchange takes the partial sums of 128 rows x its columns
+  g.stages = stages_for(g.stage_bytes, Lay<EPI>::kStageSpace - (w.parts > 1 ? kBM * w.tn * 4 : 0));
   list_tiles(g, w.cg);
   if (w.parts > 1) return launch_as<1, EPI, true>(g, w, s);
   return w.cg == 2 ? launch_as<2, EPI, false>(g, w, s) : launch_as<1, EPI, false>(g, w, s);
