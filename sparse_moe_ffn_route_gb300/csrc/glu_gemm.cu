@@ -33,9 +33,11 @@
 // Warp roles of the persistent CTA: warp 0 TMA producer; warp 1 owner of TMEM and, in the
 // first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
 // epilogue runs under the next tile's MMAs); warps 2..9 epilogue, two per TMEM lane
-// quarter on alternate column chunks; dact: warp 10 copies the saved g and u of the
-// coming chunks into a shared-memory ring, since their latency would otherwise be paid
-// at every chunk.  Every wait is bounded (see tc::mbar_wait).
+// quarter on alternate column chunks; warp 10 works out the coming tiles (list, divisions,
+// cold reads of the constant bank: about 1700 clocks, in which the producer issued nothing
+// and the MMAs ran dry) and leaves them in a ring for warps 0 and 1; dact: warp 11 copies
+// the saved g and u of the coming chunks into a shared-memory ring, since their latency
+// would otherwise be paid at every chunk.  Every wait is bounded (see tc::mbar_wait).
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,6 +61,7 @@ constexpr int kEpiWarps = 8;
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
 
 constexpr int kMaxStages = 10;
+constexpr int kInfos = 4;   // tiles worked out ahead
 
 // Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA, as many as the
 // launch's widest tile has, so that narrow tiles get more stages), then, for dact, kSlots
@@ -70,7 +73,7 @@ struct Lay {
   static constexpr int kSlotBytes = 2 * 128 * 16 * 4;
   static constexpr int kStageSpace = 225 * 1024 - kSlots * kSlotBytes;
   static constexpr int kSmemBytes = kStageSpace + kSlots * kSlotBytes + 1024;
-  static constexpr int kThreads = 32 * (2 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
+  static constexpr int kThreads = 32 * (3 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
 };
 
 // One product: D [M, N] over `segs` runs of `nkc` chunks of 64 k.  Run s multiplies
@@ -131,6 +134,16 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& g, int t) {
   tl.m = m0 + (r - tl.n * rows);
   return tl;
 }
+
+// What the producer and the MMA issuer of a CTA need to know of a tile.
+struct alignas(16) TileInfo {
+  const CUtensorMap *a[2], *b[2];   // of either run of k (pair, CG 1: b of gate, of up)
+  int m0, n0;                       // first row of A, of B
+  int nkc, from, to;                // chunks of a run; those to take, over both runs (to 0: no tile is left)
+  int half, boxes;                  // rows of gate, of up; boxes of an MN-major B
+  uint32_t bytes, idesc;
+  int a_mn, b_mn, a_blocks, b_blocks, two_b;
+};
 
 // The i-th tile of a unit, or -1.
 __device__ __forceinline__ int nth_tile(const GemmParams& g, int unit, int units, int i) {
@@ -428,6 +441,8 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   uint8_t* smem = tc::smem_align1024(smem_raw);
   __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t sfull_bar[L::kRing], sempty_bar[L::kRing];
+  __shared__ __align__(8) uint64_t ifull_bar[kInfos], iempty_bar[kInfos];
+  __shared__ TileInfo infos[kInfos];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
 
@@ -449,6 +464,10 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     for (int s = 0; s < L::kSlots; ++s) {
       tc::mbar_init(tc::smem_u32(&sfull_bar[s]), 1);
       tc::mbar_init(tc::smem_u32(&sempty_bar[s]), kEpiWarps / 2);
+    }
+    for (int i = 0; i < kInfos; ++i) {
+      tc::mbar_init(tc::smem_u32(&ifull_bar[i]), 1);
+      tc::mbar_init(tc::smem_u32(&iempty_bar[i]), rank == 0 ? 2 : 1);   // the producer and the issuer
     }
     tc::mbar_init(tc::smem_u32(&drain_bar), 1);
     abort_s = 0;
@@ -475,29 +494,22 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       uint32_t ph = 0;
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
       const uint32_t lead0 = CG == 2 ? in_leader(full0) : full0, stage0 = tc::smem_u32(smem);
-      for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
-        const Tile tl = tile_at(g, t);
-        const Problem& p = g.p[tl.pi];
-        const int m0 = (tl.m * CG + rank) * kBM;
-        const bool a_mn = p.a_mn, b_mn = p.b_mn, two_b = CG == 1 && p.pair;
-        const bool a_blocks = p.a_blocks, b_blocks = p.b_blocks;
-        const int half = p.tn >> 1;                          // pair: rows of gate, of up
-        const int brows = p.tn / CG;                         // rows of B in this CTA
-        const int n0 = p.pair ? tl.n * half : tl.n * p.tn + rank * brows;
-        const int boxes = b_mn ? (brows + 63) / 64 : 0;      // MN-major boxes of 64 columns
-        const uint32_t bytes = CG * ((uint32_t)kTileA + (b_mn ? (uint32_t)boxes * 8192u : (uint32_t)brows * 128u));
-        const int nkc = p.nkc, segs = p.segs;
-        bool ok = true;
+      for (int nth = 0; !*abort; ++nth) {
+        if (!tc::mbar_wait(tc::smem_u32(&ifull_bar[nth % kInfos]), (nth / kInfos) & 1, abort, g.status)) break;
+        const TileInfo in = infos[nth % kInfos];
+        tc::mbar_arrive(tc::smem_u32(&iempty_bar[nth % kInfos]));
         if (nth == 0) {
           pdl_wait();
           if (g.clear_status && blockIdx.x == 0) *g.status = 0u;
         }
-        const int from = nkc * segs * part / parts, to = nkc * segs * (part + 1) / parts;   // SPLIT: of its chunks
-        for (int seg = 0; seg < segs && ok; ++seg) {
-          const CUtensorMap* ma = &p.a[seg];
-          const CUtensorMap* mb = p.pair ? &p.b[CG == 2 ? rank : 0] : &p.b[seg];
-          const CUtensorMap* mb1 = &p.b[1];
-          const int c0 = max(from - seg * nkc, 0), c1 = min(to - seg * nkc, nkc);
+        if (in.to == 0) break;
+        const bool a_mn = in.a_mn, b_mn = in.b_mn, a_blocks = in.a_blocks, b_blocks = in.b_blocks, two_b = in.two_b;
+        const int m0 = in.m0, n0 = in.n0, half = in.half, boxes = in.boxes;
+        const uint32_t bytes = in.bytes;
+        bool ok = true;
+        for (int seg = 0; seg < 2 && ok; ++seg) {
+          const CUtensorMap *ma = seg ? in.a[1] : in.a[0], *mb = seg ? in.b[1] : in.b[0], *mb1 = in.b[1];
+          const int c0 = max(in.from - seg * in.nkc, 0), c1 = min(in.to - seg * in.nkc, in.nkc);
           for (int c = c0, k0 = c0 * kBK; c < c1; ++c, k0 += kBK) {
             if (!tc::mbar_wait(empty0 + 8u * s, ph ^ 1, abort, g.status)) {
               ok = false;
@@ -550,11 +562,14 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       bool any = false;
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
       const uint32_t stage0 = tc::smem_u32(smem);
-      for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
-        const Tile tl = tile_at(g, t);
-        const Problem& p = g.p[tl.pi];
-        const bool a_mn = p.a_mn, b_mn = p.b_mn;
-        const uint32_t idesc = tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+      for (int nth = 0; !*abort; ++nth) {
+        if (!tc::mbar_wait(tc::smem_u32(&ifull_bar[nth % kInfos]), (nth / kInfos) & 1, abort, g.status)) break;
+        const TileInfo& in = infos[nth % kInfos];
+        const bool a_mn = in.a_mn, b_mn = in.b_mn;
+        const uint32_t idesc = in.idesc;
+        const int chunks = in.to - in.from;
+        tc::mbar_arrive(tc::smem_u32(&iempty_bar[nth % kInfos]));
+        if (chunks == 0) break;
         const uint32_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;   // 16 k, in 16-byte units
         const uint64_t ad0 = a_mn ? sdesc_mn_sw128(stage0) : tc::sdesc_sw128(stage0);
         const uint64_t bd0 = b_mn ? sdesc_mn_sw128(stage0 + kTileA) : tc::sdesc_sw128(stage0 + kTileA);
@@ -562,7 +577,6 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         tc::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)b * 256u;
         bool ok = true;
-        const int all = p.nkc * p.segs, chunks = all * (part + 1) / parts - all * part / parts;
         for (int c = 0; c < chunks; ++c) {
           if (!tc::mbar_wait(full0 + 8u * s, ph, abort, g.status)) {
             ok = false;
@@ -594,7 +608,43 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         tc::mbar_wait(tc::smem_u32(&drain_bar), 0, never, g.status);
       }
     }
-  } else if (EPI == kEpiDact && warp == 2 + kEpiWarps) {
+  } else if (warp == 2 + kEpiWarps) {
+    // ---------------------------------------------------------------- the coming tiles
+    if (tc::elect_one()) {
+      for (int nth = 0, t = 0; t >= 0 && !*abort; ++nth) {
+        t = nth_tile(g, unit, units, nth);
+        TileInfo in;
+        in.to = in.from = 0;
+        if (t >= 0) {
+          const Tile tl = tile_at(g, t);
+          const Problem& p = g.p[tl.pi];
+          const int brows = p.tn / CG;   // rows of B in this CTA
+          for (int i = 0; i < 2; ++i) {
+            in.a[i] = &p.a[i];
+            in.b[i] = &p.b[p.pair && CG == 2 ? rank : i];   // a pair of CTAs: one takes gate, one up
+          }
+          in.half = p.tn >> 1;
+          in.m0 = (tl.m * CG + rank) * kBM;
+          in.n0 = p.pair ? tl.n * in.half : tl.n * p.tn + rank * brows;
+          in.a_mn = p.a_mn;
+          in.b_mn = p.b_mn;
+          in.a_blocks = p.a_blocks;
+          in.b_blocks = p.b_blocks;
+          in.two_b = CG == 1 && p.pair;
+          in.boxes = in.b_mn ? (brows + 63) / 64 : 0;
+          in.bytes = CG * ((uint32_t)kTileA + (in.b_mn ? (uint32_t)in.boxes * 8192u : (uint32_t)brows * 128u));
+          in.idesc = tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)in.a_mn << 15) | ((uint32_t)in.b_mn << 16);
+          in.nkc = p.nkc;
+          const int all = p.nkc * p.segs;
+          in.from = all * part / parts;
+          in.to = all * (part + 1) / parts;
+        }
+        if (!tc::mbar_wait(tc::smem_u32(&iempty_bar[nth % kInfos]), (nth / kInfos & 1) ^ 1, abort, g.status)) break;
+        infos[nth % kInfos] = in;
+        tc::mbar_arrive(tc::smem_u32(&ifull_bar[nth % kInfos]));
+      }
+    }
+  } else if (EPI == kEpiDact && warp == 3 + kEpiWarps) {
     // ---------------------------------------------------------------- saved g, u
     // 16 columns of the CTA's 128 rows are 8 KiB of g and 8 KiB of u, contiguous each.
     if (!SPLIT && tc::elect_one()) {
