@@ -44,14 +44,20 @@ cudaError_t launch_glu_gate_up(const GluParams& p, const uint16_t* x, int T, uin
 // y = h Wd^T
 cudaError_t launch_glu_down(const GluParams& p, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
                             cudaStream_t s);
-// dg, du [T, ff] from dy and the saved g and u; and dWd, if dwd is non-null and the launch
-// can take it along (*with_down)
-cudaError_t launch_glu_dact(const GluParams& p, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint16_t* dwd, bool* with_down, uint32_t* status, cudaStream_t s);
-// dx, dWg, dWu, dWd, each where its pointer is non-null
-cudaError_t launch_glu_grads(const GluParams& p, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
-                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
-                             uint16_t* dwd, uint32_t* status, cudaStream_t s);
+// Room for the weight gradients' products whose k (the tokens) several units share:
+// glu_split_tiles(d, ff, T) x 256 KiB of partial sums (none for long weights or few tokens),
+// and the counts of the parts that are there.
+int glu_split_tiles(int d, int ff, int T);
+constexpr size_t kGluSplitBytes = 256 * 256 * 4, kGluArrivedBytes = 152 * 16 * 4;
+struct GluSplit {
+  float* partial;
+  uint32_t* arrived;
+};
+// dg, du [T, ff] (scratch) from dy and the saved g and u; then dx, dWg, dWu, dWd, each where
+// its pointer is non-null
+cudaError_t launch_glu_backward(const GluParams& p, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
+                                uint16_t* dg, uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint16_t* dwd,
+                                const GluSplit& split, uint32_t* status, cudaStream_t s);
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold);
 
 // Few tokens (skinny.cu): the weights stream through warp MMAs, every 16 tokens.

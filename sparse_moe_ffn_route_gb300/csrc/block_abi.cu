@@ -40,9 +40,10 @@ int check_glu(const moe_glu_cfg_t* c) {
   return c->d_model % 8 || c->ff % 8 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// Workspace: status word | h [T, ff] (forward that keeps nothing) or dg, du [T, ff].
+// Workspace: status word | h [T, ff] (forward that keeps nothing) or dg, du [T, ff] | the
+// backward pass's counts and partial sums of split products.
 struct GluLayout {
-  size_t status, h, dg, du, total;
+  size_t status, h, dg, du, arrived, partial, total;
 };
 
 GluLayout glu_layout(const moe_glu_cfg_t& c, int T) {
@@ -51,7 +52,10 @@ GluLayout glu_layout(const moe_glu_cfg_t& c, int T) {
   L.status = 0;
   L.h = L.dg = 256;
   L.du = L.dg + a;
-  L.total = L.du + a;
+  L.arrived = L.du + a;
+  const size_t split = (size_t)glu_split_tiles(c.d_model, c.ff, T);
+  L.partial = L.arrived + (split ? align_up(kGluArrivedBytes) : 0);
+  L.total = L.partial + split * kGluSplitBytes;
   return L;
 }
 
@@ -173,12 +177,10 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
   uint16_t* du = reinterpret_cast<uint16_t*>(base + L.du);
   const GluSaved sv = saved_at(const_cast<void*>(saved), saved_layout(*cfg, T));
   const uint16_t* dyi = static_cast<const uint16_t*>(dy);
-  bool with_down = false;
-  uint16_t* dwd = static_cast<uint16_t*>(dw.down);
-  BLOCK_CUDA(launch_glu_dact(p, dyi, T, sv, dg, du, dwd, &with_down, status, s));
-  BLOCK_CUDA(launch_glu_grads(p, static_cast<const uint16_t*>(x), dyi, T, sv, dg, du, static_cast<uint16_t*>(dx),
-                              static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up),
-                              with_down ? nullptr : dwd, status, s));
+  const GluSplit split{reinterpret_cast<float*>(base + L.partial), reinterpret_cast<uint32_t*>(base + L.arrived)};
+  BLOCK_CUDA(launch_glu_backward(p, static_cast<const uint16_t*>(x), dyi, T, sv, dg, du, static_cast<uint16_t*>(dx),
+                                 static_cast<uint16_t*>(dw.gate), static_cast<uint16_t*>(dw.up),
+                                 static_cast<uint16_t*>(dw.down), split, status, s));
   return MOE_OK;
 }
 

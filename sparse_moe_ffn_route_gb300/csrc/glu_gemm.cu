@@ -87,6 +87,7 @@ struct Problem {
   int a_blocks, b_blocks;   // MN-major, 1: maps of [block of 64][k][64], one load per chunk
   int tn;               // columns of B per tile (MMA N)
   int mt, nt;           // tiles (of 128 CG rows)
+  int parts, base;      // of a tile's k, each a unit's work; tiles of the problems before it
   int wide;             // output rows and base allow 32-byte stores
   uint16_t* out;        // bf16 [M, N]
 };
@@ -100,6 +101,9 @@ struct GemmParams {
   int n_problems, tiles, listed;
   int stages, stage_bytes;   // of the ring
   uint16_t first[kMaxUnits + 1], list[kMaxListed];
+  float4* partial;      // sums of the parts of split tiles (parts > 1)
+  uint32_t* arrived;    // parts that have written theirs, per tile, CTA and epilogue warp
+  int zeros;            // kEpiDact: so many of `arrived` to clear for the launch that splits
   GluAct act;
   float *g, *u;         // saved (kEpiGlu: written when non-null; kEpiDact: read)
   uint16_t* out2;       // kEpiDact: du (out: dg)
@@ -114,18 +118,29 @@ struct GemmParams {
 
 struct Tile {
   int pi, m, n;
+  int idx, part;   // within its problem; of its k
 };
 
 // Tiles run in groups of 8 m tiles: the CTAs working at one time share a few A tiles and
 // a few B tiles through L2.
+// PARTS: some products' k may be split over units.
+template <bool PARTS>
 __device__ __forceinline__ Tile tile_at(const GemmParams& g, int t) {
   Tile tl;
   tl.pi = 0;
-  while (tl.pi + 1 < g.n_problems && t >= g.p[tl.pi].mt * g.p[tl.pi].nt) {
-    t -= g.p[tl.pi].mt * g.p[tl.pi].nt;
+  while (tl.pi + 1 < g.n_problems) {
+    const int n = g.p[tl.pi].mt * g.p[tl.pi].nt * (PARTS ? g.p[tl.pi].parts : 1);
+    if (t < n) break;
+    t -= n;
     ++tl.pi;
   }
   const Problem& p = g.p[tl.pi];
+  tl.part = 0;
+  if (PARTS && p.parts > 1) {
+    tl.part = t % p.parts;
+    t /= p.parts;
+  }
+  tl.idx = t;
   constexpr int kGroup = 8;
   const int per = kGroup * p.nt;
   const int grp = t / per, r = t - grp * per;
@@ -651,7 +666,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         TileInfo in;
         in.to = in.from = 0;
         if (t >= 0) {
-          const Tile tl = tile_at(g, t);
+          const Tile tl = tile_at<EPI == kEpiStore && !SPLIT>(g, t);
           const Problem& p = g.p[tl.pi];
           const int brows = p.tn / CG;   // rows of B in this CTA
           for (int i = 0; i < 2; ++i) {
@@ -671,8 +686,9 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           in.idesc = tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)in.a_mn << 15) | ((uint32_t)in.b_mn << 16);
           in.nkc = p.nkc;
           const int all = p.nkc * p.segs;
-          in.from = all * part / parts;
-          in.to = all * (part + 1) / parts;
+          const int pt = SPLIT ? part : tl.part, pts = SPLIT ? parts : EPI == kEpiStore ? p.parts : 1;
+          in.from = all * pt / pts;
+          in.to = all * (pt + 1) / pts;
         }
         if (!tc::mbar_wait(tc::smem_u32(&iempty_bar[nth % kInfos]), (nth / kInfos & 1) ^ 1, abort, g.status)) break;
         infos[nth % kInfos] = in;
@@ -686,7 +702,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       int slot = 0, filled = 0;
       uint32_t ph = 0;
       for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
-        const Tile tl = tile_at(g, t);
+        const Tile tl = tile_at<EPI == kEpiStore && !SPLIT>(g, t);
         const Problem& p = g.p[tl.pi];
         if (nth == 0) pdl_wait();
         if (tl.pi) continue;
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     int b = 0, sl = 0;                      // sl: dact, chunks seen (slot sl % kSlots)
     uint32_t aph = 0;
     for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
-      const Tile tl = tile_at(g, t);
+      const Tile tl = tile_at<EPI == kEpiStore && !SPLIT>(g, t);
       const Problem& p = g.p[tl.pi];
       const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * 256u;
       const int mb = tl.m * CG + rank;
@@ -737,7 +753,11 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       const int tn = p.pair ? p.tn >> 1 : p.tn;
       const int n0 = tl.n * tn, cols = min(tn, p.N - n0);
       uint16_t* orow = p.out + (size_t)m * p.N + n0;
-      if (nth == 0) pdl_wait();
+      if (nth == 0) {
+        pdl_wait();
+        if (EPI == kEpiDact && blockIdx.x == 0)
+          for (int i = threadIdx.x - 64; i < g.zeros; i += 32 * kEpiWarps) g.arrived[i] = 0u;
+      }
       if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       if (SPLIT) {
@@ -834,6 +854,55 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           }
         }
         sl += n_chunks;
+      } else if (EPI == kEpiStore && !SPLIT && p.parts > 1) {
+        // This warp's share of the part's sums, [part][CTA][columns / 4][row], goes to
+        // memory.  The warp that does so last of all parts' adds the shares up in order, so
+        // that the result does not depend on who that is, and finishes the tile.
+        const size_t each = (size_t)kBM * kMaxN / 4;
+        float4* all = g.partial + ((size_t)(p.base + tl.idx) * p.parts * CG + rank) * each + row;
+        float4* mine = all + (size_t)tl.part * CG * each;
+        for (int c0 = 32 * par; c0 < cols; c0 += 64) {
+          float v[16], w[16];
+          tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(c0 + 16), v, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mine[(c0 / 4 + i) * kBM] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            mine[(c0 / 4 + 4 + i) * kBM] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = (int)atomicAdd(g.arrived + ((p.base + tl.idx) * CG + rank) * kEpiWarps + warp - 2, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == p.parts - 1) {
+          __threadfence();
+          for (int c0 = 32 * par; c0 < cols; c0 += 64) {
+            float v[32] = {};
+            for (int r = 0; r < p.parts; r += 2) {   // two parts in flight
+              const float4* from = all + (size_t)r * CG * each + (c0 / 4) * kBM;
+              const bool two = r + 1 < p.parts;
+              float4 x[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[i] = __ldcg(from + i * kBM);
+                x[8 + i] = two ? __ldcg(from + CG * each + i * kBM) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int j = 4 * (i & 7);
+                v[j] += x[i].x;
+                v[j + 1] += x[i].y;
+                v[j + 2] += x[i].z;
+                v[j + 3] += x[i].w;
+              }
+            }
+            uint32_t z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            store_32x32(orow + c0 - (size_t)lane * p.N, p.N, z, p.M - (m - lane), cols - c0, lane);
+          }
+        }
       } else {
         for (int c0 = 32 * par; c0 < cols; c0 += 64) {
           float v[16], w[16];
@@ -859,7 +928,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     cluster_sync();   // every part has arrived
     if (warp >= 2 && warp < 2 + kEpiWarps) {
       const int q = warp & 3, par = (warp - 2) >> 2, row = 32 * q + lane;
-      const Tile tl = tile_at(g, unit);
+      const Tile tl = tile_at<false>(g, unit);
       const Problem& p = g.p[tl.pi];
       const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn, shares = tn / 8, each = EPI == kEpiGlu ? 16 : 8;
       const float* ex = reinterpret_cast<const float*>(smem + kStages * kStageBytes) + row;
@@ -999,6 +1068,10 @@ int chunk_clocks(int cg, int tn) {
   return std::max(mma, std::max(feed, wait));
 }
 
+// Split tiles of the weight gradients: at most 8 parts, and so many parts in all (two per
+// pair of SMs; the sums of all are 40 MB, which L2 holds).
+constexpr int kMaxParts = 8, kMaxSplit = 152;
+
 // The way to run one product [M, N] (per = 2: gate/up, N columns of each) alone on the GPU
 // for which
 //   waves of tiles x (chunks of a unit x clocks per chunk + a tile's fixed cost)
@@ -1025,10 +1098,17 @@ Way pick_way(int M, int N, int chunks, int per) {
   return best;
 }
 
-// Clocks of a tile: its chunks, and what its epilogue adds to the next tile's start.
-long long tile_clocks(const Problem& p, int cg) {
-  return (long long)p.nkc * p.segs * chunk_clocks(cg, p.tn) + kTileClocks;
+// Clocks of a unit's work on a tile: its chunks, and what its epilogue adds to the next
+// tile's start.  A part of a split tile writes its sums (128 KiB a CTA) and the last one reads
+// all parts' at about 60 bytes a clock: 2500 clocks a part, and as long as four of these go
+// by in memory fences and in what is late for the last (measured: a weak rule at the border,
+// 1500 x 1024 x 512 backward is 23.3 us whole and 26.2 in two parts; 16384 x 512 x 512 is
+// 161 us whole, 73 in two parts, 61 in four and 68 in six).
+constexpr int kPartClocks = 2500;
+long long tile_clocks(int chunks, int parts, int cg, int tn) {
+  return (long long)cdiv(chunks, parts) * chunk_clocks(cg, tn) + kTileClocks + (parts > 1 ? (parts + 4LL) * kPartClocks : 0);
 }
+long long tile_clocks(const Problem& p, int cg) { return tile_clocks(p.nkc * p.segs, p.parts, cg, p.tn); }
 
 // Gives the tiles of several products, the longest first, each to the unit that is done
 // first.  With more tiles than the list holds (then there are many per unit) they go round
@@ -1036,14 +1116,14 @@ long long tile_clocks(const Problem& p, int cg) {
 void list_tiles(GemmParams& g, int cg) {
   const int units = cluster_count(cg);
   g.tiles = 0;
-  for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt;
+  for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt * g.p[i].parts;
   g.listed = g.n_problems > 1 && g.tiles <= kMaxListed && units <= kMaxUnits;
   if (!g.listed) return;
   int order[kMaxProblems], start[kMaxProblems], n = 0;
   for (int i = 0; i < g.n_problems; ++i) {
     order[i] = i;
     start[i] = n;
-    n += g.p[i].mt * g.p[i].nt;
+    n += g.p[i].mt * g.p[i].nt * g.p[i].parts;
   }
   std::sort(order, order + g.n_problems, [&](int a, int b) { return tile_clocks(g.p[a], cg) > tile_clocks(g.p[b], cg); });
   // a heap of (clocks so far, unit); who took which tile
@@ -1057,7 +1137,7 @@ void list_tiles(GemmParams& g, int cg) {
   for (int i = 0; i < g.n_problems; ++i) {
     const Problem& p = g.p[order[i]];
     const long long c = tile_clocks(p, cg);
-    for (int t = 0; t < p.mt * p.nt; ++t) {
+    for (int t = 0; t < p.mt * p.nt * p.parts; ++t) {
       std::pop_heap(heap, heap + units, later);
       auto& least = heap[units - 1];
       least.first += c;
@@ -1071,7 +1151,7 @@ void list_tiles(GemmParams& g, int cg) {
   uint16_t at[kMaxUnits];
   std::copy(g.first, g.first + units, at);
   for (int i = 0; i < g.n_problems; ++i)   // a unit's tiles in the order it took them
-    for (int t = start[order[i]], e = t + g.p[order[i]].mt * g.p[order[i]].nt; t < e; ++t) g.list[at[taken_by[t]]++] = (uint16_t)t;
+    for (int t = start[order[i]], e = t + g.p[order[i]].mt * g.p[order[i]].nt * g.p[order[i]].parts; t < e; ++t) g.list[at[taken_by[t]]++] = (uint16_t)t;
 }
 
 template <int EPI>
@@ -1095,6 +1175,7 @@ bool set_problem(Problem& p, int cg, int tn, int M, int N, int K, const uint16_t
   p.nkc = cdiv(K, kBK);
   p.segs = a1 ? 2 : 1;
   p.pair = 0;
+  p.parts = 1;
   p.a_mn = a_mn;
   p.b_mn = b_mn;
   p.mt = cdiv(M, kBM * cg);
@@ -1133,6 +1214,7 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   p.nkc = cdiv(w.d, kBK);
   p.segs = 1;
   p.pair = 1;
+  p.parts = 1;
   const Way way = pick_way(T, w.ff, p.nkc, 2);
   p.tn = way.tn;
   p.mt = cdiv(T, kBM * way.cg);
@@ -1168,12 +1250,113 @@ cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16
   return launch<kEpiStore>(g, way, s);
 }
 
-cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const GluSaved& sv, uint16_t* dg,
-                            uint16_t* du, uint16_t* dwd, bool* with_down, uint32_t* status, cudaStream_t s) {
+namespace {
+
+// The tiles of a launch that are alike: how many, and the clocks of each.
+struct Alike {
+  int tiles;
+  long long clocks;
+};
+
+// When the last of `units` is done if the longest tiles go out first, each to the unit that
+// is free first.
+long long span(int units, Alike* a, int n) {
+  std::sort(a, a + n, [](const Alike& x, const Alike& y) { return x.clocks > y.clocks; });
+  std::pair<long long, int> level[64];   // busy until, units: in order
+  int levels = 1;
+  level[0] = {0, units};
+  for (int i = 0; i < n; ++i) {
+    int left = a[i].tiles;
+    while (left > 0) {
+      const int k = std::min(level[0].second, left);
+      const long long until = level[0].first + a[i].clocks;
+      left -= k;
+      if ((level[0].second -= k) == 0) std::copy(level + 1, level + levels--, level);
+      int at = 0;
+      while (at < levels && level[at].first < until) ++at;
+      if (at < levels && level[at].first == until) {
+        level[at].second += k;
+      } else if (levels < 64) {
+        std::copy_backward(level + at, level + levels, level + levels + 1);
+        level[at] = {until, k};
+        ++levels;
+      } else {
+        return until;   // more levels than any few kinds of tiles give
+      }
+    }
+  }
+  return level[levels - 1].first;
+}
+
+// How a backward pass is laid out: whether dWd = dy^T h, which waits for nothing that the
+// pass computes, fills up the SMs beside dg and du; dx in a launch of its own, its long sum
+// over few tiles split; and over how many units the k (tokens) of a weight gradient's tile.
+struct Backward {
+  Way dact, dx;
+  int cg, parts;
+  bool down_first, dx_alone;
+};
+
+Backward plan_backward(const GluParams& w, int T, bool dx, bool dwg, bool dwu, bool dwd) {
+  Backward b;
+  b.dact = pick_way(T, w.ff, cdiv(w.d, kBK), 1);
+  b.dx = dx ? pick_way(T, w.d, 2 * cdiv(w.ff, kBK), 1) : Way{1, 1, kMaxN};
+  b.dx_alone = dx && b.dx.parts > 1;
+  const bool with_dx = dx && !b.dx_alone;
+  b.cg = w.d > kBM && w.ff > kBM && (!with_dx || T > kBM) ? 2 : 1;
+  const int k = cdiv(T, kBK);
+  auto tiles = [&](int M, int N, int cg, int tn) { return (int)std::min<long long>((long long)cdiv(M, kBM * cg) * cdiv(N, tn), 1 << 28); };
+  long long least = -1;
+  auto consider = [&](bool down_first, int parts) {
+    Alike a[2];
+    int n = 0;
+    long long clocks = 0;
+    if (b.dact.parts == 1) {
+      a[n++] = Alike{tiles(T, w.ff, b.dact.cg, b.dact.tn), tile_clocks(cdiv(w.d, kBK), 1, b.dact.cg, b.dact.tn)};
+      if (down_first) a[n++] = Alike{tiles(w.d, w.ff, b.dact.cg, kMaxN), tile_clocks(k, 1, b.dact.cg, kMaxN)};
+      clocks = span(cluster_count(b.dact.cg), a, n);
+    }
+    const int each = tiles(w.d, w.ff, b.cg, kMaxN), products = dwg + dwu + (dwd && !down_first);
+    n = 0;
+    if (with_dx) a[n++] = Alike{tiles(T, w.d, b.cg, kMaxN), tile_clocks(2 * cdiv(w.ff, kBK), 1, b.cg, kMaxN)};
+    if (products) a[n++] = Alike{products * each * parts, tile_clocks(k, parts, b.cg, kMaxN)};
+    if (n) clocks += span(cluster_count(b.cg), a, n) + kTileClocks;   // and the launch itself
+    if (least < 0 || clocks < least) {
+      least = clocks;
+      b.down_first = down_first;
+      b.parts = parts;
+    }
+  };
+  const bool can = dwd && b.dact.parts == 1;   // a launch that splits k has no other tiles
+  // with more tiles than a list holds nothing is split: there are many per unit
+  const int most = glu_split_tiles(w.d, w.ff, T);
+  if (can) consider(true, 1);
+  if (!can) consider(false, 1);
+  if (b.cg == 2)
+    for (int parts = 2; parts <= kMaxParts && k >= 4 * parts; ++parts) {
+      const int each = tiles(w.d, w.ff, 2, kMaxN);
+      if (can && each * (dwg + dwu) * parts <= most) consider(true, parts);
+      if (each * (dwg + dwu + dwd) * parts <= most) consider(false, parts);
+    }
+  return b;
+}
+
+}  // namespace
+
+// A pair's tile of a split product is 256 x 256 fp32 sums.
+int glu_split_tiles(int d, int ff, int T) {
+  const long long tiles = 3LL * cdiv(d, 2 * kBM) * cdiv(ff, kMaxN);
+  if (T < 8 * kBK || 2 * tiles > kMaxSplit) return 0;
+  return (int)std::min<long long>(kMaxParts * tiles, kMaxSplit);
+}
+
+cudaError_t launch_glu_backward(const GluParams& w, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
+                                uint16_t* dg, uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu, uint16_t* dwd,
+                                const GluSplit& split, uint32_t* status, cudaStream_t s) {
+  const Backward b = plan_backward(w, T, dx, dwg, dwu, dwd);
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
-  const Way way = pick_way(T, w.ff, cdiv(w.d, kBK), 1);
-  if (!set_problem(g.p[g.n_problems++], way.cg, way.tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg))
+  if (!set_problem(g.p[g.n_problems++], b.dact.cg, b.dact.tn, T, w.ff, w.d, dy, nullptr, false, w.down, nullptr, true, dg))
     return cudaErrorInvalidValue;
   g.p[0].wide = g.p[0].wide && aligned32(du);
   g.act = GluAct{w.act, w.limit, w.alpha};
@@ -1182,41 +1365,43 @@ cudaError_t launch_glu_dact(const GluParams& w, const uint16_t* dy, int T, const
   g.out2 = du;
   g.status = status;
   g.clear_status = 1;
-  // dWd = dy^T h waits for nothing that this launch computes: its tiles fill up the SMs
-  // (a launch that splits k has none of its own)
-  *with_down = dwd && way.parts == 1;
-  if (*with_down &&
-      !set_problem(g.p[g.n_problems++], way.cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd))
+  g.arrived = split.arrived;
+  g.zeros = b.parts > 1 ? kMaxSplit * 2 * kEpiWarps : 0;
+  if (b.down_first &&
+      !set_problem(g.p[g.n_problems++], b.dact.cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd))
     return cudaErrorInvalidValue;
-  return launch<kEpiDact>(g, way, s);
-}
+  cudaError_t e = launch<kEpiDact>(g, b.dact, s);
+  if (e != cudaSuccess) return e;
 
-cudaError_t launch_glu_grads(const GluParams& w, const uint16_t* x, const uint16_t* dy, int T, const GluSaved& sv,
-                             const uint16_t* dg, const uint16_t* du, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
-                             uint16_t* dwd, uint32_t* status, cudaStream_t s) {
-  GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.status = status;
-  if (dx) {   // a long sum over few tiles splits it, in a launch of its own
-    const Way way = pick_way(T, w.d, 2 * cdiv(w.ff, kBK), 1);
-    if (way.parts > 1) {
-      if (!set_problem(g.p[g.n_problems++], way.cg, way.tn, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx))
-        return cudaErrorInvalidValue;
-      const cudaError_t e = launch<kEpiStore>(g, way, s);
-      if (e != cudaSuccess) return e;
-      g.n_problems = 0;
-      dx = nullptr;
-    }
+  if (b.dx_alone) {
+    if (!set_problem(g.p[g.n_problems++], b.dx.cg, b.dx.tn, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx))
+      return cudaErrorInvalidValue;
+    e = launch<kEpiStore>(g, b.dx, s);
+    if (e != cudaSuccess) return e;
+    g.n_problems = 0;
+    dx = nullptr;
   }
   bool ok = true;
-  const int cg = w.d > kBM && w.ff > kBM && (!dx || T > kBM) ? 2 : 1;
-  if (dx) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, T, w.d, w.ff, dg, du, false, w.gate, w.up, true, dx);
-  if (dwg) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, dg, nullptr, true, x, nullptr, true, dwg);
-  if (dwu) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.ff, w.d, T, du, nullptr, true, x, nullptr, true, dwu);
-  if (dwd) ok = ok && set_problem(g.p[g.n_problems++], cg, kMaxN, w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, true, dwd);
+  int base = 0;
+  auto product = [&](int M, int N, int K, const uint16_t* a0, const uint16_t* a1, bool a_mn, const uint16_t* b0,
+                     const uint16_t* b1, int parts, uint16_t* out) {
+    Problem& p = g.p[g.n_problems++];
+    ok = ok && set_problem(p, b.cg, kMaxN, M, N, K, a0, a1, a_mn, b0, b1, true, out);
+    p.parts = parts;
+    p.base = base;
+    if (parts > 1) base += p.mt * p.nt;
+  };
+  if (dx) product(T, w.d, w.ff, dg, du, false, w.gate, w.up, 1, dx);
+  if (dwg) product(w.ff, w.d, T, dg, nullptr, true, x, nullptr, b.parts, dwg);
+  if (dwu) product(w.ff, w.d, T, du, nullptr, true, x, nullptr, b.parts, dwu);
+  if (dwd && !b.down_first) product(w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, b.parts, dwd);
   if (!ok) return cudaErrorInvalidValue;
   if (!g.n_problems) return cudaSuccess;
-  return launch<kEpiStore>(g, Way{cg, 1, kMaxN}, s);
+  g.partial = reinterpret_cast<float4*>(split.partial);
+  g.arrived = split.arrived;
+  return launch<kEpiStore>(g, Way{b.cg, 1, kMaxN}, s);
 }
 
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold) { return tc::set_wait_test(polls, withhold); }
