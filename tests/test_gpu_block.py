@@ -152,6 +152,33 @@ def test_glu_backward(T, d, ff, act):
         out[name].check()
 
 
+@pytest.mark.parametrize("T,d,ff,act", [(8192, 256, 512, 0), (2060, 624, 344, 1), (2708, 632, 592, 0),
+                                        (5000, 264, 136, 1), (4100, 520, 1032, 0)])
+def test_glu_backward_of_many_tokens_on_few_weights(T, d, ff, act):
+    """Weights of few tiles: units share the tokens of a tile's gradient.  The workspace
+    starts as rubbish, is not left, and a second run gives the same bits."""
+    x, w, dy = glu_inputs(T, d, ff, act)
+    want = glu64(x, w.gate, w.up, w.down, dy, act)
+    cfg = moe.glu_cfg(d, ff, act=act)
+    saved = moe.glu_saved(cfg, T)
+    moe.moe_glu_forward(cfg, x, w, saved=saved)
+    ws = Guarded((moe.moe_glu_workspace_bytes(cfg, T),), torch.uint8)
+    first = None
+    for names in (("gate", "up", "down"), ("gate", "up", "down"), ("up",), ("down",)):
+        ws.t.fill_(0xFF)
+        grads = moe.GluGrads(*(torch.empty_like(getattr(w, n)) if n in names else None for n in ("gate", "up", "down")))
+        dx, got = moe.moe_glu_backward(cfg, x, w, saved, dy, grads=grads, ws=ws.t)
+        assert moe.moe_device_status(ws.t)[0] == moe.MOE_OK
+        close(dx, *want["dx"], "dx")
+        for n in names:
+            close(getattr(got, n), *want[n], n)
+        ws.check()
+        if len(names) == 3:
+            if first is not None:
+                assert all(torch.equal(getattr(first, n), getattr(got, n)) for n in names)
+            first = got
+
+
 @pytest.mark.parametrize("act", [moe.ACT_SWIGLU, moe.ACT_CLAMPED_GLU])
 def test_glu_gradient_against_differences(act):
     """Directional derivatives of sum(dy * FFN) by central differences in 64 bits."""
