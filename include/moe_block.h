@@ -27,7 +27,9 @@ extern "C" {
  *   g = x Wg^T;  u = x Wu^T;  h = act(g, u);  y = h Wd^T
  *   MOE_ACT_SWIGLU:       h = g sigmoid(g) u
  *   MOE_ACT_CLAMPED_GLU:  h = (clamp(u, +-limit) + 1) g' sigmoid(alpha g'), g' = min(g, limit)
- * h is rounded to bf16 between the two products (the operand type of the tensor cores). */
+ * h is rounded to bf16 between the two products (the operand type of the tensor cores);
+ * with saved NULL, at most 8 tokens and ff <= 4096, where that rounding would show beside
+ * y's own, h keeps its low half as a second bf16. */
 typedef struct {
   int32_t d_model;     /* d, a positive multiple of 8 */
   int32_t ff;          /* hidden width, a positive multiple of 8 */
@@ -70,8 +72,10 @@ int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const mo
  *   one-sided derivative 1 at the border itself);
  *   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dWd = dy^T h.
  * dh stays in fp32; dg and du are rounded to bf16 for the products that follow.
- * dx [T, d] bf16 or NULL; grads or any member of it NULL: not computed.  Gradients are
- * written, not added to.  T == 0 sets the weight gradients to zero. */
+ * dx [T, d] bf16 or NULL; grads or any member of it NULL: not computed.  With many tokens
+ * and few weights the sum over the tokens is cut into parts, and which cut is taken depends
+ * on the outputs asked for (their last bits may, with it).  Gradients are written, not
+ * added to.  T == 0 sets the weight gradients to zero. */
 int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const moe_glu_weights_t* w,
                      const void* saved, size_t saved_bytes, const void* dy, void* dx,
                      const moe_glu_grads_t* grads, void* ws, size_t ws_bytes, void* stream);
