@@ -30,12 +30,12 @@
 // the others write their partial sums of these into its shared memory, and it adds them up
 // in order (reading them from the others instead cost up to 5 us of round trips).
 //
-// Warp roles of the persistent CTA: warp 0 TMA producer; warp 1 owner of TMEM and, in the
+// Warp roles of the persistent CTA: warps 0 and 11 TMA producers; warp 1 owner of TMEM and, in the
 // first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
 // epilogue runs under the next tile's MMAs); warps 2..9 epilogue, two per TMEM lane
 // quarter on alternate column chunks; warp 10 works out the coming tiles (list, divisions,
-// cold reads of the constant bank: about 1700 clocks, in which the producer issued nothing
-// and the MMAs ran dry) and leaves them in a ring for warps 0 and 1; dact: warp 11 copies
+// cold reads of the constant bank: about 1700 clocks, in which the producers issued nothing
+// and the MMAs ran dry) and leaves them in a ring for warps 0, 1 and 11; dact: warp 12 copies
 // the saved g and u of the coming chunks into a shared-memory ring, since their latency
 // would otherwise be paid at every chunk.  Every wait is bounded (see tc::mbar_wait).
 #include <cuda.h>
@@ -55,7 +55,7 @@ namespace {
 constexpr int kBM = 128, kBK = 64, kMaxN = 256;
 constexpr int kTileA = kBM * kBK * 2;
 constexpr int kMaxProblems = 4;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8, kProducer1 = 3 + kEpiWarps;
 
 // The epilogue of a launch's first product (any others: kEpiStore).
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
@@ -73,7 +73,7 @@ struct Lay {
   static constexpr int kSlotBytes = 2 * 128 * 16 * 4;
   static constexpr int kStageSpace = 225 * 1024 - kSlots * kSlotBytes;
   static constexpr int kSmemBytes = kStageSpace + kSlots * kSlotBytes + 1024;
-  static constexpr int kThreads = 32 * (3 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
+  static constexpr int kThreads = 32 * (4 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
 };
 
 // One product: D [M, N] over `segs` runs of `nkc` chunks of 64 k.  Run s multiplies
@@ -271,6 +271,16 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Whether phase `parity` of `bar` is over, without waiting.
+__device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return done != 0;
 }
 
 template <int CG>
@@ -517,7 +527,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     }
     for (int i = 0; i < kInfos; ++i) {
       tc::mbar_init(tc::smem_u32(&ifull_bar[i]), 1);
-      tc::mbar_init(tc::smem_u32(&iempty_bar[i]), rank == 0 ? 2 : 1);   // the producer and the issuer
+      tc::mbar_init(tc::smem_u32(&iempty_bar[i]), rank == 0 ? 3 : 2);   // the producers and the issuer
     }
     tc::mbar_init(tc::smem_u32(&drain_bar), 1);
     abort_s = 0;
@@ -535,11 +545,15 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   // memory: the barriers, TMEM and the first tile's parameters (cold reads of the constant
   // bank: about 1 us) are then ready.
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    // Everything that a chunk needs is in registers: with the parameters read per chunk
-    // this thread took 527 clocks a chunk and the MMAs (512) waited for it.
+  if (warp == 0 || warp == kProducer1) {
+    // ---------------------------------------------------------------- TMA producers
+    // A thread takes about 390 clocks for a chunk's loads and barriers, although all that it
+    // needs is in registers and it asks for its next stage before the loads go out: less
+    // than the MMAs of a 256-column tile (512), more than those of a narrow one.  So two
+    // take the chunks in turn.
     if (tc::elect_one()) {
+      const int me = warp == 0 ? 0 : 1;
+      bool free = true;   // this producer's next stage is
       int s = 0, issued = 0, withheld = tc::withheld_load(0, blockIdx.x == 0) ? 0 : -1;
       uint32_t ph = 0;
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         tc::mbar_arrive(tc::smem_u32(&iempty_bar[nth % kInfos]));
         if (nth == 0) {
           pdl_wait();
-          if (g.clear_status && blockIdx.x == 0) *g.status = 0u;
+          if (g.clear_status && blockIdx.x == 0 && me == 0) *g.status = 0u;
         }
         if (in.to == 0) break;
         const bool a_mn = in.a_mn, b_mn = in.b_mn, a_blocks = in.a_blocks, b_blocks = in.b_blocks, two_b = in.two_b;
@@ -561,35 +575,40 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           const CUtensorMap *ma = seg ? in.a[1] : in.a[0], *mb = seg ? in.b[1] : in.b[0], *mb1 = in.b[1];
           const int c0 = max(in.from - seg * in.nkc, 0), c1 = min(in.to - seg * in.nkc, in.nkc);
           for (int c = c0, k0 = c0 * kBK; c < c1; ++c, k0 += kBK) {
-            if (!tc::mbar_wait(empty0 + 8u * s, ph ^ 1, abort, g.status)) {
-              ok = false;
-              break;
-            }
-            if (issued != withheld) {
+            if ((issued & 1) == me) {
+              if (!free && !tc::mbar_wait(empty0 + 8u * s, ph ^ 1, abort, g.status)) {
+                ok = false;
+                break;
+              }
               const uint32_t fb = lead0 + 8u * s, sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + kTileA;
-              if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8u * s, bytes);   // the peer's loads count here too
-              if (a_blocks) {
-                load_blocks<CG>(sa, ma, k0, m0 >> 6, fb);
-              } else if (a_mn) {
-                load_tile<CG>(sa, ma, m0, k0, fb);
-                load_tile<CG>(sa + 8192, ma, m0 + 64, k0, fb);
-              } else {
-                load_tile<CG>(sa, ma, k0, m0, fb);
-              }
-              if (b_blocks) {
-                load_blocks<CG>(sb, mb, k0, n0 >> 6, fb);
-              } else if (b_mn) {
-                for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, mb, n0 + 64 * j, k0, fb);
-              } else {
-                load_tile<CG>(sb, mb, k0, n0, fb);
-                if (two_b) load_tile<CG>(sb + (uint32_t)half * 128u, mb1, k0, n0, fb);
+              const bool now = issued != withheld;
+              if (now && rank == 0) tc::mbar_arrive_expect_tx(full0 + 8u * s, bytes);   // the peer's loads count here too
+              const bool wraps = s + 2 >= kStages;
+              free = mbar_over(empty0 + 8u * (wraps ? s + 2 - kStages : s + 2), ph ^ (wraps ? 0 : 1));
+              if (now) {
+                if (a_blocks) {
+                  load_blocks<CG>(sa, ma, k0, m0 >> 6, fb);
+                } else if (a_mn) {
+                  load_tile<CG>(sa, ma, m0, k0, fb);
+                  load_tile<CG>(sa + 8192, ma, m0 + 64, k0, fb);
+                } else {
+                  load_tile<CG>(sa, ma, k0, m0, fb);
+                }
+                if (b_blocks) {
+                  load_blocks<CG>(sb, mb, k0, n0 >> 6, fb);
+                } else if (b_mn) {
+                  for (int j = 0; j < boxes; ++j) load_tile<CG>(sb + 8192u * j, mb, n0 + 64 * j, k0, fb);
+                } else {
+                  load_tile<CG>(sb, mb, k0, n0, fb);
+                  if (two_b) load_tile<CG>(sb + (uint32_t)half * 128u, mb1, k0, n0, fb);
+                }
               }
             }
-            ++issued;
             if (++s == kStages) {
               s = 0;
               ph ^= 1;
             }
+            ++issued;
           }
         }
         if (!ok) break;
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         int zero = 0;
         volatile int* never = &zero;
         for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          if (i != withheld) tc::mbar_wait(full0 + 8u * (i % kStages), (i / kStages) & 1, never, g.status);
+          if ((i & 1) == me && i != withheld) tc::mbar_wait(full0 + 8u * (i % kStages), (i / kStages) & 1, never, g.status);
       }
     }
   } else if (warp == 1) {
@@ -609,7 +628,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     if (rank == 0 && tc::elect_one()) {
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 0;
-      bool any = false;
+      bool any = false, full = false;   // stage s is (asked for before the MMAs of the one before)
       const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
       const uint32_t stage0 = tc::smem_u32(smem);
       for (int nth = 0; !*abort; ++nth) {
@@ -628,20 +647,22 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         const uint32_t dt = tmem + (uint32_t)b * 256u;
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
-          if (!tc::mbar_wait(full0 + 8u * s, ph, abort, g.status)) {
+          if (!full && !tc::mbar_wait(full0 + 8u * s, ph, abort, g.status)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
           const uint64_t ad = ad0 + (uint32_t)s * (kStageBytes >> 4), bd = bd0 + (uint32_t)s * (kStageBytes >> 4);
-#pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) mma<CG>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
-          commit<CG>(empty0 + 8u * s);
-          any = true;
+          const uint32_t done = empty0 + 8u * s;
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
           }
+          full = mbar_over(full0 + 8u * s, ph);
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j) mma<CG>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
+          commit<CG>(done);
+          any = true;
         }
         if (!ok) break;
         commit<CG>(tc::smem_u32(&tfull_bar[b]));
@@ -695,7 +716,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         tc::mbar_arrive(tc::smem_u32(&ifull_bar[nth % kInfos]));
       }
     }
-  } else if (EPI == kEpiDact && warp == 3 + kEpiWarps) {
+  } else if (EPI == kEpiDact && warp == 4 + kEpiWarps) {
     // ---------------------------------------------------------------- saved g, u
     // 16 columns of the CTA's 128 rows are 8 KiB of g and 8 KiB of u, contiguous each.
     if (!SPLIT && tc::elect_one()) {
