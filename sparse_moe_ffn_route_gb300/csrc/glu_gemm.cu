@@ -1019,29 +1019,36 @@ cudaError_t prepare_kernel() {
   return allow_smem<glu_gemm_kernel<CG, EPI, SPLIT>>(Lay<EPI>::kSmemBytes);
 }
 
-// How many clusters of n CTAs (one CTA per SM) the GPU holds at one time.
-int cluster_count(int n) {
+// How many clusters of n = 1, 2, 4, 8 CTAs (one CTA per SM) the GPU holds at one time: [n].
+// Asked of the driver once per device.
+const int* cluster_counts() {
   static int count[64][9] = {};
-  const int sms = sm_count();
-  if (n == 1) return sms;
+  static const int one[9] = {0, 1, 1, 1, 1, 1, 1, 1, 1};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return sms / n;
-  if (count[dev][n]) return count[dev][n];
-  if (prepare_kernel<2, kEpiStore, false>() != cudaSuccess) return sms / n;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)n;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms / n * n);
-  cfg.blockDim = dim3(Lay<kEpiStore>::kThreads);
-  cfg.dynamicSmemBytes = Lay<kEpiStore>::kSmemBytes;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int c = 0;
-  if (cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore, false>, &cfg) != cudaSuccess || c < 1) c = sms / n;
-  return count[dev][n] = c;
+  if (dev < 0 || dev >= 64) return one;
+  int* of = count[dev];
+  if (of[1]) return of;
+  const int sms = sm_count();
+  const bool ready = prepare_kernel<2, kEpiStore, false>() == cudaSuccess;
+  for (int n = 2; n <= 8; n <<= 1) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / n * n);
+    cfg.blockDim = dim3(Lay<kEpiStore>::kThreads);
+    cfg.dynamicSmemBytes = Lay<kEpiStore>::kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (!ready || cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore, false>, &cfg) != cudaSuccess || c < 1)
+      c = std::max(1, sms / n);
+    of[n] = c;
+  }
+  of[1] = sms;
+  return of;
 }
 
 // How a launch runs: single CTAs or pairs (cg), or clusters of `parts` CTAs that split k.
@@ -1054,7 +1061,7 @@ cudaError_t launch_as(const GemmParams& g, const Way& w, cudaStream_t s) {
   const cudaError_t e = prepare_kernel<CG, EPI, SPLIT>();
   if (e != cudaSuccess) return e;
   const int size = CG * w.parts;   // CTAs of a unit
-  const int units = SPLIT ? g.tiles : cluster_count(size);
+  const int units = SPLIT ? g.tiles : cluster_counts()[size];
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1081,13 +1088,21 @@ int stages_for(int bytes, int space) {
 }
 
 // Clocks of one chunk of 64 k with tn columns of B: the MMAs (2 per column for the 128
-// rows of an SM), its operands' way into shared memory (about 64 bytes per clock), or a
-// load's latency (about 2400 clocks while memory is busy) over the stages in flight.
-int chunk_clocks(int cg, int tn) {
-  const int mma = 2 * tn, feed = (kTileA + tn * 128 / cg) / 64;
-  const int wait = 2400 / stages_for(stage_bytes(cg, tn, false), Lay<kEpiStore>::kStageSpace);
-  return std::max(mma, std::max(feed, wait));
+// rows of an SM, and 1 in 22 more), its operands' way into shared memory (86 bytes a clock),
+// or the MMA issuer's own 330.  Fitted to launches of one wave of tiles at k 512 to 4096, as
+// are the clocks below (one CTA at 256 columns: 307 ns a chunk, 128: 196, 32: 168; pairs:
+// 278, 183, 176).  space: shared memory for the stages, given for MN-major operands, whose
+// loads take up to 2600 clocks (one CTA at 256 columns, 4 stages: 657 a chunk).
+int chunk_clocks(int cg, int tn, int space) {
+  const int mma = 2 * tn * 23 / 22, feed = (kTileA + tn * 128 / cg) / 86;
+  const int wait = space ? 2600 / stages_for(stage_bytes(cg, tn, true), space) : 0;
+  return std::max(std::max(mma, wait), std::max(feed, 330));
 }
+
+// What a tile of tn columns adds to its chunks (its epilogue, as far as nothing hides it),
+// and what a launch of pairs costs more than one of single CTAs (1.4 us).
+int tile_fixed(int tn) { return 1000 + 8 * tn; }
+constexpr int kPairClocks = 2100, kLaunchClocks = 2500;
 
 // Split tiles of the weight gradients: at most 8 parts, and so many parts in all (two per
 // pair of SMs; the sums of all are 40 MB, which L2 holds).
@@ -1096,26 +1111,37 @@ constexpr int kMaxParts = 8, kMaxSplit = 152;
 // The way to run one product [M, N] (per = 2: gate/up, N columns of each) alone on the GPU
 // for which
 //   waves of tiles x (chunks of a unit x clocks per chunk + a tile's fixed cost)
-// is least.  A part of a split tile pays about 2500 clocks more for the exchange.
-constexpr int kTileClocks = 2500;
-Way pick_way(int M, int N, int chunks, int per) {
-  Way best{1, 1, 256};
+// is least.  A long launch (kLongClocks: 100 us) runs against the power limit, where what
+// the last wave leaves idle speeds the others up: there only the tiles count (8192 x
+// 2048 x 8192 forward with y in pairs' tiles of 256 columns, 3.4 waves: 485 us, of 192, 4.6
+// waves: 493 us).  A part of a split tile pays for the exchange (two parts of 128 columns 2.7 us,
+// of 32 columns 1.3 us).
+constexpr long long kLongClocks = 200000;
+Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = nullptr) {
+  Way best{1, 1, kMaxN};
   long long least = -1;
+  const int* const counts = cluster_counts();
   auto consider = [&](int cg, int parts, int tn) {
-    const int units = cluster_count(cg * parts);
+    const int units = counts[cg * parts];
     const long long tiles = (long long)cdiv(M, kBM * cg) * cdiv(N, tn / per);
-    const long long cost = (tiles + units - 1) / units *
-                           ((long long)cdiv(chunks, parts) * chunk_clocks(cg, tn) + kTileClocks + (parts > 1 ? 2500 : 0));
+    const int exchange = parts > 1 ? 1500 + 29 * tn + 500 * (parts - 2) : 0;
+    const long long each = (long long)cdiv(chunks, parts) * chunk_clocks(cg, tn, space) + tile_fixed(tn) + exchange;
+    long long cost = (tiles + units - 1) / units * each;
+    if (cost > kLongClocks) cost = tiles * each / units;
+    cost += cg == 2 ? kPairClocks : 0;
     if (least < 0 || cost < least) {
       least = cost;
       best = Way{cg, parts, tn};
     }
   };
   for (int cg = 1; cg <= 2; ++cg)
-    for (int tn = 256; tn >= 32; tn -= 32) consider(cg, 1, tn);
+    // boxes of 16 rows of gate and of up are too small for few tokens (16 x 1080 x 1520:
+    // 18.6 us, of 32 rows 15.6; 126 x 376 x 1216: 9.9, 10.4)
+    for (int tn = 256; tn >= 32 * per; tn -= 32) consider(cg, 1, tn);
   for (int parts = 2; parts <= 8 && parts <= chunks; parts <<= 1)
     // up to 128 columns: the exchange's space leaves the ring three stages at least
     for (int tn = 128; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(1, parts, tn);
+  if (clocks) *clocks = least;
   return best;
 }
 
@@ -1126,16 +1152,16 @@ Way pick_way(int M, int N, int chunks, int per) {
 // 1500 x 1024 x 512 backward is 23.3 us whole and 26.2 in two parts; 16384 x 512 x 512 is
 // 161 us whole, 73 in two parts, 61 in four and 68 in six).
 constexpr int kPartClocks = 2500;
-long long tile_clocks(int chunks, int parts, int cg, int tn) {
-  return (long long)cdiv(chunks, parts) * chunk_clocks(cg, tn) + kTileClocks + (parts > 1 ? (parts + 4LL) * kPartClocks : 0);
+long long tile_clocks(int chunks, int parts, int cg, int tn, int space) {
+  return (long long)cdiv(chunks, parts) * chunk_clocks(cg, tn, space) + tile_fixed(tn) + (parts > 1 ? (parts + 4LL) * kPartClocks : 0);
 }
-long long tile_clocks(const Problem& p, int cg) { return tile_clocks(p.nkc * p.segs, p.parts, cg, p.tn); }
+long long tile_clocks(const Problem& p, int cg) { return tile_clocks(p.nkc * p.segs, p.parts, cg, p.tn, Lay<kEpiStore>::kStageSpace); }
 
 // Gives the tiles of several products, the longest first, each to the unit that is done
 // first.  With more tiles than the list holds (then there are many per unit) they go round
 // in turn.
 void list_tiles(GemmParams& g, int cg) {
-  const int units = cluster_count(cg);
+  const int units = cluster_counts()[cg];
   g.tiles = 0;
   for (int i = 0; i < g.n_problems; ++i) g.tiles += g.p[i].mt * g.p[i].nt * g.p[i].parts;
   g.listed = g.n_problems > 1 && g.tiles <= kMaxListed && units <= kMaxUnits;
@@ -1236,7 +1262,7 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   p.segs = 1;
   p.pair = 1;
   p.parts = 1;
-  const Way way = pick_way(T, w.ff, p.nkc, 2);
+  const Way way = pick_way(T, w.ff, p.nkc, 2, 0);
   p.tn = way.tn;
   p.mt = cdiv(T, kBM * way.cg);
   p.nt = cdiv(w.ff, p.tn / 2);
@@ -1265,7 +1291,7 @@ cudaError_t launch_glu_down(const GluParams& w, const uint16_t* h, int T, uint16
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.n_problems = 1;
-  const Way way = pick_way(T, w.d, cdiv(w.ff, kBK), 1);
+  const Way way = pick_way(T, w.d, cdiv(w.ff, kBK), 1, 0);
   if (!set_problem(g.p[0], way.cg, way.tn, T, w.d, w.ff, h, nullptr, false, w.down, nullptr, false, y)) return cudaErrorInvalidValue;
   g.status = status;
   return launch<kEpiStore>(g, way, s);
@@ -1314,51 +1340,54 @@ long long span(int units, Alike* a, int n) {
 // over few tiles split; and over how many units the k (tokens) of a weight gradient's tile.
 struct Backward {
   Way dact, dx;
-  int cg, parts;
+  int cg, parts, tn;   // of the launch of dx and the weight gradients
   bool down_first, dx_alone;
 };
 
 Backward plan_backward(const GluParams& w, int T, bool dx, bool dwg, bool dwu, bool dwd) {
-  Backward b;
-  b.dact = pick_way(T, w.ff, cdiv(w.d, kBK), 1);
-  b.dx = dx ? pick_way(T, w.d, 2 * cdiv(w.ff, kBK), 1) : Way{1, 1, kMaxN};
-  b.dx_alone = dx && b.dx.parts > 1;
-  const bool with_dx = dx && !b.dx_alone;
-  b.cg = w.d > kBM && w.ff > kBM && (!with_dx || T > kBM) ? 2 : 1;
-  const int k = cdiv(T, kBK);
+  constexpr int kDactSpace = Lay<kEpiDact>::kStageSpace, kSpace = Lay<kEpiStore>::kStageSpace;
+  const int* const counts = cluster_counts();
+  const int k = cdiv(T, kBK), kd = cdiv(w.d, kBK), kff = cdiv(w.ff, kBK);
   auto tiles = [&](int M, int N, int cg, int tn) { return (int)std::min<long long>((long long)cdiv(M, kBM * cg) * cdiv(N, tn), 1 << 28); };
-  long long least = -1;
-  auto consider = [&](bool down_first, int parts) {
-    Alike a[2];
-    int n = 0;
-    long long clocks = 0;
-    if (b.dact.parts == 1) {
-      a[n++] = Alike{tiles(T, w.ff, b.dact.cg, b.dact.tn), tile_clocks(cdiv(w.d, kBK), 1, b.dact.cg, b.dact.tn)};
-      if (down_first) a[n++] = Alike{tiles(w.d, w.ff, b.dact.cg, kMaxN), tile_clocks(k, 1, b.dact.cg, kMaxN)};
-      clocks = span(cluster_count(b.dact.cg), a, n);
+  auto pairs = [](int cg) { return cg == 2 ? kPairClocks : 0; };
+  Alike a[2];
+  // dg and du alone, or with dWd beside them (a launch that splits k has no other tiles)
+  long long dact[2], alone_dx = 0, least = -1;
+  Way way[2];
+  way[0] = pick_way(T, w.ff, kd, 1, kDactSpace, &dact[0]);
+  dact[1] = -1;
+  for (int cg = 1; dwd && cg <= 2; ++cg)
+    for (int tn = kMaxN; tn >= 64; tn -= 32) {
+      a[0] = Alike{tiles(T, w.ff, cg, tn), tile_clocks(kd, 1, cg, tn, kDactSpace)};
+      a[1] = Alike{tiles(w.d, w.ff, cg, kMaxN), tile_clocks(k, 1, cg, kMaxN, kDactSpace)};
+      const long long clocks = span(counts[cg], a, 2) + pairs(cg);
+      if (dact[1] < 0 || clocks < dact[1]) {
+        dact[1] = clocks;
+        way[1] = Way{cg, 1, tn};
+      }
     }
-    const int each = tiles(w.d, w.ff, b.cg, kMaxN), products = dwg + dwu + (dwd && !down_first);
-    n = 0;
-    if (with_dx) a[n++] = Alike{tiles(T, w.d, b.cg, kMaxN), tile_clocks(2 * cdiv(w.ff, kBK), 1, b.cg, kMaxN)};
-    if (products) a[n++] = Alike{products * each * parts, tile_clocks(k, parts, b.cg, kMaxN)};
-    if (n) clocks += span(cluster_count(b.cg), a, n) + kTileClocks;   // and the launch itself
-    if (least < 0 || clocks < least) {
-      least = clocks;
-      b.down_first = down_first;
-      b.parts = parts;
-    }
+  Backward b{};
+  if (dx) b.dx = pick_way(T, w.d, 2 * kff, 1, kSpace, &alone_dx);
+  const int most = glu_split_tiles(w.d, w.ff, T);   // no split over more tiles: there are many per unit
+  auto consider = [&](int cg, int tn, int parts) {
+    for (int first = dwd ? 1 : 0; first >= 0; --first)
+      for (int alone = 0; alone <= (dx && b.dx.parts > 1 ? 1 : 0); ++alone) {
+        const int products = dwg + dwu + (dwd && !first), each = tiles(w.d, w.ff, cg, tn);
+        if (parts > 1 && (long long)products * each * parts > most) continue;
+        int n = 0;
+        if (dx && !alone) a[n++] = Alike{tiles(T, w.d, cg, tn), tile_clocks(2 * kff, 1, cg, tn, kSpace)};
+        if (products) a[n++] = Alike{products * each * parts, tile_clocks(k, parts, cg, tn, kSpace)};
+        long long clocks = dact[first] + (alone ? alone_dx + kLaunchClocks : 0);
+        if (n) clocks += span(counts[cg], a, n) + kLaunchClocks + pairs(cg);
+        if (least < 0 || clocks < least) {
+          least = clocks;
+          b = Backward{way[first], b.dx, cg, parts, tn, first == 1, alone == 1};
+        }
+      }
   };
-  const bool can = dwd && b.dact.parts == 1;   // a launch that splits k has no other tiles
-  // with more tiles than a list holds nothing is split: there are many per unit
-  const int most = glu_split_tiles(w.d, w.ff, T);
-  if (can) consider(true, 1);
-  if (!can) consider(false, 1);
-  if (b.cg == 2)
-    for (int parts = 2; parts <= kMaxParts && k >= 4 * parts; ++parts) {
-      const int each = tiles(w.d, w.ff, 2, kMaxN);
-      if (can && each * (dwg + dwu) * parts <= most) consider(true, parts);
-      if (each * (dwg + dwu + dwd) * parts <= most) consider(false, parts);
-    }
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int tn = kMaxN; tn >= 128; tn >>= 1) consider(cg, tn, 1);
+  for (int parts = 2; parts <= kMaxParts && k >= 4 * parts; ++parts) consider(2, kMaxN, parts);
   return b;
 }
 
@@ -1409,7 +1438,7 @@ cudaError_t launch_glu_backward(const GluParams& w, const uint16_t* x, const uin
   auto product = [&](int M, int N, int K, const uint16_t* a0, const uint16_t* a1, bool a_mn, const uint16_t* b0,
                      const uint16_t* b1, int parts, uint16_t* out) {
     Problem& p = g.p[g.n_problems++];
-    ok = ok && set_problem(p, b.cg, kMaxN, M, N, K, a0, a1, a_mn, b0, b1, true, out);
+    ok = ok && set_problem(p, b.cg, b.tn, M, N, K, a0, a1, a_mn, b0, b1, true, out);
     p.parts = parts;
     p.base = base;
     if (parts > 1) base += p.mt * p.nt;
@@ -1422,7 +1451,7 @@ cudaError_t launch_glu_backward(const GluParams& w, const uint16_t* x, const uin
   if (!g.n_problems) return cudaSuccess;
   g.partial = reinterpret_cast<float4*>(split.partial);
   g.arrived = split.arrived;
-  return launch<kEpiStore>(g, Way{b.cg, 1, kMaxN}, s);
+  return launch<kEpiStore>(g, Way{b.cg, 1, b.tn}, s);
 }
 
 cudaError_t glu_set_wait_test(uint32_t polls, int withhold) { return tc::set_wait_test(polls, withhold); }
