@@ -2,12 +2,12 @@
 // the six of its backward pass, all D[M x N] = A[M x K] . B[N x K]^T tiles with fp32
 // accumulators in TMEM, fed by TMA through an mbarrier ring.
 //
-//   gate/up:  g = x Wg^T, u = x Wu^T in one tile (the B tile holds nf rows of each), so
+//   gate/up:  g = x Wg^T, u = x Wu^T in one tile (the B tile holds tn / 2 rows of each), so
 //             that the epilogue has both and writes h = act(g, u) (and, in training, g, u)
 //   down:     y = h Wd^T
 //   dact:     dh = dy Wd, whose epilogue turns it into dg and du with the saved g and u
 //             (dh never reaches memory and is never rounded)
-//             (dWd = dy^T h rides along in that launch)
+//             (dWd = dy^T h may ride along in that launch)
 //   grads:    dx = dg Wg + du Wu (one sum over two runs of k), dWg = dg^T x and
 //             dWu = du^T x in one launch, so that the tiles of the small products fill the
 //             SMs that the large ones leave
@@ -21,17 +21,20 @@
 // CG = 2: two CTAs of a cluster share one tile of 256 rows (cta_group::2).  Each holds its
 // 128 rows of A and half of the B tile, and the accumulators of its rows; the tensor cores
 // read the other half of B from the peer.  Against CG = 1 a chunk of 64 k moves 32 KiB
-// into each SM instead of 48 KiB for the same MMAs, which is what bounds CG = 1 (the same
-// tile at 256 columns: 96 bytes per clock and SM).  CG = 1 (128-row tiles) serves outputs
-// of few rows.
+// into each SM instead of 48 KiB for the same MMAs (278 ns a chunk of 256 columns instead
+// of 307), but a launch of pairs costs 1.4 us more, so that single CTAs serve short sums
+// and few rows.
 //
 // SPLIT: when the tiles are too few for the SMs (few tokens), the 2, 4 or 8 CTAs of a
 // cluster take consecutive parts of one tile's k.  Each CTA finishes a share of the columns:
 // the others write their partial sums of these into its shared memory, and it adds them up
 // in order (reading them from the others instead cost up to 5 us of round trips).
 //
-// Warp roles of the persistent CTA: warps 0 and 11 TMA producers; warp 1 owner of TMEM and, in the
-// first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
+// parts (of a Problem): with many tokens and few weights the k of a weight gradient's tile is
+// cut into parts that are units' work like tiles; the last part to end adds the sums up.
+//
+// Warp roles of the persistent CTA: warps 0 and 11 TMA producers; warp 1 owner of TMEM and,
+// in the first CTA of a pair, MMA issuer (two accumulators of up to 256 columns, so that a tile's
 // epilogue runs under the next tile's MMAs); warps 2..9 epilogue, two per TMEM lane
 // quarter on alternate column chunks; warp 10 works out the coming tiles (list, divisions,
 // cold reads of the constant bank: about 1700 clocks, in which the producers issued nothing
