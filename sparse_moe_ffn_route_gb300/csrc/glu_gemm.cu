@@ -41,6 +41,12 @@
 // and the MMAs ran dry) and leaves them in a ring for warps 0, 1 and 11; dact: warp 12 copies
 // the saved g and u of the coming chunks into a shared-memory ring, since their latency
 // would otherwise be paid at every chunk.  Every wait is bounded (see tc::mbar_wait).
+//
+// Measured at 8192 tokens, d 2048, ff 8192 (tensor cores under the power limit; a library's
+// bf16 product reaches 1.87 PFLOP/s): gate/up 276 us (1.99 PFLOP/s; 322 with g and u kept,
+// 0.5 GB), down 162 us (1.70: 256 tiles on 76 pairs), dact 211 us, grads with dWd 707 us
+// (1.94).  At 4096, 2048, 512 the four launches take 20, 14, 19 and 33 us: one wave each,
+// bound by the first loads' latency and the open epilogue.
 #include <cuda.h>
 
 #include <algorithm>
