@@ -7,7 +7,7 @@
 
 namespace moe {
 
-// Lets KERNEL use up to `bytes` of dynamic shared memory; asked of the driver once per
+// Lets KERNEL use up to `bytes` of dynamic shared memory; asked of the runtime once per
 // device (`bytes` is the same at every call).
 template <auto KERNEL>
 cudaError_t allow_smem(int bytes) {

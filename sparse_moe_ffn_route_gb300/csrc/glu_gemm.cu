@@ -1029,7 +1029,7 @@ cudaError_t prepare_kernel() {
 }
 
 // How many clusters of n = 1, 2, 4, 8 CTAs (one CTA per SM) the GPU holds at one time: [n].
-// Asked of the driver once per device.
+// Asked of the runtime once per device.
 const int* cluster_counts() {
   static int count[64][9] = {};
   static const int one[9] = {0, 1, 1, 1, 1, 1, 1, 1, 1};
