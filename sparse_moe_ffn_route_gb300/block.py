@@ -5,12 +5,17 @@ Three operators, each with the C ABI's name: the gated FFN (``moe_glu_forward``,
 (``moe_block_norm_forward``, ``moe_block_norm_backward``) and the linear layer with 4-bit
 weights and group scales (``moe_w4_linear``).  Every function checks its tensors (device,
 type, shape, contiguity: ValueError), allocates the outputs and the workspace that are
-not passed in, and runs on the given stream or torch's current one.  Its ``bind_*`` twin
-takes the same arguments and returns a ``BoundCall``: the call with its arguments
-marshalled once, for steps repeated on the same buffers.
+not passed in, and runs on the given stream or torch's current one.  What it allocates
+belongs to the stream that it runs on, and every tensor is recorded (record_stream) on a
+stream other than the one that was current at the call, so that torch's allocator gives
+none of them away before the kernels are done with it; ordering the streams is left to the
+caller, as with any torch operation.  Its ``bind_*`` twin takes the same arguments and
+returns a ``BoundCall``: the call with its arguments marshalled once, for steps repeated on
+the same buffers.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 from typing import Optional
@@ -114,25 +119,60 @@ def _current_stream(device: torch.device) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _current_handle(device: torch.device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else _current_stream(device)
+
+
+def _stream_object(stream, device: torch.device):
+    """What a caller gives as `stream` (a torch stream, or a cudaStream_t's value) as torch's
+    object; None stays None."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _allocating_on(stream):
+    """What is allocated inside belongs to `stream` (None: the current one), where it is used:
+    memory that the current stream has freed but still works on is not handed out there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class BoundCall:
     """A library call with its arguments marshalled once.  Each call enqueues the same work
     on the same buffers (their contents are read when it runs) on the stream given to
     ``bind_*``, or, where none was given, on torch's current stream of that moment, and
-    returns the same output tensors.  The tensors stay alive as long as the object."""
+    returns the same output tensors.  The tensors stay alive as long as the object, and
+    their memory until the streams that it was called on are done with it."""
 
-    __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream")
+    __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream", "_tensors", "_seen")
 
-    def __init__(self, where, args, out, keep, device, stream):
+    def __init__(self, where, args, out, keep, tensors, device, stream):
         self._fn, self._where = getattr(_lib, where), where
-        self._args, self._out, self._keep = args, out, keep
+        self._args, self._out, self._keep = args, out, (keep, stream)
+        self._tensors = [t for t in tensors if t is not None]
         self._device = device.index if _raw_stream is not None else device
-        self._stream = None if stream is None else (
-            stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        self._stream = None if stream is None else stream.cuda_stream
+        # streams whose work the allocator knows to use the tensors: the current one owns
+        # them, or, beside one that is given, is where the caller will use the outputs
+        here = _current_handle(device)
+        self._seen = {here}
+        if stream is not None and self._stream != here:
+            self._record(self._stream, stream)
+            for t in self._tensors:
+                t.record_stream(torch.cuda.current_stream(device))
+
+    def _record(self, handle, stream):
+        for t in self._tensors:
+            t.record_stream(stream)
+        self._seen.add(handle)
 
     def __call__(self):
         stream = self._stream
         if stream is None:
             stream = (_raw_stream or _current_stream)(self._device)
+            if stream not in self._seen:
+                self._record(stream, torch.cuda.current_stream(self._device))
         status = self._fn(*self._args, stream)
         if status != MOE_OK:
             raise MoeError(status, self._where)
@@ -195,14 +235,16 @@ def _glu_weights(cfg: GluCfg, w: GluWeights) -> _Three:
 
 def bind_glu_forward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved=None, y=None, ws=None,
                      stream=None) -> BoundCall:
-    T = _rows(x, cfg.d_model)
-    y = torch.empty_like(x) if y is None else y
-    ws = glu_workspace(cfg, T, x.device) if ws is None else ws
-    _one_device(x, w.gate, w.up, w.down, saved, y, ws)
+    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    with _allocating_on(stream):
+        y = torch.empty_like(x) if y is None else y
+        ws = glu_workspace(cfg, T, x.device) if ws is None else ws
+    tensors = (x, w.gate, w.up, w.down, saved, y, ws)
+    _one_device(*tensors)
     shape, keep = (T, cfg.d_model), (cfg, x, w, saved, y, ws, _glu_weights(cfg, w))
     args = (_ref(cfg), _tensor(x, "x", shape), T, _ref(keep[-1]), _tensor(y, "y", shape),
             *_bytes(saved, "saved"), *_bytes(ws, "ws"))
-    return BoundCall("moe_glu_forward", args, y, keep, x.device, stream)
+    return BoundCall("moe_glu_forward", args, y, keep, tensors, x.device, stream)
 
 
 def moe_glu_forward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved=None, y=None, ws=None,
@@ -213,20 +255,22 @@ def moe_glu_forward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved=None, y=N
 
 def bind_glu_backward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved: torch.Tensor, dy: torch.Tensor, dx=None,
                       grads: Optional[GluGrads] = None, ws=None, need_dx: bool = True, stream=None) -> BoundCall:
-    T = _rows(x, cfg.d_model)
-    if need_dx and dx is None:
-        dx = torch.empty_like(x)
-    if grads is None:
-        grads = GluGrads(*(torch.empty_like(t) for t in (w.gate, w.up, w.down)))
-    ws = glu_workspace(cfg, T, x.device) if ws is None else ws
-    _one_device(x, w.gate, w.up, w.down, saved, dy, dx, grads.gate, grads.up, grads.down, ws)
+    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    with _allocating_on(stream):
+        if need_dx and dx is None:
+            dx = torch.empty_like(x)
+        if grads is None:
+            grads = GluGrads(*(torch.empty_like(t) for t in (w.gate, w.up, w.down)))
+        ws = glu_workspace(cfg, T, x.device) if ws is None else ws
+    tensors = (x, w.gate, w.up, w.down, saved, dy, dx, grads.gate, grads.up, grads.down, ws)
+    _one_device(*tensors)
     shape, up = (T, cfg.d_model), (cfg.ff, cfg.d_model)
     g = _Three(_tensor(grads.gate, "grads.gate", up), _tensor(grads.up, "grads.up", up),
                _tensor(grads.down, "grads.down", (cfg.d_model, cfg.ff)))
     keep = (cfg, x, w, saved, dy, dx, grads, ws, _glu_weights(cfg, w), g)
     args = (_ref(cfg), _tensor(x, "x", shape), T, _ref(keep[-2]), *_bytes(saved, "saved"),
             _tensor(dy, "dy", shape), _tensor(dx, "dx", shape), _ref(g), *_bytes(ws, "ws"))
-    return BoundCall("moe_glu_backward", args, (dx, grads), keep, x.device, stream)
+    return BoundCall("moe_glu_backward", args, (dx, grads), keep, tensors, x.device, stream)
 
 
 def moe_glu_backward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved: torch.Tensor, dy: torch.Tensor, dx=None,
@@ -257,16 +301,18 @@ def _norm_inputs(cfg: NormCfg, T: int, x, branch, post_w, gate, pre_w) -> _Five:
 
 def bind_block_norm_forward(cfg: NormCfg, x: torch.Tensor, branch=None, post_w=None, gate=None, pre_w=None, y=None,
                             a=None, stream=None) -> BoundCall:
-    T = _rows(x, cfg.d_model)
-    if branch is not None and y is None:
-        y = torch.empty_like(x)
-    if pre_w is not None and a is None:
-        a = torch.empty_like(x)
-    _one_device(x, branch, post_w, gate, pre_w, y, a)
+    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    with _allocating_on(stream):
+        if branch is not None and y is None:
+            y = torch.empty_like(x)
+        if pre_w is not None and a is None:
+            a = torch.empty_like(x)
+    tensors = (x, branch, post_w, gate, pre_w, y, a)
+    _one_device(*tensors)
     shape, keep = (T, cfg.d_model), (cfg, x, branch, post_w, gate, pre_w, y, a,
                                      _norm_inputs(cfg, T, x, branch, post_w, gate, pre_w))
     args = (_ref(cfg), _ref(keep[-1]), T, _tensor(y, "y", shape), _tensor(a, "a", shape))
-    return BoundCall("moe_block_norm_forward", args, (y, a), keep, x.device, stream)
+    return BoundCall("moe_block_norm_forward", args, (y, a), keep, tensors, x.device, stream)
 
 
 def moe_block_norm_forward(cfg: NormCfg, x: torch.Tensor, branch=None, post_w=None, gate=None, pre_w=None, y=None,
@@ -287,15 +333,20 @@ def block_norm_workspace(cfg: NormCfg, T: int, device=None) -> torch.Tensor:
 def bind_block_norm_backward(cfg: NormCfg, x: torch.Tensor, dy=None, da=None, branch=None, post_w=None, gate=None,
                              pre_w=None, grads: Optional[NormGrads] = None, ws=None, stream=None) -> BoundCall:
     T, dev = _rows(x, cfg.d_model), x.device
-    if grads is None:
-        def f32(n):
-            return torch.empty(n, dtype=torch.float32, device=dev)
-        grads = NormGrads(torch.empty_like(x), None if branch is None else torch.empty_like(x),
-                          None if gate is None else f32(T), None if post_w is None else f32(cfg.d_model),
-                          None if pre_w is None else f32(cfg.d_model))
-    ws = block_norm_workspace(cfg, T, dev) if ws is None else ws
-    _one_device(x, dy, da, branch, post_w, gate, pre_w, grads.dx, grads.dbranch, grads.dgate, grads.dpost_w,
-                grads.dpre_w, ws)
+    stream = _stream_object(stream, dev)
+
+    def f32(n):
+        return torch.empty(n, dtype=torch.float32, device=dev)
+
+    with _allocating_on(stream):
+        if grads is None:
+            grads = NormGrads(torch.empty_like(x), None if branch is None else torch.empty_like(x),
+                              None if gate is None else f32(T), None if post_w is None else f32(cfg.d_model),
+                              None if pre_w is None else f32(cfg.d_model))
+        ws = block_norm_workspace(cfg, T, dev) if ws is None else ws
+    tensors = (x, dy, da, branch, post_w, gate, pre_w, grads.dx, grads.dbranch, grads.dgate, grads.dpost_w,
+               grads.dpre_w, ws)
+    _one_device(*tensors)
     shape, d = (T, cfg.d_model), (cfg.d_model,)
     g = _Five(_tensor(grads.dx, "grads.dx", shape), _tensor(grads.dbranch, "grads.dbranch", shape),
               _tensor(grads.dgate, "grads.dgate", (T,), torch.float32),
@@ -305,7 +356,7 @@ def bind_block_norm_backward(cfg: NormCfg, x: torch.Tensor, dy=None, da=None, br
             _norm_inputs(cfg, T, x, branch, post_w, gate, pre_w), g)
     args = (_ref(cfg), _ref(keep[-2]), T, _tensor(dy, "dy", shape), _tensor(da, "da", shape), _ref(g),
             *_bytes(ws, "ws"))
-    return BoundCall("moe_block_norm_backward", args, grads, keep, dev, stream)
+    return BoundCall("moe_block_norm_backward", args, grads, keep, tensors, dev, stream)
 
 
 def moe_block_norm_backward(cfg: NormCfg, x: torch.Tensor, dy=None, da=None, branch=None, post_w=None, gate=None,
@@ -345,15 +396,17 @@ def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = True) -> W4Weig
 
 
 def bind_w4_linear(cfg: W4Cfg, x: torch.Tensor, w: W4Weights, y=None, stream=None) -> BoundCall:
-    T = _rows(x, cfg.n_in)
-    y = torch.empty((T, cfg.n_out), dtype=torch.bfloat16, device=x.device) if y is None else y
-    _one_device(x, w.codes, w.scales, w.zeros, y)
+    T, stream = _rows(x, cfg.n_in), _stream_object(stream, x.device)
+    with _allocating_on(stream):
+        y = torch.empty((T, cfg.n_out), dtype=torch.bfloat16, device=x.device) if y is None else y
+    tensors = (x, w.codes, w.scales, w.zeros, y)
+    _one_device(*tensors)
     rows, groups = cfg.n_out * (2 if cfg.glu else 1), cfg.n_in // max(cfg.group, 1)
     keep = (cfg, x, w, y, _Three(_tensor(w.codes, "w.codes", (rows, cfg.n_in // 2), torch.uint8),
                                  _tensor(w.scales, "w.scales", (rows, groups)),
                                  _tensor(w.zeros, "w.zeros", (rows, groups), torch.uint8)))
     args = (_ref(cfg), _tensor(x, "x", (T, cfg.n_in)), T, _ref(keep[-1]), _tensor(y, "y", (T, cfg.n_out)))
-    return BoundCall("moe_w4_linear", args, y, keep, x.device, stream)
+    return BoundCall("moe_w4_linear", args, y, keep, tensors, x.device, stream)
 
 
 def moe_w4_linear(cfg: W4Cfg, x: torch.Tensor, w: W4Weights, y=None, stream=None) -> torch.Tensor:
