@@ -142,8 +142,9 @@ class BoundCall:
     """A library call with its arguments marshalled once.  Each call enqueues the same work
     on the same buffers (their contents are read when it runs) on the stream given to
     ``bind_*``, or, where none was given, on torch's current stream of that moment, and
-    returns the same output tensors.  The tensors stay alive as long as the object, and
-    their memory until the streams that it was called on are done with it."""
+    returns the same output tensors.  The configuration and the tensors are those of that
+    moment (a field of ``w`` or ``grads`` that is replaced later does not count); the tensors
+    stay alive as long as the object, and their memory until the streams that it was called on are done with it."""
 
     __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream", "_tensors", "_seen")
 
@@ -181,6 +182,12 @@ class BoundCall:
 
 def _ref(struct):
     return ctypes.cast(ctypes.pointer(struct), _P)
+
+
+def _own(cfg):
+    """The configuration as it is now: sizes that change after a call's tensors were checked
+    would send its kernels past their ends."""
+    return type(cfg).from_buffer_copy(cfg)
 
 
 # ----------------------------------------------------------------------------- gated FFN
@@ -235,7 +242,7 @@ def _glu_weights(cfg: GluCfg, w: GluWeights) -> _Three:
 
 def bind_glu_forward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved=None, y=None, ws=None,
                      stream=None) -> BoundCall:
-    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    cfg, T, stream = _own(cfg), _rows(x, cfg.d_model), _stream_object(stream, x.device)
     with _allocating_on(stream):
         y = torch.empty_like(x) if y is None else y
         ws = glu_workspace(cfg, T, x.device) if ws is None else ws
@@ -255,7 +262,7 @@ def moe_glu_forward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved=None, y=N
 
 def bind_glu_backward(cfg: GluCfg, x: torch.Tensor, w: GluWeights, saved: torch.Tensor, dy: torch.Tensor, dx=None,
                       grads: Optional[GluGrads] = None, ws=None, need_dx: bool = True, stream=None) -> BoundCall:
-    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    cfg, T, stream = _own(cfg), _rows(x, cfg.d_model), _stream_object(stream, x.device)
     with _allocating_on(stream):
         if need_dx and dx is None:
             dx = torch.empty_like(x)
@@ -301,7 +308,7 @@ def _norm_inputs(cfg: NormCfg, T: int, x, branch, post_w, gate, pre_w) -> _Five:
 
 def bind_block_norm_forward(cfg: NormCfg, x: torch.Tensor, branch=None, post_w=None, gate=None, pre_w=None, y=None,
                             a=None, stream=None) -> BoundCall:
-    T, stream = _rows(x, cfg.d_model), _stream_object(stream, x.device)
+    cfg, T, stream = _own(cfg), _rows(x, cfg.d_model), _stream_object(stream, x.device)
     with _allocating_on(stream):
         if branch is not None and y is None:
             y = torch.empty_like(x)
@@ -332,7 +339,7 @@ def block_norm_workspace(cfg: NormCfg, T: int, device=None) -> torch.Tensor:
 
 def bind_block_norm_backward(cfg: NormCfg, x: torch.Tensor, dy=None, da=None, branch=None, post_w=None, gate=None,
                              pre_w=None, grads: Optional[NormGrads] = None, ws=None, stream=None) -> BoundCall:
-    T, dev = _rows(x, cfg.d_model), x.device
+    cfg, T, dev = _own(cfg), _rows(x, cfg.d_model), x.device
     stream = _stream_object(stream, dev)
 
     def f32(n):
@@ -396,7 +403,7 @@ def w4_quantize(w: torch.Tensor, group: int = 128, zeros: bool = True) -> W4Weig
 
 
 def bind_w4_linear(cfg: W4Cfg, x: torch.Tensor, w: W4Weights, y=None, stream=None) -> BoundCall:
-    T, stream = _rows(x, cfg.n_in), _stream_object(stream, x.device)
+    cfg, T, stream = _own(cfg), _rows(x, cfg.n_in), _stream_object(stream, x.device)
     with _allocating_on(stream):
         y = torch.empty((T, cfg.n_out), dtype=torch.bfloat16, device=x.device) if y is None else y
     tensors = (x, w.codes, w.scales, w.zeros, y)

@@ -252,3 +252,42 @@ def test_stream_handle_zero_is_the_default_stream(world):
     with world.using(Stream(0x55)):
         call(cfg, **kw, stream=0)
     assert world.calls[-1].stream == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_bound_call_keeps_its_configuration_and_tensors(world, name):
+    """Changing the configuration, or replacing the tensors in the structures that were given,
+    after the checks changes nothing that the kernels get."""
+    cfg, bind, _, kw = operators(world)[name]
+    before = bytes(cfg)
+    call = bind(cfg, **kw)
+    call()
+    first = pointers(world.calls[-1])
+    for field in ("d_model", "ff", "n_in", "n_out"):
+        if hasattr(cfg, field):
+            setattr(cfg, field, 1 << 20)
+    if "w" in kw:
+        for f in vars(kw["w"]):
+            setattr(kw["w"], f, None)
+    out = call()
+    for o in out if isinstance(out, tuple) else (out,):
+        if isinstance(o, (moe.GluGrads, moe.NormGrads)):
+            for f in vars(o):
+                setattr(o, f, None)
+    del kw, out
+    call()
+    assert ctypes.string_at(world.calls[-1].args[0], len(before)) == before
+    assert pointers(world.calls[-1]) == first
+    world.calls.clear()
+    got, _ = refill(world, freed_sizes(world))
+    assert not got & first
+
+
+def test_pointers_of_replaced_tensors_are_not_handed_out(world):
+    cfg, bind, _, kw = operators(world)["glu_backward"]
+    call = bind(cfg, **kw)
+    call()
+    mine = pointers(world.calls[-1])
+    kw["w"].gate = kw["w"].up = kw["w"].down = None
+    got, _ = refill(world, freed_sizes(world))
+    assert not got & mine
