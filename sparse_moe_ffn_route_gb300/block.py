@@ -111,12 +111,16 @@ def _one_device(x: torch.Tensor, *others) -> None:
             raise ValueError(f"tensors on {x.device} and {t.device}")
 
 
-def _current_stream(device: torch.device) -> int:
+def _current_stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
 # The same handle without the Stream object around it, 0.1 us instead of 2, where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+# The current device's index; torch's own function without its check for initialisation, where
+# torch has it (a CUDA tensor exists by then).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current_handle(device: torch.device) -> int:
@@ -126,25 +130,33 @@ def _current_handle(device: torch.device) -> int:
 def _stream_object(stream, device: torch.device):
     """What a caller gives as `stream` (a torch stream, or a cudaStream_t's value) as torch's
     object; None stays None."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
+    if stream is None:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError(f"tensors on {device} and a stream of {stream.device}")
         return stream
     handle = int(getattr(stream, "cuda_stream", stream))
     return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
 
 
+_here = contextlib.nullcontext()
+
+
 def _allocating_on(stream):
     """What is allocated inside belongs to `stream` (None: the current one), where it is used:
     memory that the current stream has freed but still works on is not handed out there."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
 class BoundCall:
     """A library call with its arguments marshalled once.  Each call enqueues the same work
     on the same buffers (their contents are read when it runs) on the stream given to
     ``bind_*``, or, where none was given, on torch's current stream of that moment, and
-    returns the same output tensors.  The configuration and the tensors are those of that
-    moment (a field of ``w`` or ``grads`` that is replaced later does not count); the tensors
-    stay alive as long as the object, and their memory until the streams that it was called on are done with it."""
+    returns the same output tensors.  It runs on the tensors' device, whichever is current.
+    The configuration and the tensors are those of the moment it was bound (a field of ``w``
+    or ``grads`` that is replaced later does not count).  The tensors stay alive as long as
+    the object, and their memory until the streams that it was called on are done with it."""
 
     __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream", "_tensors", "_seen")
 
@@ -152,7 +164,7 @@ class BoundCall:
         self._fn, self._where = getattr(_lib, where), where
         self._args, self._out, self._keep = args, out, (keep, stream)
         self._tensors = [t for t in tensors if t is not None]
-        self._device = device.index if _raw_stream is not None else device
+        self._device = device.index
         self._stream = None if stream is None else stream.cuda_stream
         # streams whose work the allocator knows to use the tensors: the current one owns
         # them, or, beside one that is given, is where the caller will use the outputs
@@ -174,7 +186,11 @@ class BoundCall:
             stream = (_raw_stream or _current_stream)(self._device)
             if stream not in self._seen:
                 self._record(stream, torch.cuda.current_stream(self._device))
-        status = self._fn(*self._args, stream)
+        if _current_device() == self._device:
+            status = self._fn(*self._args, stream)
+        else:   # the library launches on the current device
+            with torch.cuda.device(self._device):
+                status = self._fn(*self._args, stream)
         if status != MOE_OK:
             raise MoeError(status, self._where)
         return self._out
@@ -210,10 +226,13 @@ class GluGrads:
 
 
 def _buffer(fn: str, cfg, T: int, device) -> torch.Tensor:
-    n = int(getattr(_lib, fn)(ctypes.byref(cfg), T))
+    device = torch.device(device or "cuda")
+    # sizes may depend on the GPU: those of the one that the buffer is for
+    with torch.cuda.device(device) if device.type == "cuda" else _here:
+        n = int(getattr(_lib, fn)(ctypes.byref(cfg), T))
     if n == 0:
         raise MoeError(-1, fn)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def moe_glu_workspace_bytes(cfg: GluCfg, T: int) -> int:

@@ -72,7 +72,7 @@ class World:
     """The parts of torch that the binding uses, and a library that notes its calls."""
 
     def __init__(self, monkeypatch):
-        self.memory, self.calls, self.selected = Memory(), [], 0
+        self.memory, self.calls, self.selected, self.sized = Memory(), [], 0, []
         self.current = {0: Stream(0), 1: Stream(0, torch.device("cuda", 1))}
         world = self
 
@@ -128,7 +128,10 @@ class World:
 
         class Library:
             def __getattr__(self, name):
-                return getattr(real, name) if name.endswith("_bytes") else noted(name)
+                if not name.endswith("_bytes"):
+                    return noted(name)
+                world.sized.append(world.selected)
+                return getattr(real, name)
 
         monkeypatch.setattr(block, "_lib", Library())
 
@@ -291,3 +294,23 @@ def test_pointers_of_replaced_tensors_are_not_handed_out(world):
     kw["w"].gate = kw["w"].up = kw["w"].down = None
     got, _ = refill(world, freed_sizes(world))
     assert not got & mine
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_run_on_the_device_of_their_tensors(world, name):
+    """The library sizes grids and launches on the current device: that of the tensors."""
+    other = torch.device("cuda", 1)
+    world.current[1] = Stream(0x31, other)
+    cfg, bind, call, kw = operators(world, device=other)[name]
+    world.sized.clear()
+    call(cfg, **kw)
+    bound = bind(cfg, **kw)
+    bound()
+    with world.using(Stream(0x32, other)):
+        bound()
+    call(cfg, **kw, stream=Stream(0x33, other))
+    assert [(c.device, c.stream) for c in world.calls] == [(1, 0x31), (1, 0x31), (1, 0x32), (1, 0x33)]
+    assert world.selected == 0 and set(world.sized) <= {1}
+    with pytest.raises(ValueError, match="stream"):
+        call(cfg, **kw, stream=Stream(0x34, DEVICE))
+    assert len(world.calls) == 4
