@@ -93,7 +93,14 @@ def _tensor(t: Optional[torch.Tensor], name: str, shape, dtype=torch.bfloat16) -
 def _rows(x: torch.Tensor, width: int, name: str = "x") -> int:
     if x.dim() != 2 or x.shape[1] != width:
         raise ValueError(f"{name} must have shape (T, {width}), not {tuple(x.shape)}")
-    return x.shape[0]
+    return _tokens(x.shape[0])
+
+
+def _tokens(T: int) -> int:
+    """T as the library's int32 takes it: ctypes would drop what does not fit."""
+    if T >= 1 << 31:
+        raise ValueError(f"{T} tokens are more than the library's sizes hold")
+    return T
 
 
 def _bytes(t: Optional[torch.Tensor], name: str):
@@ -229,18 +236,18 @@ def _buffer(fn: str, cfg, T: int, device) -> torch.Tensor:
     device = torch.device(device or "cuda")
     # sizes may depend on the GPU: those of the one that the buffer is for
     with torch.cuda.device(device) if device.type == "cuda" else _here:
-        n = int(getattr(_lib, fn)(ctypes.byref(cfg), T))
+        n = int(getattr(_lib, fn)(ctypes.byref(cfg), _tokens(T)))
     if n == 0:
         raise MoeError(-1, fn)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def moe_glu_workspace_bytes(cfg: GluCfg, T: int) -> int:
-    return int(_lib.moe_glu_workspace_bytes(ctypes.byref(cfg), T))
+    return int(_lib.moe_glu_workspace_bytes(ctypes.byref(cfg), _tokens(T)))
 
 
 def moe_glu_saved_bytes(cfg: GluCfg, T: int) -> int:
-    return int(_lib.moe_glu_saved_bytes(ctypes.byref(cfg), T))
+    return int(_lib.moe_glu_saved_bytes(ctypes.byref(cfg), _tokens(T)))
 
 
 def glu_workspace(cfg: GluCfg, T: int, device=None) -> torch.Tensor:
@@ -349,7 +356,7 @@ def moe_block_norm_forward(cfg: NormCfg, x: torch.Tensor, branch=None, post_w=No
 
 
 def moe_block_norm_workspace_bytes(cfg: NormCfg, T: int) -> int:
-    return int(_lib.moe_block_norm_workspace_bytes(ctypes.byref(cfg), T))
+    return int(_lib.moe_block_norm_workspace_bytes(ctypes.byref(cfg), _tokens(T)))
 
 
 def block_norm_workspace(cfg: NormCfg, T: int, device=None) -> torch.Tensor:

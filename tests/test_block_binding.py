@@ -314,3 +314,19 @@ def test_calls_run_on_the_device_of_their_tensors(world, name):
     with pytest.raises(ValueError, match="stream"):
         call(cfg, **kw, stream=Stream(0x34, DEVICE))
     assert len(world.calls) == 4
+
+
+@pytest.mark.parametrize("T", [1 << 31, (1 << 32) + 3])
+def test_more_tokens_than_the_library_counts(T):
+    """Sizes are int32 in the library: a larger T must not arrive there without its upper bits."""
+    glu, norm, w4 = moe.glu_cfg(8, 8), moe.norm_cfg(8), moe.w4_cfg(32, 8, 32)
+    x, wide = torch.empty(T, 8, dtype=torch.bfloat16, device="meta"), torch.empty(T, 32, dtype=torch.bfloat16, device="meta")
+    w = moe.GluWeights(x[:8], x[:8], x[:8])
+    for call in (lambda: moe.moe_glu_forward(glu, x, w), lambda: moe.moe_block_norm_forward(norm, x, pre_w=x[0]),
+                 lambda: moe.moe_block_norm_backward(norm, x, da=x, pre_w=x[0]),
+                 lambda: moe.moe_w4_linear(w4, wide, moe.W4Weights(x, x)),
+                 lambda: moe.moe_glu_workspace_bytes(glu, T), lambda: moe.moe_glu_saved_bytes(glu, T),
+                 lambda: moe.moe_block_norm_workspace_bytes(norm, T), lambda: moe.glu_workspace(glu, T, "meta"),
+                 lambda: moe.glu_saved(glu, T, "meta"), lambda: moe.block_norm_workspace(norm, T, "meta")):
+        with pytest.raises(ValueError, match="tokens"):
+            call()
