@@ -8,6 +8,7 @@
  * patterns in row-major order, weight matrices are row = output, column = input.
  * Every tensor pointer must be 16-byte aligned (MOE_ERR_ALIGNMENT).  On error nothing
  * has been enqueued unless the code is MOE_ERR_CUDA.  Reserved members must be zero.
+ * The gated FFN and the norms take up to 2^30 tokens (MOE_ERR_UNSUPPORTED past that).
  *
  * Sums, norm statistics and activations are computed in fp32; results are rounded once
  * to their type (round to nearest even).  All reductions run in a fixed order, so equal
@@ -31,8 +32,8 @@ extern "C" {
  * with saved NULL, at most 8 tokens and ff <= 4096, where that rounding would show beside
  * y's own, h keeps its low half as a second bf16. */
 typedef struct {
-  int32_t d_model;     /* d, a positive multiple of 8 */
-  int32_t ff;          /* hidden width, a positive multiple of 8 */
+  int32_t d_model;     /* d, a positive multiple of 8, at most 2^29 */
+  int32_t ff;          /* hidden width, a positive multiple of 8, at most 2^29 */
   int32_t act;         /* MOE_ACT_* */
   float glu_limit;     /* clamped GLU limit, >= 0 */
   float glu_alpha;     /* clamped GLU sigmoid slope */
@@ -134,8 +135,8 @@ int moe_block_norm_backward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* 
  *   y[t, o] = sum_k x[t, k] * (code[o, k] - zero[o, k / group]) * scale[o, k / group]
  * glu = 1: the matrix has 2 n_out rows, gate rows first, and y = act(gate, up) [T, n_out]. */
 typedef struct {
-  int32_t n_in;        /* a positive multiple of group */
-  int32_t n_out;       /* columns of y, >= 1 */
+  int32_t n_in;        /* a positive multiple of group, at most 2^29 */
+  int32_t n_out;       /* columns of y, 1 to 2^30 */
   int32_t group;       /* inputs per scale: 32, 64 or 128 */
   int32_t glu;         /* 0 or 1 */
   int32_t act;         /* MOE_ACT_*, with glu */

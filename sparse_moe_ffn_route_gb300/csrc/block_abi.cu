@@ -12,6 +12,11 @@ namespace {
 // MMAs (16 tokens a pass) instead of tcgen05 tiles of 128 token rows.
 constexpr int kSkinnyTokens = 16;
 
+// The kernels count rows and columns in 32 bits and step a whole grid's rows (norms: 3 rows
+// ahead of up to 2432 groups of threads) or a row's bytes (skinny.cu: 2 per input) past the
+// last one before they compare.  These bounds keep every such sum below 2^31.
+constexpr int kMaxTokens = 1 << 30, kMaxInputs = 1 << 29, kMaxOutputs = 1 << 30;
+
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Null or 16-byte aligned.
@@ -31,13 +36,15 @@ int check_act(int act, float limit, float alpha) {
   return MOE_OK;
 }
 
+int check_tokens(int T) { return T < 0 ? MOE_ERR_INVALID_ARG : T > kMaxTokens ? MOE_ERR_UNSUPPORTED : MOE_OK; }
+
 int check_glu(const moe_glu_cfg_t* c) {
   if (!c || c->d_model <= 0 || c->ff <= 0) return MOE_ERR_INVALID_ARG;
   for (int r : c->reserved)
     if (r) return MOE_ERR_INVALID_ARG;
   const int st = check_act(c->act, c->glu_limit, c->glu_alpha);
   if (st != MOE_OK) return st;
-  return c->d_model % 8 || c->ff % 8 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return c->d_model % 8 || c->ff % 8 || c->d_model > kMaxInputs || c->ff > kMaxInputs ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // Workspace: status word | h [T, ff] (forward that keeps nothing) or dg, du [T, ff] | the
@@ -108,18 +115,17 @@ int check_norm_inputs(const moe_norm_inputs_t* in) {
 extern "C" {
 
 size_t moe_glu_workspace_bytes(const moe_glu_cfg_t* cfg, int32_t T) {
-  return check_glu(cfg) != MOE_OK || T < 0 ? 0 : glu_layout(*cfg, T).total;
+  return check_glu(cfg) != MOE_OK || check_tokens(T) != MOE_OK ? 0 : glu_layout(*cfg, T).total;
 }
 
 size_t moe_glu_saved_bytes(const moe_glu_cfg_t* cfg, int32_t T) {
-  return check_glu(cfg) != MOE_OK || T < 0 ? 0 : align_up(saved_layout(*cfg, T).total) + 256;
+  return check_glu(cfg) != MOE_OK || check_tokens(T) != MOE_OK ? 0 : align_up(saved_layout(*cfg, T).total) + 256;
 }
 
 int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const moe_glu_weights_t* w, void* y,
                     void* saved, size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
   int st = check_glu(cfg);
-  if (st != MOE_OK) return st;
-  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK || (st = check_tokens(T)) != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!x || !y || !ws) return MOE_ERR_INVALID_ARG;
   if ((st = check_glu_weights(w)) != MOE_OK) return st;
@@ -153,8 +159,7 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
                      const void* saved, size_t saved_bytes, const void* dy, void* dx,
                      const moe_glu_grads_t* grads, void* ws, size_t ws_bytes, void* stream) {
   int st = check_glu(cfg);
-  if (st != MOE_OK) return st;
-  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK || (st = check_tokens(T)) != MOE_OK) return st;
   const moe_glu_grads_t none{nullptr, nullptr, nullptr};
   const moe_glu_grads_t& dw = grads ? *grads : none;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -187,8 +192,7 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
 int moe_block_norm_forward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* in, int32_t T, void* y, void* a,
                            void* stream) {
   int st = check_norm(cfg);
-  if (st != MOE_OK) return st;
-  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK || (st = check_tokens(T)) != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if ((st = check_norm_inputs(in)) != MOE_OK) return st;
   if ((in->branch != nullptr) != (y != nullptr) || (in->pre_w != nullptr) != (a != nullptr)) return MOE_ERR_INVALID_ARG;
@@ -199,7 +203,7 @@ int moe_block_norm_forward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* i
 }
 
 size_t moe_block_norm_workspace_bytes(const moe_norm_cfg_t* cfg, int32_t T) {
-  if (check_norm(cfg) != MOE_OK || T < 0) return 0;
+  if (check_norm(cfg) != MOE_OK || check_tokens(T) != MOE_OK) return 0;
   return 256 + (size_t)block_norm_parts(T) * 2 * cfg->d_model * 4;
 }
 
@@ -207,8 +211,8 @@ int moe_block_norm_backward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* 
                             const void* da, const moe_norm_grads_t* grads, void* ws, size_t ws_bytes,
                             void* stream) {
   int st = check_norm(cfg);
-  if (st != MOE_OK) return st;
-  if (T < 0 || !grads) return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK || (st = check_tokens(T)) != MOE_OK) return st;
+  if (!grads) return MOE_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const moe_norm_grads_t& o = *grads;
   if (!aligned16(dy, da, o.dx, o.dbranch, o.dgate, o.dpost_w, o.dpre_w)) return MOE_ERR_ALIGNMENT;
@@ -236,7 +240,7 @@ int moe_w4_linear(const moe_w4_cfg_t* c, const void* x, int32_t T, const moe_w4_
   const int st = check_act(c->act, c->glu_limit, c->glu_alpha);
   if (st != MOE_OK) return st;
   if (c->group != 32 && c->group != 64 && c->group != 128) return MOE_ERR_UNSUPPORTED;
-  if (c->n_in % c->group) return MOE_ERR_UNSUPPORTED;
+  if (c->n_in % c->group || c->n_in > kMaxInputs || c->n_out > kMaxOutputs) return MOE_ERR_UNSUPPORTED;
   if (T < 0) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!x || !y || !w || !w->codes || !w->scales) return MOE_ERR_INVALID_ARG;
