@@ -4,6 +4,7 @@
 
 #include "../../include/moe_block.h"
 #include "internal.h"
+#include "per_device.h"
 
 namespace moe {
 
@@ -11,12 +12,15 @@ namespace moe {
 // device (`bytes` is the same at every call).
 template <auto KERNEL>
 cudaError_t allow_smem(int bytes) {
-  static bool done[64] = {};
-  int dev = 0;
+  static PerDevice<1> allowed;
+  int dev = 0, got[1];
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  cudaError_t e = cudaSuccess;
+  allowed.get(dev, got, [&](int (&out)[1]) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    out[0] = bytes;
+    return e == cudaSuccess;
+  });
   return e;
 }
 

@@ -1029,35 +1029,39 @@ cudaError_t prepare_kernel() {
 }
 
 // How many clusters of n = 1, 2, 4, 8 CTAs (one CTA per SM) the GPU holds at one time: [n].
+struct ClusterCounts {
+  int of[9];
+  int operator[](int n) const { return of[n]; }
+};
+
 // Asked of the runtime once per device.
-const int* cluster_counts() {
-  static int count[64][9] = {};
-  static const int one[9] = {0, 1, 1, 1, 1, 1, 1, 1, 1};
+ClusterCounts cluster_counts() {
+  static PerDevice<9> counts;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return one;
-  int* of = count[dev];
-  if (of[1]) return of;
-  const int sms = sm_count();
-  const bool ready = prepare_kernel<2, kEpiStore, false>() == cudaSuccess;
-  for (int n = 2; n <= 8; n <<= 1) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)n;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms / n * n);
-    cfg.blockDim = dim3(Lay<kEpiStore>::kThreads);
-    cfg.dynamicSmemBytes = Lay<kEpiStore>::kSmemBytes;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int c = 0;
-    if (!ready || cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore, false>, &cfg) != cudaSuccess || c < 1)
-      c = std::max(1, sms / n);
-    of[n] = c;
-  }
-  of[1] = sms;
-  return of;
+  ClusterCounts found;
+  counts.get(dev, found.of, [](int (&of)[9]) {
+    const int sms = sm_count();
+    for (int n = 0; n < 9; ++n) of[n] = n ? std::max(1, sms / n) : 0;
+    const bool ready = prepare_kernel<2, kEpiStore, false>() == cudaSuccess;
+    for (int n = 2; n <= 8; n <<= 1) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)n;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(sms / n * n);
+      cfg.blockDim = dim3(Lay<kEpiStore>::kThreads);
+      cfg.dynamicSmemBytes = Lay<kEpiStore>::kSmemBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int c = 0;
+      if (ready && cudaOccupancyMaxActiveClusters(&c, glu_gemm_kernel<2, kEpiStore, false>, &cfg) == cudaSuccess && c > 0)
+        of[n] = c;
+    }
+    return true;
+  });
+  return found;
 }
 
 // How a launch runs: single CTAs or pairs (cg), or clusters of `parts` CTAs that split k.
@@ -1129,7 +1133,7 @@ constexpr long long kLongClocks = 200000;
 Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = nullptr) {
   Way best{1, 1, kMaxN};
   long long least = -1;
-  const int* const counts = cluster_counts();
+  const ClusterCounts counts = cluster_counts();
   auto consider = [&](int cg, int parts, int tn) {
     const int units = counts[cg * parts];
     const long long tiles = (long long)cdiv(M, kBM * cg) * cdiv(N, tn / per);
@@ -1355,7 +1359,7 @@ struct Backward {
 
 Backward plan_backward(const GluParams& w, int T, bool dx, bool dwg, bool dwu, bool dwd) {
   constexpr int kDactSpace = Lay<kEpiDact>::kStageSpace, kSpace = Lay<kEpiStore>::kStageSpace;
-  const int* const counts = cluster_counts();
+  const ClusterCounts counts = cluster_counts();
   const int k = cdiv(T, kBK), kd = cdiv(w.d, kBK), kff = cdiv(w.ff, kBK);
   auto tiles = [&](int M, int N, int cg, int tn) { return (int)std::min<long long>((long long)cdiv(M, kBM * cg) * cdiv(N, tn), 1 << 28); };
   auto pairs = [](int cg) { return cg == 2 ? kPairClocks : 0; };
