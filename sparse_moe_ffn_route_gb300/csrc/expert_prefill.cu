@@ -792,27 +792,17 @@ transpose_scales_kernel(const uint8_t* __restrict__ src, int E, int rows, int nb
 }  // namespace
 
 // ---------------------------------------------------------------- host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-namespace {
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+// A local static: threads that come while the first one looks it up wait for what it finds.
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
   return fn;
 }
-}  // namespace
 
 int sm_count() {
   int dev = 0, n = 0;
@@ -826,7 +816,7 @@ int sm_count() {
 bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows,
               uint64_t cols, uint64_t stride, uint32_t box_rows, uint32_t box_cols,
               CUtensorMapSwizzle swz) {
-  EncodeTiledFn fn = encode_fn();
+  const EncodeTiled fn = encode_tiled();
   if (!fn || !base) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {stride};

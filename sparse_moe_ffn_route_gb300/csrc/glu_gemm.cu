@@ -994,19 +994,6 @@ bool map_bf16(CUtensorMap* m, const uint16_t* base, int rows, int cols, int box_
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                        cudaSuccess && q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeTiled>(p) : nullptr;
-  }();
-  return fn;
-}
-
 // A matrix [k, cols], cols a multiple of 64, seen as [cols / 64][k][64]: an MN-major tile of
 // `blocks` x 64 columns and 64 k is one box.  (With a ragged last block its rows would run
 // into the next row of the matrix, and past its end: those go by boxes of the plain map.)

@@ -86,6 +86,9 @@ struct RouteState {
 };
 
 // ---------------------------------------------------------------- host helpers
+// The driver's cuTensorMapEncodeTiled, or null where it has none.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+EncodeTiled encode_tiled();
 // 2D TMA map over a row-major matrix [rows, cols] of `type` (row stride in bytes)
 // with a box of box_rows x box_cols elements; false if the driver rejects it.
 bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows,
