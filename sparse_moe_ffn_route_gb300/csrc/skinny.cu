@@ -66,6 +66,10 @@ struct Cut {
 __device__ __forceinline__ void copy_weights16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// The same, of which only `bytes` (0 or 16) are read and the rest is zero.
+__device__ __forceinline__ void copy_weights16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 // The row of tile b of a unit that this lane takes first (gq), clamped to the last row, and
 // how many rows on its second one lies (8, clamped alike; a clamped row's sums are not
@@ -89,6 +93,7 @@ struct Bf16 {
   static constexpr int kStep = 32, kScaleSteps = 1 << 20;
   static constexpr int kPad = 64;       // bytes between x's rows beyond a multiple of 128
   static constexpr bool kPairs = false;
+  static constexpr bool kZeroEnd = true;   // past the end of a row: zeros, since x's zeros times infinity are NaN
   const uint16_t *w0, *w1;   // gated: gate, up
   struct Scales {};
   struct ScaleRows {};
@@ -159,6 +164,7 @@ struct W4 {
   static constexpr int kStep = 128;
   static constexpr int kPad = GROUP == 32 ? 64 : 16;   // bytes between x's rows beyond a multiple of 128
   static constexpr bool kPairs = true;
+  static constexpr bool kZeroEnd = false;  // past the end of a row: any codes, which are finite
   static constexpr int kGroups = 128 / GROUP, kWords = 4 / kGroups;   // groups of a step; words of a group
   static constexpr int kScaleSteps = 4 / kGroups;   // steps whose groups the four lanes of a quad hold
   const uint8_t* codes;
@@ -353,12 +359,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n
       const int st0 = phase * cut.phase_steps + first;
       const int run = busy ? min(per_phase, cut.steps - st0) : 0;   // may be negative
       int off = 64 * st0;
-      // the copies: DEPTH steps ahead of the multiplications; past the end of a row its last
-      // piece is read again (x is zero there)
+      // the copies: DEPTH steps ahead of the multiplications; past the end of a row zeros, or
+      // its last piece again (x is zero there)
       auto copy = [&](uint32_t dst) {
         const int o = min(off, last);
+        const uint32_t bytes = off <= last ? 16u : 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) copy_weights16(dst + 512 * e, p[e >> 1][e & 1] + o);
+        for (int e = 0; e < 4; ++e) {
+          if (F::kZeroEnd) copy_weights16(dst + 512 * e, p[e >> 1][e & 1] + o, bytes);
+          else copy_weights16(dst + 512 * e, p[e >> 1][e & 1] + o);
+        }
         off += 64;
       };
       if (run > 0) f.load_scales(scale_next, scale_rows, st0, c, K);

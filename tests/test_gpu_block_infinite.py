@@ -1,0 +1,62 @@
+"""Infinite weights of the dense block: the results are infinite or NaN where the formulas,
+computed in 64 bits, make them so, and nowhere else."""
+import pytest
+
+torch = pytest.importorskip("torch")
+moe = pytest.importorskip("sparse_moe_ffn_route_gb300")
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def rnd(gen, *shape, scale=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * scale).bfloat16()
+
+
+def ffn(T, d, ff, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed + 31 * T + d + 7 * ff)
+    return rnd(gen, T, d), moe.GluWeights(rnd(gen, ff, d, scale=d ** -0.5), rnd(gen, ff, d, scale=d ** -0.5),
+                                          rnd(gen, d, ff, scale=ff ** -0.5))
+
+
+def formula(x, w):
+    x, g, u, d = (t.double() for t in (x, w.gate, w.up, w.down))
+
+    def product(a, b):   # term by term, so that infinities meet what the formula says they meet
+        return torch.stack([(row * b).sum(1) for row in a])
+
+    g, u = product(x, g), product(x, u)
+    return product(g * torch.sigmoid(g) * u, d)
+
+
+def same_classes(got, want, name):
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), (name, "NaN")
+    assert torch.equal(torch.isinf(got), torch.isinf(want)), (name, "infinite")
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf].sign(), want[inf].sign()), (name, "sign")
+
+
+@pytest.mark.parametrize("back", [1, 3, 8])
+@pytest.mark.parametrize("T,d,ff", [(1, 40, 64), (5, 72, 96), (8, 136, 32), (12, 104, 128), (16, 40, 64)])
+def test_infinite_gate_and_up_at_the_end_of_a_row(T, d, ff, back):
+    """d is no multiple of the 32 inputs that a step of the few-token kernel takes."""
+    x, w = ffn(T, d, ff, back)
+    x[:, d - back] = x[:, d - back].abs() + 0.5
+    w.gate[3, d - back] = INF
+    w.up[ff - 2, d - back] = -INF
+    want = formula(x, w)
+    assert torch.isinf(want).any()
+    same_classes(moe.moe_glu_forward(moe.glu_cfg(d, ff), x, w), want, "y")
+
+
+@pytest.mark.parametrize("back", [1, 8])
+@pytest.mark.parametrize("T,d,ff", [(9, 64, 72), (16, 32, 40), (12, 96, 4104)])
+def test_infinite_down_at_the_end_of_a_row(T, d, ff, back):
+    x, w = ffn(T, d, ff, back)
+    w.down[5, ff - back] = INF
+    w.down[d - 1, ff - back] = -INF
+    want = formula(x, w)
+    assert torch.isinf(want[:, 5]).all() and torch.isfinite(want[:, 6:-1]).all()
+    same_classes(moe.moe_glu_forward(moe.glu_cfg(d, ff), x, w), want, "y")
