@@ -425,7 +425,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n
       if (NC == 2 && tk.lo) {
         float l = 0.f;
         for (int v = 0; v < ws; ++v) l += q[(v * TOK + 8) * kPitch];
-        s += l;
+        // the low halves only refine: where a weight is infinite they, or their zeros, would
+        // turn it into NaN
+        if (isfinite(s)) s += l;
       }
       int o = u * kUnitRows + lane;
       if (GLU) {

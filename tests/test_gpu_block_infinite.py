@@ -60,3 +60,15 @@ def test_infinite_down_at_the_end_of_a_row(T, d, ff, back):
     want = formula(x, w)
     assert torch.isinf(want[:, 5]).all() and torch.isfinite(want[:, 6:-1]).all()
     same_classes(moe.moe_glu_forward(moe.glu_cfg(d, ff), x, w), want, "y")
+
+@pytest.mark.parametrize("T,d,ff,at", [(1, 64, 64, 7), (4, 96, 512, 300), (8, 64, 4096, 4000), (7, 32, 40, 39)])
+def test_infinite_down_weight_meets_a_two_part_h(T, d, ff, at):
+    """Few tokens, narrow FFN: h goes into the product as two bf16 numbers, of which the second
+    one's sign, or a zero, must not decide what an infinite weight gives."""
+    x, w = ffn(T, d, ff, at)
+    w.down[5, at] = INF
+    w.down[d - 1, at] = -INF
+    w.down[9, at] = float("nan")
+    want = formula(x, w)
+    assert torch.isinf(want[:, 5]).all() and torch.isnan(want[:, 9]).all()
+    same_classes(moe.moe_glu_forward(moe.glu_cfg(d, ff), x, w), want, "y")
