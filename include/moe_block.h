@@ -132,7 +132,7 @@ int moe_block_norm_backward(const moe_norm_cfg_t* cfg, const moe_norm_inputs_t* 
                             void* stream);
 
 /* ------------------------------------------------------------------ 4-bit linear layer
- *   y[t, o] = sum_k x[t, k] * (code[o, k] - zero[o, k / group]) * scale[o, k / group]
+ *   y[t, o] = sum_g scale[o, g] * (sum_{k in group g} x[t, k] * (code[o, k] - zero[o, g]))
  * glu = 1: the matrix has 2 n_out rows, gate rows first, and y = act(gate, up) [T, n_out]. */
 typedef struct {
   int32_t n_in;        /* a positive multiple of group, at most 2^29 */

@@ -203,15 +203,17 @@ struct W4 {
       r.down[b] = (unsigned)down * (unsigned)(K / GROUP);
     }
   }
-  // Lane c: group kGroups st + c of its rows (the row's last one past the end).
+  // Lane c: group kGroups st + c of its rows; past the end a scale of 0, since the sum of x's
+  // zeros there times an infinite one would be NaN.
   __device__ __forceinline__ void load_scales(Scales& s, const ScaleRows& r, int st, int c, int K) const {
-    const int gi = min(kGroups * st + c, K / GROUP - 1);
+    const int end = K / GROUP - 1, gi = min(kGroups * st + c, end);
+    const uint32_t keep = GROUP == 128 || kGroups * st + c <= end ? 0xffffu : 0u;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const size_t at = r.at[b] + (unsigned)gi + (h ? r.down[b] : 0u);
-        s.sz[b][h] = ((uint32_t)scales[at] << 16) | (0x4300u + (zeros ? zeros[at] & 15u : 8u));
+        s.sz[b][h] = ((scales[at] & keep) << 16) | (0x4300u + (zeros ? zeros[at] & 15u : 8u));
       }
   }
 

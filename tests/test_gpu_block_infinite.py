@@ -72,3 +72,20 @@ def test_infinite_down_weight_meets_a_two_part_h(T, d, ff, at):
     want = formula(x, w)
     assert torch.isinf(want[:, 5]).all() and torch.isnan(want[:, 9]).all()
     same_classes(moe.moe_glu_forward(moe.glu_cfg(d, ff), x, w), want, "y")
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("T,k,n,group", [(1, 32, 5, 32), (5, 96, 40, 32), (16, 224, 33, 32), (3, 64, 17, 64),
+                                         (12, 192, 40, 64), (16, 8256, 20, 64)])
+def test_infinite_last_group_scale(T, k, n, group, zeros):
+    """n_in is no multiple of the 128 inputs that a step of the kernel takes.  The last group's
+    codes lie above its zero and its inputs are positive, so every term is +inf."""
+    gen = torch.Generator(device="cuda").manual_seed(T + k + n)
+    x = rnd(gen, T, k)
+    x[:, -group:] = x[:, -group:].abs() + 0.5
+    codes = torch.randint(0, 256, (n, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    codes[2, -group // 2:] = 0xCB
+    scales = rnd(gen, n, k // group, scale=0.1)
+    scales[2, -1] = INF
+    z = torch.randint(0, 8, (n, k // group), generator=gen, device="cuda", dtype=torch.uint8) if zeros else None
+    y = moe.moe_w4_linear(moe.w4_cfg(k, n, group), x, moe.W4Weights(codes, scales, z))
+    assert (y[:, 2] == INF).all() and torch.isfinite(y[:, [i for i in range(n) if i != 2]]).all()
