@@ -16,7 +16,7 @@
 // Backward: with rz = 1 / sqrt(mean z^2 + eps), ry alike for y, c the branch's factor,
 //   D  = dy + ry (da pre_w - y ry^2 mean(da pre_w y))        (gradient of y)
 //   dx = residual_scale D;   W = D post_w;   S = sum W z
-//   dgate = branch_scale s (1 - s) rz S;   dz = c rz (W - z rz^2 S / d)
+//   dgate = branch_scale s (1 - s) rz S, s = sigmoid(gate);   dz = c rz (W - z rz^2 S / d)
 //   dpost_w += c D z rz;   dpre_w += da y ry
 // One CTA per SM holds several groups of threads, each on rows of its own (named barriers),
 // with 16 elements per thread and row: the fixed work of a row (exchanges, roots) is paid
@@ -62,9 +62,15 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
 }
 
 // rsqrtf is 2 units in the last place off at most, sigmoid a few: far below what the sums
-// that go in have lost.
+// that go in have lost, and what the rounding to bf16 of all that they scale loses after.
 __device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(sum * inv_d + eps); }
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// sigmoid(v) sigmoid(-v) = e / (1 + e)^2 with e = exp(-|v|): dgate is fp32, and 1 - sigmoid(v)
+// would cancel for open gates (a thousandth off at 10, 0 from 17 on).
+__device__ __forceinline__ float sigmoid_slope(float v) {
+  const float e = expf(-fabsf(v)), r = __fdividef(1.f, 1.f + e);
+  return e * r * r;
+}
 
 // Two fp32 values that one instruction works on (fma.rn.f32x2 and its kin): the kernels
 // are near the issue rate, and this halves their arithmetic.
@@ -368,10 +374,10 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
   for (; t < T; t += stride, par ^= 1) {
     const size_t base = (size_t)t * d;
     F2 y[V][4], D[V][4];
-    float c = g.bs, s = 1.f;
+    float c = g.bs;
+    const float own = gate;   // this row's
     if (g.gate) {
-      s = sigmoid(gate);
-      c *= s;
+      c *= sigmoid(own);
       if (t + stride < T) gate = g.gate[t + stride];   // the next row's, ahead of its use
     }
     const float rz = POST ? inv_rms(sz, inv_d, eps) : 1.f;
@@ -464,7 +470,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormArgs g, const int gt) {
       if (POST || g.dgate) group_sum(sw, sums[group][par][1], tid, gt, 1 + group);
       sz = sw[1];
       const F2 kz = f2(POST ? -(rz * rz * sw[0] * inv_d) : 0.f);
-      if (g.dgate && tid == 0) g.dgate[t] = g.bs * s * (1.f - s) * rz * sw[0];
+      if (g.dgate && tid == 0) g.dgate[t] = g.bs * sigmoid_slope(own) * rz * sw[0];
       if (g.dz) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
