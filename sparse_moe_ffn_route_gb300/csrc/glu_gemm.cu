@@ -292,6 +292,13 @@ __device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// A wait of a whole warp whose lanes go on together: each lane polls for itself, and one that
+// sees the barrier's phase end while another sees the abort flag would leave the rest of the
+// warp alone in the collective instructions that follow.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, status));
+}
+
 template <int CG>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   if (CG == 1) {
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     const bool clamped = g.act.act == MOE_ACT_CLAMPED_GLU;
     int b = 0, sl = 0;                      // sl: dact, chunks seen (slot sl % kSlots)
     uint32_t aph = 0;
-    for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && !*abort; ++nth) {
+    for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && __all_sync(0xffffffffu, !*abort); ++nth) {
       const Tile tl = tile_at<EPI == kEpiStore && !SPLIT>(g, t);
       const Problem& p = g.p[tl.pi];
       const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)b * 256u;
@@ -788,7 +795,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         if (EPI == kEpiDact && blockIdx.x == 0)
           for (int i = threadIdx.x - 64; i < g.zeros; i += 32 * kEpiWarps) g.arrived[i] = 0u;
       }
-      if (!tc::mbar_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
+      if (!warp_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       if (SPLIT) {
         // every 8 columns to the CTA that finishes them: [its share][part][8 (pair: 16)][row]
@@ -859,7 +866,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           const int slot = n % L::kRing, c0 = 16 * j;
           float v[16], du[16];
           tc::tmem_ld16(taddr + (uint32_t)c0, v);
-          if (!tc::mbar_wait(tc::smem_u32(&sfull_bar[slot]), (n / L::kRing) & 1, abort, g.status)) break;
+          if (!warp_wait(tc::smem_u32(&sfull_bar[slot]), (n / L::kRing) & 1, abort, g.status)) break;
           const float4* gs = reinterpret_cast<const float4*>(smem + kStages * kStageBytes + slot * L::kSlotBytes) + row;
           const float4* us = gs + L::kSlotBytes / 32;
           const int left = cols - c0;
