@@ -42,9 +42,10 @@ struct GluSaved {
 };
 
 // tcgen05 kernels (glu_gemm.cu).  Each clears or may set bits of *status.
-// h = act(x Wg^T, x Wu^T); g, u non-null: kept as GluSaved describes.
+// h = act(x Wg^T, x Wu^T); g, u non-null: kept as GluSaved describes; norms: scratch for the
+// norms of x's rows and of both weights' (T + 2 ff floats; clamped, with g and u).
 cudaError_t launch_glu_gate_up(const GluParams& p, const uint16_t* x, int T, uint16_t* h, float* g, float* u,
-                               uint32_t* status, cudaStream_t s);
+                               float* norms, uint32_t* status, cudaStream_t s);
 // y = h Wd^T
 cudaError_t launch_glu_down(const GluParams& p, const uint16_t* h, int T, uint16_t* y, uint32_t* status,
                             cudaStream_t s);

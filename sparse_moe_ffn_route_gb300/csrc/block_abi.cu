@@ -47,22 +47,24 @@ int check_glu(const moe_glu_cfg_t* c) {
   return c->d_model % 8 || c->ff % 8 || c->d_model > kMaxInputs || c->ff > kMaxInputs ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// Workspace: status word | h [T, ff] (forward that keeps nothing) or dg, du [T, ff] | the
-// backward pass's counts and partial sums of split products.
+// Workspace: status word | h [T, ff] (forward that keeps nothing), norms (forward that keeps,
+// clamped) or dg, du [T, ff] | the backward pass's counts and partial sums of split products.
 struct GluLayout {
-  size_t status, h, dg, du, arrived, partial, total;
+  size_t status, h, norms, dg, du, arrived, partial, total;
 };
 
 GluLayout glu_layout(const moe_glu_cfg_t& c, int T) {
   const size_t a = align_up((size_t)T * c.ff * 2);
   GluLayout L;
   L.status = 0;
-  L.h = L.dg = 256;
+  L.h = L.norms = L.dg = 256;
   L.du = L.dg + a;
   L.arrived = L.du + a;
   const size_t split = (size_t)glu_split_tiles(c.d_model, c.ff, T);
   L.partial = L.arrived + (split ? align_up(kGluArrivedBytes) : 0);
   L.total = L.partial + split * kGluSplitBytes;
+  const size_t norms = c.act == MOE_ACT_CLAMPED_GLU ? align_up(((size_t)T + 2 * (size_t)c.ff) * 4) : 0;
+  if (L.total < L.norms + norms) L.total = L.norms + norms;
   return L;
 }
 
@@ -150,7 +152,7 @@ int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const mo
   }
   GluSaved sv{reinterpret_cast<uint16_t*>(base + L.h), nullptr, nullptr};
   if (saved) sv = saved_at(saved, saved_layout(*cfg, T));
-  BLOCK_CUDA(launch_glu_gate_up(p, xi, T, sv.h, sv.g, sv.u, status, s));
+  BLOCK_CUDA(launch_glu_gate_up(p, xi, T, sv.h, sv.g, sv.u, reinterpret_cast<float*>(base + L.norms), status, s));
   BLOCK_CUDA(launch_glu_down(p, sv.h, T, yo, status, s));
   return MOE_OK;
 }

@@ -116,11 +116,12 @@ struct GemmParams {
   GluAct act;
   float *g, *u;         // saved (kEpiGlu: written when non-null; kEpiDact: read)
   uint16_t* out2;       // kEpiDact: du (out: dg)
-  // kEpiGlu with g: clamp inputs nearer than `tau` to their border are computed again
-  // from these (the accumulation truncates: its error is about d / 16 steps of 2^-24)
+  // kEpiGlu, clamped, with g: clamp inputs nearer to their border than the sum may be off
+  // (see border_gap) are computed again from these; norm: of the rows of x, wg and wu
   const uint16_t *x, *wg, *wu;
   int d;
-  float tau;
+  const float* norm;    // [M] | [N] | [N]; null where nothing is settled
+  float gap;
   uint32_t* status;
   int clear_status;     // this is the call's first kernel
 };
@@ -397,9 +398,9 @@ __device__ __forceinline__ void two_sum(float& s, float& lost, float v) {
 }
 
 // x . w over k by the whole warp: the products of bf16 values are exact in fp32, and the
-// sum keeps what its roundings lose.
+// sums (four, whose additions do not wait for one another) keep what their roundings lose.
 __device__ __noinline__ float exact_dot(const uint16_t* x, const uint16_t* w, int k, int lane) {
-  float s = 0.f, lost = 0.f;
+  float s[4] = {}, lost[4] = {};
   for (int i = 8 * lane; i < k; i += 1024) {
     uint4 a[4], b[4];
 #pragma unroll
@@ -409,25 +410,50 @@ __device__ __noinline__ float exact_dot(const uint16_t* x, const uint16_t* w, in
       b[j] = in ? *reinterpret_cast<const uint4*>(w + i + 256 * j) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t av[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bv[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        two_sum(s, lost, __fmul_rn(bf16_lo(av[e]), bf16_lo(bv[e])));
-        two_sum(s, lost, __fmul_rn(bf16_hi(av[e]), bf16_hi(bv[e])));
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t av = e == 0 ? a[j].x : e == 1 ? a[j].y : e == 2 ? a[j].z : a[j].w;
+        const uint32_t bv = e == 0 ? b[j].x : e == 1 ? b[j].y : e == 2 ? b[j].z : b[j].w;
+        two_sum(s[j], lost[j], __fmul_rn(bf16_lo(av), bf16_lo(bv)));
+        two_sum(s[j], lost[j], __fmul_rn(bf16_hi(av), bf16_hi(bv)));
       }
-    }
+  }
+#pragma unroll
+  for (int j = 1; j < 4; ++j) {
+    two_sum(s[0], lost[0], s[j]);
+    lost[0] = __fadd_rn(lost[0], lost[j]);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    const float other = __shfl_xor_sync(0xffffffffu, s, o), l = __shfl_xor_sync(0xffffffffu, lost, o);
-    two_sum(s, lost, other);
-    lost = __fadd_rn(lost, l);
+    const float other = __shfl_xor_sync(0xffffffffu, s[0], o), l = __shfl_xor_sync(0xffffffffu, lost[0], o);
+    two_sum(s[0], lost[0], other);
+    lost[0] = __fadd_rn(lost[0], l);
   }
-  return __fadd_rn(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, lost, 0));
+  return __fadd_rn(__shfl_sync(0xffffffffu, s[0], 0), __shfl_sync(0xffffffffu, lost[0], 0));
 }
 
-// Values of a clamp's input within `tau` of its border, one per lane: computed again, so
+// How far the tensor cores' sum of x . w may be from the exact one near the clamp's border.
+// They truncate the sum at every step of 16 products, by at most 2^-23 of the larger of the
+// sum and the products.  By Cauchy and
+// Schwarz a sum S_i of the first i products is at most p_i = |x[:i]| |w[:i]|, and, since the
+// whole sum is near the limit L, at most L + q_i, q_i that of the products still to come;
+// p_i + q_i <= |x| |w|.  So |S_i| <= (|x| |w| + L) / 2, and all steps together are off by at
+// most (d / 16) 2^-24 (|x| |w| + L); `gap` is that factor, with 9 steps more for the rounding
+// of the norms and, in split tiles, of the parts' sum.  Measured at d 72 to 8192: at most 0.54
+// of it, where the first products alone make the sum (half of 2^-23 on average at each step),
+// 0.1 where large terms cancel, 0.006 for random operands.  (A fixed share of the limit, without
+// the norms, let values cross the border whose terms cancel, or with a limit below the
+// terms' size.)  Rows of zeros have no gap and no error.
+__device__ __forceinline__ float border_gap(const GemmParams& g, float x_norm, float w_norm) {
+  return g.gap * fmaf(x_norm, w_norm, x_norm > 0.f ? g.act.limit : 0.f);
+}
+
+// Whether v, at a distance from its border, is nearer than gap.  A gap that is infinite or NaN
+// belongs to a row or feature whose sums are, or leave fp32's range on the way.
+__device__ __forceinline__ bool nearer(float distance, float gap) { return distance < gap && gap < 3.0e38f; }
+
+// Values of a clamp's input nearer to its border than that, one per lane: computed again, so
 // that the backward pass takes the side that the exact value takes.  row0: the warp's
 // first row.
 __device__ __forceinline__ void settle(float& v, bool near, const uint16_t* x, const uint16_t* w, int k, int row0,
@@ -470,12 +496,14 @@ __device__ __forceinline__ void finish8(const GemmParams& g, const Problem& p, i
   const bool valid = m < p.M;
   const size_t blk = ((size_t)mb * (p.N / 4) + n / 4) * 128 + row;   // saved g, u: float4 index
   if (EPI == kEpiGlu) {
-    if (clamped && g.g) {
+    if (g.norm) {
+      const float xn = valid ? g.norm[m] : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const size_t f = (size_t)(n + i) * g.d;
-        settle(v[i], valid && fabsf(v[i] - g.act.limit) <= g.tau, g.x, g.wg + f, g.d, m - lane, lane);
-        settle(w[i], valid && fabsf(fabsf(w[i]) - g.act.limit) <= g.tau, g.x, g.wu + f, g.d, m - lane, lane);
+        settle(v[i], nearer(fabsf(v[i] - g.act.limit), border_gap(g, xn, g.norm[p.M + n + i])), g.x, g.wg + f, g.d, m - lane, lane);
+        settle(w[i], nearer(fabsf(fabsf(w[i]) - g.act.limit), border_gap(g, xn, g.norm[p.M + p.N + n + i])), g.x, g.wu + f,
+               g.d, m - lane, lane);
       }
     }
     if (!valid) return;
@@ -819,22 +847,30 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           }
       } else if (EPI == kEpiGlu) {
         const size_t blk = ((size_t)mb * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
+        const float xn = g.norm && valid ? g.norm[m] : 0.f;
         for (int c0 = 16 * par; c0 < cols; c0 += 32) {
           float v[16], w[16];
+          float wn = 0.f;   // lane i: the norm of gate's row of column i, 16 + i: of up's
+          if (g.norm && c0 + (lane & 15) < cols) {
+            wn = g.norm[p.M + (lane & 16 ? p.N : 0) + n0 + c0 + (lane & 15)];
+            if (!(wn < 3.0e38f)) wn = 0.f;   // its own sums are not finite; the widest gap is the others'
+          }
           tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), v, w);
           const int left = cols - c0;
-          if (clamped && g.g) {
-            const float lim = g.act.limit, tau = g.tau;
+          if (g.norm) {
+            // against the widest gap of the 32 columns first; columns past the last have none
+            const float lim = g.act.limit, top = border_gap(g, xn, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wn))));
             bool any = false;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) any |= fabsf(v[i] - lim) <= tau || fabsf(fabsf(w[i]) - lim) <= tau;
-            if (__any_sync(0xffffffffu, any && valid)) {
+            for (int i = 0; i < 16; ++i) any |= fabsf(v[i] - lim) < top || fabsf(fabsf(w[i]) - lim) < top;
+            if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const bool in = valid && i < left;
+                const float gn = __shfl_sync(0xffffffffu, wn, i), un = __shfl_sync(0xffffffffu, wn, 16 + i);
+                const bool in = i < left;
                 const size_t f = (size_t)(n0 + c0 + i) * g.d;
-                settle(v[i], in && fabsf(v[i] - lim) <= tau, g.x, g.wg + f, g.d, m - lane, lane);
-                settle(w[i], in && fabsf(fabsf(w[i]) - lim) <= tau, g.x, g.wu + f, g.d, m - lane, lane);
+                settle(v[i], in && nearer(fabsf(v[i] - lim), border_gap(g, xn, gn)), g.x, g.wg + f, g.d, m - lane, lane);
+                settle(w[i], in && nearer(fabsf(fabsf(w[i]) - lim), border_gap(g, xn, un)), g.x, g.wu + f, g.d, m - lane, lane);
               }
             }
           }
@@ -991,6 +1027,51 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
   if (CG == 2) cluster_sync();   // neither CTA leaves while the other's MMAs or arrivals may reach it
   tc::tc_fence_after();
   if (warp == 1) tmem_dealloc<CG>(tmem);
+}
+
+// ---------------------------------------------------------------- norms
+// out[r] = |row r| of x (rows of x first), wg and wu: a warp per row, bound by the reads.  A
+// sum of squares that leaves fp32's range, or comes near its smallest numbers, is formed again
+// from the row times 2^-80 or 2^80.  At 1001 x 2880 x 2880
+// it takes 9 us of a training step's 137 (39 MB).  Beside the gate/up kernel, in what that
+// leaves of an SM, it was no faster (4 warps of its own there and the settling left to the
+// backward pass, whose ring of g and u then stalls on it: 161 us).
+constexpr int kNormWarps = 8, kNormLoads = 6;
+__global__ void __launch_bounds__(kNormWarps * 32, 6) glu_norm_kernel(const uint16_t* x, const uint16_t* wg, const uint16_t* wu,
+                                                                      int T, int ff, int d, float* out) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long rows = T + 2LL * ff;
+  for (long long r = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5); r < rows; r += (long long)gridDim.x * kNormWarps) {
+    const uint16_t* row = r < T ? x + r * d : r < T + (long long)ff ? wg + (r - T) * d : wu + (r - T - ff) * d;
+    float by = 1.f, sum = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+      float s = 0.f;
+      for (int i = 8 * lane; i < d; i += 256 * kNormLoads) {
+        uint4 q[kNormLoads];
+#pragma unroll
+        for (int j = 0; j < kNormLoads; ++j)
+          q[j] = i + 256 * j < d ? *reinterpret_cast<const uint4*>(row + i + 256 * j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < kNormLoads; ++j) {
+          const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = bf16_lo(u[e]) * by, hi = bf16_hi(u[e]) * by;
+            s = fmaf(lo, lo, s);
+            s = fmaf(hi, hi, s);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      sum = s;
+      if (pass || (s > 1e-30f && s < 1e30f)) break;
+      by = s < 1.f ? 0x1p80f : 0x1p-80f;
+    }
+    if (lane == 0) out[r] = sqrtf(sum) / by;
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -1258,7 +1339,15 @@ bool set_problem(Problem& p, int cg, int tn, int M, int N, int K, const uint16_t
 }  // namespace
 
 cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uint16_t* h, float* sg, float* su,
-                               uint32_t* status, cudaStream_t s) {
+                               float* norms, uint32_t* status, cudaStream_t s) {
+  // Only what the backward pass will need to know: without it h is continuous at the border.
+  const bool settled = sg && w.act == MOE_ACT_CLAMPED_GLU;
+  if (settled) {
+    const long long blocks = (T + 2LL * w.ff + kNormWarps - 1) / kNormWarps, most = 6LL * sm_count();
+    const cudaError_t e = launch_pdl(glu_norm_kernel, dim3((unsigned)std::min(blocks, most)), dim3(kNormWarps * 32), 0, s, x,
+                                     w.gate, w.up, T, w.ff, w.d, norms);
+    if (e != cudaSuccess) return e;
+  }
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.n_problems = 1;
@@ -1285,9 +1374,8 @@ cudaError_t launch_glu_gate_up(const GluParams& w, const uint16_t* x, int T, uin
   g.wg = w.gate;
   g.wu = w.up;
   g.d = w.d;
-  // Measured for limit 7 and random operands: at most 5.4e-5 off at d 2880, 1.5e-4 at d
-  // 8192; tau is three times that (1.6e-4, 4.3e-4) and touches one value in 10^5.
-  g.tau = w.limit * (float)(w.d / 16 + 8) * 0x1p-23f;
+  g.norm = settled ? norms : nullptr;
+  g.gap = (float)(w.d / 16 + 9) * 0x1p-24f;
   g.status = status;
   g.clear_status = 1;
   return launch<kEpiGlu>(g, way, s);
