@@ -76,7 +76,8 @@ int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const mo
  * dx [T, d] bf16 or NULL; grads or any member of it NULL: not computed.  With many tokens
  * and few weights the sum over the tokens is cut into parts, and which cut is taken depends
  * on the outputs asked for (their last bits may, with it).  Gradients are written, not
- * added to.  T == 0 sets the weight gradients to zero. */
+ * added to.  No output may share memory with an input or another output
+ * (MOE_ERR_INVALID_ARG).  T == 0 sets the weight gradients to zero. */
 int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const moe_glu_weights_t* w,
                      const void* saved, size_t saved_bytes, const void* dy, void* dx,
                      const moe_glu_grads_t* grads, void* ws, size_t ws_bytes, void* stream);
@@ -156,7 +157,8 @@ typedef struct {
 } moe_w4_weights_t;
 
 /* y [T, n_out] bf16 from x [T, n_in] bf16.  Made for the few tokens of a decode step: the
- * weights are read once per 16 tokens.  Needs no workspace.  T == 0 is a no-op. */
+ * weights are read once per 16 tokens.  Needs no workspace.  y may not share memory with x
+ * (MOE_ERR_INVALID_ARG).  T == 0 is a no-op. */
 int moe_w4_linear(const moe_w4_cfg_t* cfg, const void* x, int32_t T, const moe_w4_weights_t* w, void* y,
                   void* stream);
 

@@ -25,6 +25,28 @@ bool aligned16(const P*... p) {
   return (((reinterpret_cast<uintptr_t>(p) & 15u) == 0) && ...);
 }
 
+// A buffer of a call.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+// Whether any of `out` shares a byte with any of `in` or with another of `out`.
+template <int NO, int NI>
+bool overlap(const Span (&out)[NO], const Span (&in)[NI]) {
+  auto share = [](const Span& a, const Span& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+    return p && q && p < q + b.bytes && q < p + a.bytes;
+  };
+  for (int i = 0; i < NO; ++i) {
+    for (const Span& b : in)
+      if (share(out[i], b)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (share(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 #define BLOCK_CUDA(call)                            \
   do {                                              \
     if ((call) != cudaSuccess) return MOE_ERR_CUDA; \
@@ -177,6 +199,12 @@ int moe_glu_backward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const m
   if (!aligned16(x, saved, dy, dx, ws)) return MOE_ERR_ALIGNMENT;
   const GluLayout L = glu_layout(*cfg, T);
   if (ws_bytes < L.total || saved_bytes < moe_glu_saved_bytes(cfg, T)) return MOE_ERR_WORKSPACE;
+  // The products run side by side in one launch: what one of them writes another still reads.
+  const size_t rows = (size_t)T * cfg->d_model * 2, matrix = (size_t)cfg->d_model * cfg->ff * 2;
+  const Span out[] = {{dx, rows}, {dw.gate, matrix}, {dw.up, matrix}, {dw.down, matrix}, {ws, L.total}};
+  const Span in[] = {{x, rows},          {dy, rows},         {w->gate, matrix},
+                     {w->up, matrix},    {w->down, matrix},  {saved, moe_glu_saved_bytes(cfg, T)}};
+  if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   const GluParams p = glu_params(*cfg, *w);
   char* base = static_cast<char*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(base + L.status);
@@ -247,6 +275,9 @@ int moe_w4_linear(const moe_w4_cfg_t* c, const void* x, int32_t T, const moe_w4_
   if (T == 0) return MOE_OK;
   if (!x || !y || !w || !w->codes || !w->scales) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x, y, w->codes, w->scales, w->zeros)) return MOE_ERR_ALIGNMENT;
+  // Every CTA reads all of x and writes its columns of y.
+  const Span out[] = {{y, (size_t)T * c->n_out * 2}}, in[] = {{x, (size_t)T * c->n_in * 2}};
+  if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   BLOCK_CUDA(launch_skinny_w4(*c, *w, static_cast<const uint16_t*>(x), T, static_cast<uint16_t*>(y),
                               static_cast<cudaStream_t>(stream)));
   return MOE_OK;
