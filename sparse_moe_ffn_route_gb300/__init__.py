@@ -221,6 +221,51 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+class _Launch:
+    """Where a call's work goes.  Inside, the tensors' device is current (the library launches
+    on the current one) and what is allocated belongs to the stream that was given, or to the
+    current one; ``stream`` is its handle.  On the way out the tensors passed to ``uses`` are
+    recorded on a given stream, so that the allocator, which knows only the stream that a
+    tensor was made on, gives none of them away before the work is done; ordering the streams
+    is left to the caller."""
+
+    __slots__ = ("stream", "_object", "_outer", "_context", "_tensors")
+
+    def __init__(self, stream, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError(f"a CUDA tensor is expected, not one on {device}")
+        self._object = block._stream_object(stream, device)
+        self._tensors = ()
+        if self._object is not None:
+            self._outer = torch.cuda.current_stream(device)
+            self._context = torch.cuda.stream(self._object)
+        else:
+            self._context = None if block._current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._context is not None:
+            self._context.__enter__()
+        self.stream = _stream(self._object)
+        return self
+
+    def uses(self, *tensors) -> None:
+        self._tensors = tensors
+
+    def __exit__(self, *error):
+        if self._object is not None and self._outer.cuda_stream != self.stream:
+            for t in self._tensors:
+                if t is not None:
+                    t.record_stream(self._object)
+                    t.record_stream(self._outer)
+        if self._context is not None:
+            self._context.__exit__(*error)
+
+
+def _parts(*structs):
+    """The tensors of a layer's weight structures."""
+    return [getattr(s, f.name) for s in structs if s is not None for f in dataclasses.fields(s)]
+
+
 def _check(status: int, where: str) -> None:
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -266,12 +311,14 @@ def moe_route(cfg: MoeCfg, x: torch.Tensor, router: Router, shared: Optional[Sha
     """Router only.  Returns (topk_ids int32 [T,k], topk_w fp32 [T,k], sgate | None, logits | None)."""
     T = x.shape[0]
     dev = x.device
-    topk_ids = torch.empty((T, cfg.top_k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, cfg.top_k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    ws = workspace(cfg, T, dev) if ws is None else ws
-    _check(_lib.moe_route(ctypes.byref(cfg), _ptr(x, "x"), T, ctypes.byref(_router(router)),
-                          _shared(shared), _ptr(topk_ids), _ptr(topk_w), _ptr(sgate), _ptr(logits),
-                          _ptr(ws), ws.numel(), _stream(stream)), "moe_route")
+    with _Launch(stream, dev) as at:
+        topk_ids = torch.empty((T, cfg.top_k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, cfg.top_k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+        ws = workspace(cfg, T, dev) if ws is None else ws
+        at.uses(x, topk_ids, topk_w, sgate, logits, ws, *_parts(router, shared))
+        _check(_lib.moe_route(ctypes.byref(cfg), _ptr(x, "x"), T, ctypes.byref(_router(router)),
+                              _shared(shared), _ptr(topk_ids), _ptr(topk_w), _ptr(sgate), _ptr(logits),
+                              _ptr(ws), ws.numel(), at.stream), "moe_route")
     return topk_ids, topk_w, sgate, logits
 
 
@@ -279,10 +326,12 @@ def moe_topk_from_logits(cfg: MoeCfg, logits: torch.Tensor, topk_ids=None, topk_
                          stream=None):
     T = logits.shape[0]
     dev = logits.device
-    topk_ids = torch.empty((T, cfg.top_k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, cfg.top_k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
-    _check(_lib.moe_topk_from_logits(ctypes.byref(cfg), _ptr(logits, "logits"), T, _ptr(topk_ids),
-                                     _ptr(topk_w), _stream(stream)), "moe_topk_from_logits")
+    with _Launch(stream, dev) as at:
+        topk_ids = torch.empty((T, cfg.top_k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, cfg.top_k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+        at.uses(logits, topk_ids, topk_w)
+        _check(_lib.moe_topk_from_logits(ctypes.byref(cfg), _ptr(logits, "logits"), T, _ptr(topk_ids),
+                                         _ptr(topk_w), at.stream), "moe_topk_from_logits")
     return topk_ids, topk_w
 
 
@@ -292,13 +341,15 @@ def moe_group_by_expert(cfg: MoeCfg, topk_ids: torch.Tensor, counts=None, offset
     T = topk_ids.shape[0]
     dev = topk_ids.device
     E = cfg.n_experts
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
-    perm = torch.empty(max(T * cfg.top_k, 1), dtype=torch.int32, device=dev) if perm is None else perm
-    ws = workspace(cfg, T, dev) if ws is None else ws
-    _check(_lib.moe_group_by_expert(ctypes.byref(cfg), _ptr(topk_ids, "topk_ids"), T, _ptr(counts, "counts"),
-                                    _ptr(offsets, "offsets"), _ptr(perm, "perm"), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "moe_group_by_expert")
+    with _Launch(stream, dev) as at:
+        counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
+        perm = torch.empty(max(T * cfg.top_k, 1), dtype=torch.int32, device=dev) if perm is None else perm
+        ws = workspace(cfg, T, dev) if ws is None else ws
+        at.uses(topk_ids, counts, offsets, perm, ws)
+        _check(_lib.moe_group_by_expert(ctypes.byref(cfg), _ptr(topk_ids, "topk_ids"), T, _ptr(counts, "counts"),
+                                        _ptr(offsets, "offsets"), _ptr(perm, "perm"), _ptr(ws), ws.numel(),
+                                        at.stream), "moe_group_by_expert")
     return counts, offsets, perm
 
 
@@ -307,14 +358,16 @@ def moe_ffn_forward(cfg: MoeCfg, x: torch.Tensor, router: Router, experts: Exper
                     stream=None) -> torch.Tensor:
     """The whole layer; returns y [T, d] (bf16, or fp32 when cfg.y_fp32)."""
     T = x.shape[0]
-    if y is None:
-        y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
-                        device=x.device)
-    ws = workspace(cfg, T, x.device) if ws is None else ws
-    _check(_lib.moe_ffn_forward(ctypes.byref(cfg), _ptr(x, "x"), T, ctypes.byref(_router(router)),
-                                ctypes.byref(_experts(experts)), _shared(shared), _ptr(y, "y"),
-                                _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(),
-                                _stream(stream)), "moe_ffn_forward")
+    with _Launch(stream, x.device) as at:
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
+                            device=x.device)
+        ws = workspace(cfg, T, x.device) if ws is None else ws
+        at.uses(x, y, topk_ids, topk_w, ws, *_parts(router, experts, shared))
+        _check(_lib.moe_ffn_forward(ctypes.byref(cfg), _ptr(x, "x"), T, ctypes.byref(_router(router)),
+                                    ctypes.byref(_experts(experts)), _shared(shared), _ptr(y, "y"),
+                                    _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(),
+                                    at.stream), "moe_ffn_forward")
     return y
 
 
@@ -333,14 +386,16 @@ def moe_ffn_forward_noalloc(cfg: MoeCfg, x: torch.Tensor, router: Router, expert
     device array (NOALLOC_WORKSPACE_BYTES) serves as workspace (see include/moe.h).  Only
     `y` is allocated here when it is not passed in."""
     T = x.shape[0]
-    if y is None:
-        y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
-                        device=x.device)
-    _check(_lib.moe_ffn_forward_noalloc(ctypes.byref(cfg), _ptr(x, "x"), T,
-                                        ctypes.byref(_router(router)),
-                                        ctypes.byref(_experts(experts)), _shared(shared),
-                                        _ptr(y, "y"), _ptr(topk_ids), _ptr(topk_w),
-                                        _stream(stream)), "moe_ffn_forward_noalloc")
+    with _Launch(stream, x.device) as at:
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
+                            device=x.device)
+        at.uses(x, y, topk_ids, topk_w, *_parts(router, experts, shared))
+        _check(_lib.moe_ffn_forward_noalloc(ctypes.byref(cfg), _ptr(x, "x"), T,
+                                            ctypes.byref(_router(router)),
+                                            ctypes.byref(_experts(experts)), _shared(shared),
+                                            _ptr(y, "y"), _ptr(topk_ids), _ptr(topk_w),
+                                            at.stream), "moe_ffn_forward_noalloc")
     return y
 
 
@@ -348,14 +403,16 @@ def moe_ffn_forward_routed(cfg: MoeCfg, x: torch.Tensor, topk_ids: torch.Tensor,
                            topk_w: torch.Tensor, experts: Experts, shared: Optional[Shared] = None,
                            sgate=None, y=None, ws=None, stream=None) -> torch.Tensor:
     T = x.shape[0]
-    if y is None:
-        y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
-                        device=x.device)
-    ws = workspace(cfg, T, x.device) if ws is None else ws
-    _check(_lib.moe_ffn_forward_routed(ctypes.byref(cfg), _ptr(x, "x"), T, _ptr(topk_ids),
-                                       _ptr(topk_w), _ptr(sgate), ctypes.byref(_experts(experts)),
-                                       _shared(shared), _ptr(y, "y"), _ptr(ws), ws.numel(),
-                                       _stream(stream)), "moe_ffn_forward_routed")
+    with _Launch(stream, x.device) as at:
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16,
+                            device=x.device)
+        ws = workspace(cfg, T, x.device) if ws is None else ws
+        at.uses(x, topk_ids, topk_w, sgate, y, ws, *_parts(experts, shared))
+        _check(_lib.moe_ffn_forward_routed(ctypes.byref(cfg), _ptr(x, "x"), T, _ptr(topk_ids),
+                                           _ptr(topk_w), _ptr(sgate), ctypes.byref(_experts(experts)),
+                                           _shared(shared), _ptr(y, "y"), _ptr(ws), ws.numel(),
+                                           at.stream), "moe_ffn_forward_routed")
     return y
 
 
@@ -368,11 +425,13 @@ def moe_ffn_forward_host(cfg: MoeCfg, x_host: torch.Tensor, router: Router, expe
     T = x_host.shape[0]
     if y_host is None:
         y_host = torch.empty(x_host.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16)
-    ws = workspace(cfg, T) if ws is None else ws
-    _check(_lib.moe_ffn_forward_host(ctypes.byref(cfg), x_host.data_ptr(), T,
-                                     ctypes.byref(_router(router)), ctypes.byref(_experts(experts)),
-                                     _shared(shared), y_host.data_ptr(), _ptr(ws), ws.numel(),
-                                     _stream(stream)), "moe_ffn_forward_host")
+    with _Launch(stream, router.w.device) as at:
+        ws = workspace(cfg, T, router.w.device) if ws is None else ws
+        at.uses(ws, *_parts(router, experts, shared))
+        _check(_lib.moe_ffn_forward_host(ctypes.byref(cfg), x_host.data_ptr(), T,
+                                         ctypes.byref(_router(router)), ctypes.byref(_experts(experts)),
+                                         _shared(shared), y_host.data_ptr(), _ptr(ws), ws.numel(),
+                                         at.stream), "moe_ffn_forward_host")
     return y_host
 
 
@@ -392,16 +451,22 @@ class BoundForwardHost:
         T = x_host.shape[0]
         if y_host is None:
             y_host = torch.empty(x_host.shape, dtype=torch.float32 if cfg.y_fp32 else torch.bfloat16)
-        self.ws = workspace(cfg, T) if ws is None else ws
+        with _Launch(stream, router.w.device) as at:
+            self.ws = workspace(cfg, T, router.w.device) if ws is None else ws
         self.cfg, self.x_host, self.y_host = cfg, x_host, y_host
         self._keep = (router, experts, shared, _router(router), _experts(experts))
         self._args = (ctypes.byref(cfg), x_host.data_ptr(), T, ctypes.byref(self._keep[3]),
                       ctypes.byref(self._keep[4]), _shared(shared), y_host.data_ptr(), _ptr(self.ws),
-                      self.ws.numel(), _stream(stream))
+                      self.ws.numel(), at.stream)
         self._fn = _lib.moe_ffn_forward_host
+        self._device = router.w.device.index
 
     def __call__(self) -> torch.Tensor:
-        st = self._fn(*self._args)
+        if block._current_device() == self._device:
+            st = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                st = self._fn(*self._args)
         if st != MOE_OK:
             raise MoeError(st, "moe_ffn_forward_host")
         return self.y_host
@@ -412,10 +477,12 @@ def moe_mxfp4_to_bf16(blocks: torch.Tensor, scales: torch.Tensor, out=None,
     """blocks u8 [..., n_in/32, 16], scales u8 [..., n_in/32] -> bf16 [..., n_in]."""
     nb = blocks.shape[-2]
     rows = blocks.numel() // (nb * 16)
-    out = torch.empty(tuple(blocks.shape[:-2]) + (nb * 32,), dtype=torch.bfloat16,
-                      device=blocks.device) if out is None else out
-    _check(_lib.moe_mxfp4_to_bf16(_ptr(blocks, "blocks"), _ptr(scales, "scales"), rows, nb * 32,
-                                  _ptr(out, "out"), _stream(stream)), "moe_mxfp4_to_bf16")
+    with _Launch(stream, blocks.device) as at:
+        out = torch.empty(tuple(blocks.shape[:-2]) + (nb * 32,), dtype=torch.bfloat16,
+                          device=blocks.device) if out is None else out
+        at.uses(blocks, scales, out)
+        _check(_lib.moe_mxfp4_to_bf16(_ptr(blocks, "blocks"), _ptr(scales, "scales"), rows, nb * 32,
+                                      _ptr(out, "out"), at.stream), "moe_mxfp4_to_bf16")
     return out
 
 
@@ -480,5 +547,6 @@ from .block import (BoundCall, GluCfg, GluGrads, GluWeights, NormCfg, NormGrads,
                     moe_glu_backward, moe_glu_forward, moe_glu_saved_bytes, moe_glu_workspace_bytes,
                     moe_w4_linear, norm_cfg, w4_cfg, w4_quantize)
 from .block import EXPORTED as _BLOCK_EXPORTED  # noqa: E402
+from . import block  # noqa: E402
 
 EXPORTED += _BLOCK_EXPORTED

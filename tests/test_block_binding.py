@@ -81,11 +81,12 @@ class World:
                 self.stream = stream
 
             def __enter__(self):
-                self.before = world.current[self.stream.device.index]
-                world.current[self.stream.device.index] = self.stream
+                at = self.stream.device.index
+                self.before = world.current[at], world.selected
+                world.current[at], world.selected = self.stream, at
 
             def __exit__(self, *_):
-                world.current[self.stream.device.index] = self.before
+                world.current[self.stream.device.index], world.selected = self.before
 
         self.using = using
 
@@ -101,7 +102,7 @@ class World:
                 world.selected = self.before
 
         def current_stream(device=None):
-            return self.current[getattr(device, "index", device) or 0]
+            return self.current[self.selected if device is None else getattr(device, "index", device)]
 
         cuda = types.SimpleNamespace(Stream=Stream, stream=using, device=selecting, current_stream=current_stream,
                                      current_device=lambda: self.selected,
