@@ -70,7 +70,8 @@ int moe_glu_forward(const moe_glu_cfg_t* cfg, const void* x, int32_t T, const mo
 
 /* Gradients of moe_glu_forward, from the same x and w, its saved buffer and dy [T, d] bf16:
  *   dh = dy Wd;  dg = dh dact/dg;  du = dh dact/du  (0 where a clamp holds the value, its
- *   one-sided derivative 1 at the border itself);
+ *   one-sided derivative 1 at the border itself; a g or u so near the border that its sum's
+ *   rounding could decide is summed again with compensation by the forward pass);
  *   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dWd = dy^T h.
  * dh stays in fp32; dg and du are rounded to bf16 for the products that follow.
  * dx [T, d] bf16 or NULL; grads or any member of it NULL: not computed.  With many tokens

@@ -25,8 +25,8 @@
 // its columns' weight gradients in registers over all its rows; the groups add theirs up
 // and the CTA writes one row of partial sums, which a second kernel adds in order.
 //
-// Measured: forward 8192 x 2880 29.6 us in the kernel, 33.5 a call (189 MB, 83% of a copy's
-// rate); backward 8192 x 2048 47.4 us (201 MB, 4.2 TB/s), bound by issue: about 3500
+// Measured: forward 8192 x 2880 29.7 us in the kernel, 33.3 a call (189 MB, 83% of a copy's
+// rate); backward 8192 x 2048 47.7 us (201 MB, 4.2 TB/s), bound by issue: about 3500
 // instructions a row.
 #include "block.h"
 #include "common.cuh"

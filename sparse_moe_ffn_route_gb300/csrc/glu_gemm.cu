@@ -3,7 +3,9 @@
 // accumulators in TMEM, fed by TMA through an mbarrier ring.
 //
 //   gate/up:  g = x Wg^T, u = x Wu^T in one tile (the B tile holds tn / 2 rows of each), so
-//             that the epilogue has both and writes h = act(g, u) (and, in training, g, u)
+//             that the epilogue has both and writes h = act(g, u) (and, in training, g, u;
+//             clamped ones near the border are settled there, with the rows' norms of a
+//             launch before)
 //   down:     y = h Wd^T
 //   dact:     dh = dy Wd, whose epilogue turns it into dg and du with the saved g and u
 //             (dh never reaches memory and is never rounded)
@@ -43,9 +45,9 @@
 // would otherwise be paid at every chunk.  Every wait is bounded (see tc::mbar_wait).
 //
 // Measured at 8192 tokens, d 2048, ff 8192 (tensor cores under the power limit; a library's
-// bf16 product reaches 1.87 PFLOP/s): gate/up 276 us (1.99 PFLOP/s; 322 with g and u kept,
-// 0.5 GB), down 162 us (1.70: 256 tiles on 76 pairs), dact 211 us, grads with dWd 707 us
-// (1.94).  At 4096, 2048, 512 the four launches take 20, 14, 19 and 33 us: one wave each,
+// bf16 product reaches 1.87 PFLOP/s): gate/up 280 us (1.96 PFLOP/s; 325 with g and u kept,
+// 0.5 GB), down 165 us (1.67: 256 tiles on 76 pairs), dact 211 us, grads with dWd 724 us
+// (1.90).  At 4096, 2048, 512 the four launches take 20, 14, 19 and 32 us: one wave each,
 // bound by the first loads' latency and the open epilogue.
 #include <cuda.h>
 
@@ -1202,7 +1204,7 @@ constexpr int kMaxParts = 8, kMaxSplit = 152;
 // is least.  A long launch (kLongClocks: 100 us) runs against the power limit, where what
 // the last wave leaves idle speeds the others up: there only the tiles count (8192 x
 // 2048 x 8192 forward with y in pairs' tiles of 256 columns, 3.4 waves: 485 us, of 192, 4.6
-// waves: 493 us).  A part of a split tile pays for the exchange (two parts of 128 columns 2.7 us,
+// waves: 493 us; no more apart than two boxes are, so the rule is a weak one).  A part of a split tile pays for the exchange (two parts of 128 columns 2.7 us,
 // of 32 columns 1.3 us).
 constexpr long long kLongClocks = 200000;
 Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = nullptr) {

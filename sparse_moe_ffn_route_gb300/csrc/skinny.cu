@@ -25,7 +25,7 @@
 // bits of 128.0 (128 + q is exact in bf16), from which 128 + zero is subtracted exactly;
 // the scale multiplies each group's fp32 partial sum, so no product is rounded early.
 //
-// Measured: bf16, 8 tokens, 4096 x 12288 forward 53.4 us for 302 MB (5.65 TB/s, 83% of a
+// Measured: bf16, 8 tokens, 4096 x 12288 forward 53.3 us for 302 MB (5.67 TB/s, 83% of a
 // copy's rate).  4 bits, 16 tokens, 4096 x 32768: 30.4 us for 74 MB (2.4 TB/s), bound by
 // issue, integer and MMA work of about 8 us each that overlap poorly (23 us without the
 // MMAs); 1 token, 2048 x 512 gated: 3.7 us, the host's launch.
