@@ -437,16 +437,17 @@ __device__ __noinline__ float exact_dot(const uint16_t* x, const uint16_t* w, in
 
 // How far the tensor cores' sum of x . w may be from the exact one near the clamp's border.
 // They truncate the sum at every step of 16 products, by at most 2^-23 of the larger of the
-// sum and the products.  By Cauchy and
-// Schwarz a sum S_i of the first i products is at most p_i = |x[:i]| |w[:i]|, and, since the
-// whole sum is near the limit L, at most L + q_i, q_i that of the products still to come;
-// p_i + q_i <= |x| |w|.  So |S_i| <= (|x| |w| + L) / 2, and all steps together are off by at
-// most (d / 16) 2^-24 (|x| |w| + L); `gap` is that factor, with 9 steps more for the rounding
-// of the norms and, in split tiles, of the parts' sum.  Measured at d 72 to 8192: at most 0.54
-// of it, where the first products alone make the sum (half of 2^-23 on average at each step),
-// 0.1 where large terms cancel, 0.006 for random operands.  (A fixed share of the limit, without
-// the norms, let values cross the border whose terms cancel, or with a limit below the
-// terms' size.)  Rows of zeros have no gap and no error.
+// sum and the products (taken from measurements: the instruction's documents leave the
+// rounding open).  By Cauchy and Schwarz a sum S_i of the first i products is at most
+// p_i = |x[:i]| |w[:i]|, and, since the whole sum is near the limit L, at most L + q_i, q_i
+// that of the products still to come; p_i + q_i <= |x| |w|.  So |S_i| <= (|x| |w| + L) / 2, and
+// all steps together are off by at most (d / 16) 2^-24 (|x| |w| + L); `gap` is that factor,
+// with 9 steps more for the rounding of the norms and, in split tiles, of the parts' sum.
+// Measured at d 72 to 8192: at most 0.54 of it, where the first products alone make the sum
+// (half of 2^-23 on average at each step), 0.26 for terms of one sign, 0.13 where large terms
+// cancel, 0.08 for random operands (0.006 at d 2880).  A fixed share of the limit, without the
+// norms, let values cross the border whose terms cancel, or with a limit below the terms'
+// size.  Rows of zeros have no gap and no error.
 __device__ __forceinline__ float border_gap(const GemmParams& g, float x_norm, float w_norm) {
   return g.gap * fmaf(x_norm, w_norm, x_norm > 0.f ? g.act.limit : 0.f);
 }
@@ -1034,10 +1035,10 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
 // ---------------------------------------------------------------- norms
 // out[r] = |row r| of x (rows of x first), wg and wu: a warp per row, bound by the reads.  A
 // sum of squares that leaves fp32's range, or comes near its smallest numbers, is formed again
-// from the row times 2^-80 or 2^80.  At 1001 x 2880 x 2880
-// it takes 9 us of a training step's 137 (39 MB).  Beside the gate/up kernel, in what that
-// leaves of an SM, it was no faster (4 warps of its own there and the settling left to the
-// backward pass, whose ring of g and u then stalls on it: 161 us).
+// from the row times 2^-80 or 2^80.  At 1001 x 2880 x 2880 it takes 10 us of a training step's
+// 138 (39 MB).  As four more warps of the gate/up kernel it cost nothing, but came too late
+// for that kernel's epilogue, and settled in the backward pass, whose ring of g and u then
+// stalls, the step took 161 us.
 constexpr int kNormWarps = 8, kNormLoads = 6;
 __global__ void __launch_bounds__(kNormWarps * 32, 6) glu_norm_kernel(const uint16_t* x, const uint16_t* wg, const uint16_t* wu,
                                                                       int T, int ff, int d, float* out) {
