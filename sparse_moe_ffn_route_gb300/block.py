@@ -165,19 +165,20 @@ class BoundCall:
     or ``grads`` that is replaced later does not count).  The tensors stay alive as long as
     the object, and their memory until the streams that it was called on are done with it."""
 
-    __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream", "_tensors", "_seen")
+    __slots__ = ("_fn", "_args", "_out", "_keep", "_where", "_device", "_stream", "_tensors", "_here", "_seen", "_only")
 
     def __init__(self, where, args, out, keep, tensors, device, stream):
         self._fn, self._where = getattr(_lib, where), where
         self._args, self._out, self._keep = args, out, (keep, stream)
         self._tensors = [t for t in tensors if t is not None]
         self._device = device.index
+        self._only = torch.cuda.device_count() == 1   # then it is the current one
         self._stream = None if stream is None else stream.cuda_stream
         # streams whose work the allocator knows to use the tensors: the current one owns
         # them, or, beside one that is given, is where the caller will use the outputs
-        here = _current_handle(device)
-        self._seen = {here}
-        if stream is not None and self._stream != here:
+        self._here = _current_handle(device)
+        self._seen = {self._here}
+        if stream is not None and self._stream != self._here:
             self._record(self._stream, stream)
             for t in self._tensors:
                 t.record_stream(torch.cuda.current_stream(device))
@@ -191,9 +192,9 @@ class BoundCall:
         stream = self._stream
         if stream is None:
             stream = (_raw_stream or _current_stream)(self._device)
-            if stream not in self._seen:
+            if stream != self._here and stream not in self._seen:
                 self._record(stream, torch.cuda.current_stream(self._device))
-        if _current_device() == self._device:
+        if self._only or _current_device() == self._device:
             status = self._fn(*self._args, stream)
         else:   # the library launches on the current device
             with torch.cuda.device(self._device):

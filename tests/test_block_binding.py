@@ -105,7 +105,7 @@ class World:
             return self.current[self.selected if device is None else getattr(device, "index", device)]
 
         cuda = types.SimpleNamespace(Stream=Stream, stream=using, device=selecting, current_stream=current_stream,
-                                     current_device=lambda: self.selected,
+                                     current_device=lambda: self.selected, device_count=lambda: 2,
                                      default_stream=lambda d=None: Stream(0, d or DEVICE),
                                      ExternalStream=lambda h, device=DEVICE: Stream(h, device))
 
