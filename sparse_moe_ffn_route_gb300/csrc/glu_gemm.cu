@@ -826,6 +826,20 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         if (EPI == kEpiDact && blockIdx.x == 0)
           for (int i = threadIdx.x - 64; i < g.zeros; i += 32 * kEpiWarps) g.arrived[i] = 0u;
       }
+      // The norms that the border's gaps depend on, asked for under the tile's MMAs: of this
+      // lane's row of x, and of this warp's chunks of columns (at most 4) of gate's row of
+      // column i in lane i, of up's in lane 16 + i.  A feature whose own sums are not finite
+      // has none, so that the widest gap is the others'.
+      float xn = 0.f, wn[4] = {};
+      if (EPI == kEpiGlu && !SPLIT && g.norm) {
+        if (valid) xn = g.norm[m];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 16 * par + 32 * k + (lane & 15);
+          const float n = c < cols ? g.norm[p.M + (lane & 16 ? p.N : 0) + n0 + c] : 0.f;
+          wn[k] = n < 3.0e38f ? n : 0.f;
+        }
+      }
       if (!warp_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       if (SPLIT) {
@@ -850,26 +864,20 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           }
       } else if (EPI == kEpiGlu) {
         const size_t blk = ((size_t)mb * (p.N / 4) + n0 / 4) * 128 + row;   // saved g, u: float4 index
-        const float xn = g.norm && valid ? g.norm[m] : 0.f;
         for (int c0 = 16 * par; c0 < cols; c0 += 32) {
           float v[16], w[16];
-          float wn = 0.f;   // lane i: the norm of gate's row of column i, 16 + i: of up's
-          if (g.norm && c0 + (lane & 15) < cols) {
-            wn = g.norm[p.M + (lane & 16 ? p.N : 0) + n0 + c0 + (lane & 15)];
-            if (!(wn < 3.0e38f)) wn = 0.f;   // its own sums are not finite; the widest gap is the others'
-          }
           tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), v, w);
           const int left = cols - c0;
           if (g.norm) {
-            // against the widest gap of the 32 columns first; columns past the last have none
-            const float lim = g.act.limit, top = border_gap(g, xn, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wn))));
+            // against the widest gap of the 32 columns first
+            const float lim = g.act.limit, top = border_gap(g, xn, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wn[0]))));
             bool any = false;
 #pragma unroll
             for (int i = 0; i < 16; ++i) any |= fabsf(v[i] - lim) < top || fabsf(fabsf(w[i]) - lim) < top;
             if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float gn = __shfl_sync(0xffffffffu, wn, i), un = __shfl_sync(0xffffffffu, wn, 16 + i);
+                const float gn = __shfl_sync(0xffffffffu, wn[0], i), un = __shfl_sync(0xffffffffu, wn[0], 16 + i);
                 const bool in = i < left;
                 const size_t f = (size_t)(n0 + c0 + i) * g.d;
                 settle(v[i], in && nearer(fabsf(v[i] - lim), border_gap(g, xn, gn)), g.x, g.wg + f, g.d, m - lane, lane);
@@ -877,6 +885,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
               }
             }
           }
+          wn[0] = wn[1], wn[1] = wn[2], wn[2] = wn[3];   // the next chunk's
           if (valid) {
             if (g.g) {
 #pragma unroll
