@@ -549,4 +549,17 @@ from .block import (BoundCall, GluCfg, GluGrads, GluWeights, NormCfg, NormGrads,
 from .block import EXPORTED as _BLOCK_EXPORTED  # noqa: E402
 from . import block  # noqa: E402
 
-EXPORTED += _BLOCK_EXPORTED
+# ----------------------------------------------------------------------------- linear layer, exchange
+from .linear import (LINEAR_BF16, LINEAR_E4M3, LINEAR_GELU, LINEAR_GELU_TANH, LINEAR_NONE, LINEAR_SILU,  # noqa: E402,F401
+                     LinearCfg, LinearGrads, LinearWeights, bind_block_norm_quant, bind_linear_backward,
+                     bind_linear_forward, linear_cfg, linear_pre, linear_workspace, moe_block_norm_quant,
+                     moe_linear_backward, moe_linear_forward, moe_linear_workspace_bytes, w8_quantize)
+from .linear import EXPORTED as _LINEAR_EXPORTED  # noqa: E402
+from .exchange import (ROWS_BF16, ROWS_E4M3, Dispatched, ExchangeCfg, bind_combine_backward,  # noqa: E402,F401
+                       bind_combine_forward, bind_dispatch_backward, bind_dispatch_forward, dispatch_workspace,
+                       exchange_cfg, moe_combine_backward, moe_combine_forward, moe_dispatch_backward,
+                       moe_dispatch_forward, moe_dispatch_workspace_bytes)
+from .exchange import EXPORTED as _EXCHANGE_EXPORTED  # noqa: E402
+from . import exchange, linear  # noqa: E402
+
+EXPORTED += _BLOCK_EXPORTED + _LINEAR_EXPORTED + _EXCHANGE_EXPORTED

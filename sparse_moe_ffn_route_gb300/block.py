@@ -183,6 +183,11 @@ class BoundCall:
             for t in self._tensors:
                 t.record_stream(torch.cuda.current_stream(device))
 
+    @property
+    def out(self):
+        """The output tensors that every call returns."""
+        return self._out
+
     def _record(self, handle, stream):
         for t in self._tensors:
             t.record_stream(stream)

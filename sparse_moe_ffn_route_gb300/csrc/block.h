@@ -2,7 +2,7 @@
 // kernel translation units.
 #pragma once
 
-#include "../../include/moe_block.h"
+#include "../../include/moe_linear.h"
 #include "internal.h"
 #include "per_device.h"
 
@@ -75,9 +75,37 @@ cudaError_t launch_skinny_bf16(const uint16_t* w0, const uint16_t* w1, int n_out
 cudaError_t launch_skinny_w4(const moe_w4_cfg_t& c, const moe_w4_weights_t& w, const uint16_t* x, int T, uint16_t* y,
                              cudaStream_t s);
 
+// The linear layer (moe_linear.h).
+struct LinearEpi;   // linear_act.cuh
+struct LinearShape {
+  int n_in, n_out;
+  bool eight;       // operands in e4m3
+};
+// Many tokens (glu_gemm.cu): y = act(x W^T ...) as epi says.
+cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
+                               uint32_t* status, cudaStream_t s);
+// At most 16 tokens at a time (skinny.cu): the same.
+cudaError_t launch_linear_skinny(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
+                                 uint32_t* clear_status, cudaStream_t s);
+// Room for a weight gradient whose tokens several units share, as glu_split_tiles; whether a
+// backward pass does share them (split.arrived has to be zero before it).
+int linear_split_tiles(int n_in, int n_out, int T);
+bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw);
+// dx = dv W, dW = dv^T x, each where its pointer is non-null (one of them is).
+cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
+                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, uint32_t* status, cudaStream_t s);
+// dv = dy act'(pre) (dv null: not written), dbias = the sum of its rows (null: not computed;
+// parts: linear_bias_parts(n, T) x n floats); clears *status and `zeros` words at `clear`.
+int linear_bias_parts(int n, int T);
+cudaError_t launch_linear_dv(int act, const uint16_t* dy, const uint16_t* pre, int T, int n, uint16_t* dv, uint16_t* dbias,
+                             float* parts, uint32_t* status, uint32_t* clear, int zeros, cudaStream_t s);
+
 // Norms (block_norm.cu).
 cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y,
                                   uint16_t* a, cudaStream_t s);
+// The same with a in e4m3 and a scale per row; without pre_w a = y.
+cudaError_t launch_block_norm_quant(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y, uint8_t* q,
+                                    float* scale, cudaStream_t s);
 int block_norm_parts(int T);   // rows of the weight gradients' partial sums
 cudaError_t launch_block_norm_bwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, const uint16_t* dy,
                                   const uint16_t* da, const moe_norm_grads_t& g, float* parts, cudaStream_t s);

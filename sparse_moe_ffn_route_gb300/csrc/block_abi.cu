@@ -2,6 +2,7 @@
 // workspace carving and the launch sequence of each entry point.
 #include <cmath>
 
+#include "abi_check.h"
 #include "block.h"
 
 using namespace moe;
@@ -11,41 +12,6 @@ namespace {
 // Tokens up to which a forward pass that keeps nothing streams the weights through warp
 // MMAs (16 tokens a pass) instead of tcgen05 tiles of 128 token rows.
 constexpr int kSkinnyTokens = 16;
-
-// The kernels count rows and columns in 32 bits and step a whole grid's rows (norms: 3 rows
-// ahead of up to 2432 groups of threads) or a row's bytes (skinny.cu: 2 per input) past the
-// last one before they compare.  These bounds keep every such sum below 2^31.
-constexpr int kMaxTokens = 1 << 30, kMaxInputs = 1 << 29, kMaxOutputs = 1 << 30;
-
-size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
-
-// Null or 16-byte aligned.
-template <typename... P>
-bool aligned16(const P*... p) {
-  return (((reinterpret_cast<uintptr_t>(p) & 15u) == 0) && ...);
-}
-
-// A buffer of a call.
-struct Span {
-  const void* at;
-  size_t bytes;
-};
-
-// Whether any of `out` shares a byte with any of `in` or with another of `out`.
-template <int NO, int NI>
-bool overlap(const Span (&out)[NO], const Span (&in)[NI]) {
-  auto share = [](const Span& a, const Span& b) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
-    return p && q && p < q + b.bytes && q < p + a.bytes;
-  };
-  for (int i = 0; i < NO; ++i) {
-    for (const Span& b : in)
-      if (share(out[i], b)) return true;
-    for (int j = i + 1; j < NO; ++j)
-      if (share(out[i], out[j])) return true;
-  }
-  return false;
-}
 
 #define BLOCK_CUDA(call)                            \
   do {                                              \
@@ -57,8 +23,6 @@ int check_act(int act, float limit, float alpha) {
   if (!std::isfinite(limit) || !std::isfinite(alpha) || limit < 0.f) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
-
-int check_tokens(int T) { return T < 0 ? MOE_ERR_INVALID_ARG : T > kMaxTokens ? MOE_ERR_UNSUPPORTED : MOE_OK; }
 
 int check_glu(const moe_glu_cfg_t* c) {
   if (!c || c->d_model <= 0 || c->ff <= 0) return MOE_ERR_INVALID_ARG;

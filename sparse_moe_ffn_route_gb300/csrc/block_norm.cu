@@ -131,6 +131,8 @@ struct NormArgs {
   float eps, rs, bs;
   // forward
   uint16_t *y, *a;
+  uint8_t* q;            // a in 8 bits, with a scale per row
+  float* scale;
   // backward
   const uint16_t *dy, *da;
   uint16_t *dx, *dz;
@@ -172,12 +174,56 @@ struct Ahead {
   __device__ __forceinline__ uint4 get(int slot, int a, int i) const { return mine[((slot * NA + a) * V + i) * n]; }
 };
 
-// Z: there is a branch; POST: with a norm; PRE: with the next block's norm (a).
-template <int V, int DEPTH, bool Z, bool POST, bool PRE>
+// Sum of `sum` and maximum of `most` over the CTA, in every thread; `buf` as in cta_sum<2>
+// (slots past the last warp hold zeros, and `most` is not negative).
+__device__ __forceinline__ void cta_sum_max(float& sum, float& most, float* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));   // ordered as the values
+  if (lane == 0) {
+    buf[warp] = sum;
+    buf[kMaxWarps + warp] = most;
+  }
+  __syncthreads();
+  sum = most = 0.f;
+  for (int w = 0; w < nw; w += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(buf + w), m = *reinterpret_cast<const float4*>(buf + kMaxWarps + w);
+    sum += (q.x + q.y) + (q.z + q.w);
+    most = fmaxf(fmaxf(most, fmaxf(m.x, m.y)), fmaxf(m.z, m.w));
+  }
+}
+
+// 8 values times m as e4m3 (to nearest even; past 448 the largest value, NaN stays NaN).
+// EXACT: m is 1 / scale, and the quotient is corrected by its remainder, which rounds as the
+// division itself does (Markstein): rows of bf16 values have many quotients just halfway between
+// two codes, and 2 in 1000 fell on the other side.
+template <bool EXACT>
+__device__ __forceinline__ uint2 pack_e4m3x8(const F2 (&v)[4], F2 m, F2 minus_scale) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    F2 t = mul2(v[i], m);
+    if (EXACT) t = fma2(fma2(t, minus_scale, v[i]), m, t);
+    split(t, lo, hi);
+    uint16_t p;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(hi), "f"(lo));
+    u[i] = p;
+  }
+  return make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
+}
+
+// Z: there is a branch; POST: with a norm; PRE: with the next block's norm (a); EIGHT: a in
+// e4m3 with its row's scale.  There a row's scale is r max|y pre_w| / 448, r the row's 1 / rms:
+// the maximum is taken beside the sum of y^2, in the same exchange, and one factor per row
+// takes y pre_w to the codes.
+template <int V, int DEPTH, bool Z, bool POST, bool PRE, bool EIGHT>
 __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __grid_constant__ NormArgs g) {
   extern __shared__ uint4 rows[];
-  __shared__ __align__(16) float buf[2][2][kMaxWarps];
-  for (int i = threadIdx.x; i < 4 * kMaxWarps; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  // row parity, exchange (the second one may be of two values)
+  __shared__ __align__(16) float buf[2][3][kMaxWarps];
+  for (int i = threadIdx.x; i < 6 * kMaxWarps; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
   pdl_wait();
   __syncthreads();
   const int d = g.d, T = g.T;
@@ -233,7 +279,35 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
     }
     ahead.start(slot, src, t + DEPTH * (int)gridDim.x, T, d);
     if (++slot == DEPTH) slot = 0;
-    if (PRE) {
+    if (EIGHT) {
+      F2 sum = f2(0.f);
+      float most = 0.f;   // fmaxf passes a NaN over
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) {
+          F2 w[4];
+          if (PRE) unpack8(ld8(g.pre_w, ahead.elem(i)), w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (PRE) {
+              sum = fma2(y[i][j], y[i][j], sum);
+              y[i][j] = mul2(y[i][j], w[j]);
+            }
+            float lo, hi;
+            split(y[i][j], lo, hi);
+            most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+          }
+        }
+      float ss = both(sum);
+      cta_sum_max(ss, most, buf[par][1]);
+      const float r = PRE ? inv_rms(ss, inv_d, eps) : 1.f;
+      const float scale = fmaxf(__fdiv_rn(r * most, 448.f), 0x1p-126f);
+      if (threadIdx.x == 0) g.scale[t] = scale;
+      const F2 m = f2(__fdiv_rn(r, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ahead.elem(i) < d) *reinterpret_cast<uint2*>(g.q + base + ahead.elem(i)) = pack_e4m3x8<!PRE>(y[i], m, minus_scale);
+    } else if (PRE) {
       F2 sum = f2(0.f);
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -557,9 +631,9 @@ NormArgs make_args(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T) 
   return g;
 }
 
-template <int V, int DEPTH, bool Z, bool POST, bool PRE>
+template <int V, int DEPTH, bool Z, bool POST, bool PRE, bool EIGHT>
 cudaError_t run_fwd(const NormArgs& g, cudaStream_t s) {
-  constexpr auto* kernel = block_norm_fwd_kernel<V, DEPTH, Z, POST, PRE>;
+  constexpr auto* kernel = block_norm_fwd_kernel<V, DEPTH, Z, POST, PRE, EIGHT>;
   const int threads = ((g.d / 8 + V - 1) / V + 31) / 32 * 32, smem = DEPTH * 2 * V * threads * 16;
   cudaError_t e = allow_smem<kernel>(DEPTH * 2 * V * kMaxWarps * 32 * 16);
   if (e != cudaSuccess) return e;
@@ -573,11 +647,23 @@ cudaError_t run_fwd(const NormArgs& g, cudaStream_t s) {
   return launch_pdl(kernel, dim3(g.T < most ? g.T : most), dim3(threads), smem, s, g);
 }
 
-template <int V, int DEPTH>
+template <int V, int DEPTH, bool EIGHT>
 cudaError_t pick_fwd(const NormArgs& g, cudaStream_t s) {
-  if (!g.z) return run_fwd<V, DEPTH, false, false, true>(g, s);
-  if (g.post_w) return g.pre_w ? run_fwd<V, DEPTH, true, true, true>(g, s) : run_fwd<V, DEPTH, true, true, false>(g, s);
-  return g.pre_w ? run_fwd<V, DEPTH, true, false, true>(g, s) : run_fwd<V, DEPTH, true, false, false>(g, s);
+  if (!g.z) {
+    if constexpr (EIGHT)
+      if (!g.pre_w) return run_fwd<V, DEPTH, false, false, false, true>(g, s);
+    return run_fwd<V, DEPTH, false, false, true, EIGHT>(g, s);
+  }
+  if (g.post_w)
+    return g.pre_w ? run_fwd<V, DEPTH, true, true, true, EIGHT>(g, s) : run_fwd<V, DEPTH, true, true, false, EIGHT>(g, s);
+  return g.pre_w ? run_fwd<V, DEPTH, true, false, true, EIGHT>(g, s) : run_fwd<V, DEPTH, true, false, false, EIGHT>(g, s);
+}
+
+template <bool EIGHT>
+cudaError_t pick_fwd_width(const NormArgs& g, cudaStream_t s) {
+  if (g.d <= 2048) return pick_fwd<1, 3, EIGHT>(g, s);
+  if (g.d <= 8192) return pick_fwd<2, 2, EIGHT>(g, s);
+  return pick_fwd<4, 1, EIGHT>(g, s);
 }
 
 template <int V, int DEPTH, bool Z, bool POST, bool DA>
@@ -607,9 +693,16 @@ cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs
   NormArgs g = make_args(c, in, T);
   g.y = y;
   g.a = a;
-  if (g.d <= 2048) return pick_fwd<1, 3>(g, s);
-  if (g.d <= 8192) return pick_fwd<2, 2>(g, s);
-  return pick_fwd<4, 1>(g, s);
+  return pick_fwd_width<false>(g, s);
+}
+
+cudaError_t launch_block_norm_quant(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y, uint8_t* q,
+                                    float* scale, cudaStream_t s) {
+  NormArgs g = make_args(c, in, T);
+  g.y = y;
+  g.q = q;
+  g.scale = scale;
+  return pick_fwd_width<true>(g, s);
 }
 
 int block_norm_parts(int T) {

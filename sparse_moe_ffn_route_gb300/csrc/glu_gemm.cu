@@ -58,6 +58,7 @@
 #include "block.h"
 #include "common.cuh"
 #include "glu_act.cuh"
+#include "linear_act.cuh"
 #include "tc.cuh"
 
 namespace moe {
@@ -69,7 +70,8 @@ constexpr int kMaxProblems = 4;
 constexpr int kEpiWarps = 8, kProducer1 = 3 + kEpiWarps;
 
 // The epilogue of a launch's first product (any others: kEpiStore).
-enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2 };
+enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2, kEpiLinear = 3, kEpiLinear8 = 4 };
+__host__ __device__ constexpr bool is_linear(int epi) { return epi >= kEpiLinear; }
 
 constexpr int kMaxStages = 10;
 constexpr int kInfos = 4;   // tiles worked out ahead
@@ -124,6 +126,7 @@ struct GemmParams {
   int d;
   const float* norm;    // [M] | [N] | [N]; null where nothing is settled
   float gap;
+  LinearEpi lin;        // kEpiLinear, kEpiLinear8
   uint32_t* status;
   int clear_status;     // this is the call's first kernel
 };
@@ -333,9 +336,22 @@ __device__ __forceinline__ void load_blocks(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-template <int CG>
+// EIGHT: 32 bytes of k are 32 e4m3 values and not 16 bf16 ones.
+template <int CG, bool EIGHT>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if (CG == 1) {
+  if (EIGHT && CG == 1) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else if (EIGHT) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else if (CG == 1) {
     tc::umma_bf16(d, a, b, idesc, accumulate);
   } else {
     asm volatile(
@@ -535,6 +551,23 @@ __device__ __forceinline__ void finish8(const GemmParams& g, const Problem& p, i
     *reinterpret_cast<uint4*>(g.out2 + (size_t)m * p.N + n) =
         make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
   }
+  if (is_linear(EPI)) {
+    if (!valid) return;
+    constexpr bool kEight = EPI == kEpiLinear8;
+    const float xs = kEight ? g.lin.x_scale[m] : 1.f;
+    linear_affine8<kEight>(g.lin, xs, n, v);
+    if (p.pair) {
+      linear_affine8<kEight>(g.lin, xs, p.N + n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = glu_value(g.lin.gated, v[i], w[i]);
+    } else {
+      if (g.lin.pre)
+        *reinterpret_cast<uint4*>(g.lin.pre + (size_t)m * p.N + n) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      linear_values(g.lin.act, v);
+    }
+    if (g.lin.residual) add_bf16x8(v, *reinterpret_cast<const uint4*>(g.lin.residual + (size_t)m * p.N + n));
+  }
   if (valid)
     *reinterpret_cast<uint4*>(p.out + (size_t)m * p.N + n) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -707,7 +740,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           }
           full = mbar_over(full0 + 8u * s, ph);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) mma<CG>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
+          for (int j = 0; j < kBK / 16; ++j) mma<CG, EPI == kEpiLinear8>(dt, ad + j * astep, bd + j * bstep, idesc, (c | j) != 0);
           commit<CG>(done);
           any = true;
         }
@@ -751,7 +784,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           in.two_b = CG == 1 && p.pair;
           in.boxes = in.b_mn ? (brows + 63) / 64 : 0;
           in.bytes = CG * ((uint32_t)kTileA + (in.b_mn ? (uint32_t)in.boxes * 8192u : (uint32_t)brows * 128u));
-          in.idesc = tc::idesc_bf16_f32(kBM * CG, p.tn) | ((uint32_t)in.a_mn << 15) | ((uint32_t)in.b_mn << 16);
+          in.idesc = (EPI == kEpiLinear8 ? tc::idesc_e4m3_f32(kBM * CG, p.tn) : tc::idesc_bf16_f32(kBM * CG, p.tn)) | ((uint32_t)in.a_mn << 15) | ((uint32_t)in.b_mn << 16);
           in.nkc = p.nkc;
           const int all = p.nkc * p.segs;
           const int pt = SPLIT ? part : tl.part, pts = SPLIT ? parts : EPI == kEpiStore ? p.parts : 1;
@@ -847,12 +880,13 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         cluster_wait();
         all_run = true;
         const uint32_t ex = tc::smem_u32(smem) + (uint32_t)(kStages * kStageBytes + 4 * row);
-        const int shares = tn / 8, each = EPI == kEpiGlu ? 16 : 8;
+        const bool pairs = EPI == kEpiGlu || (is_linear(EPI) && p.pair);
+        const int shares = tn / 8, each = pairs ? 16 : 8;
         if (m - lane < p.M)   // of a row block past the last row nothing is needed
           for (int c0 = 16 * par; c0 < p.tn; c0 += 32) {
             float v[16];
             tc::tmem_ld16(taddr + (uint32_t)c0, v);
-            const int up = EPI == kEpiGlu && c0 >= tn, c = up ? c0 - tn : c0;
+            const int up = pairs && c0 >= tn, c = up ? c0 - tn : c0;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int u = c / 8 + k, owner = ((u + 1) * parts - 1) / shares, nth_of = u - shares * owner / parts;
@@ -904,6 +938,70 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
               for (int i = 0; i < 16; ++i) v[i] = glu_value<false>(g.act, v[i], w[i]);
             }
             store_bf16x16(orow + c0, v, left, wide);
+          }
+        }
+      } else if (is_linear(EPI)) {
+        constexpr bool kEight = EPI == kEpiLinear8;
+        const float xs = kEight && valid ? g.lin.x_scale[m] : 1.f;
+        const int rows = p.M - (m - lane);
+        const uint16_t* rrow = g.lin.residual ? g.lin.residual + (size_t)m * p.N + n0 : nullptr;
+        if (p.pair) {
+          for (int c0 = 16 * par; c0 < cols; c0 += 32) {
+            const int left = cols - c0;
+            uint4 res[2] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (rrow && valid && 8 * h < left) res[h] = *reinterpret_cast<const uint4*>(rrow + c0 + 8 * h);
+            float v[16], w[16];
+            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), v, w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (8 * h < left) {
+                linear_affine8<kEight>(g.lin, xs, n0 + c0 + 8 * h, v + 8 * h);
+                linear_affine8<kEight>(g.lin, xs, p.N + n0 + c0 + 8 * h, w + 8 * h);
+              }
+            if (g.lin.gated.act == MOE_ACT_CLAMPED_GLU) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = glu_value<true>(g.lin.gated, v[i], w[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = glu_value<false>(g.lin.gated, v[i], w[i]);
+            }
+            if (rrow) {
+              add_bf16x8(v, res[0]);
+              add_bf16x8(v + 8, res[1]);
+            }
+            if (valid) store_bf16x16(orow + c0, v, left, wide);
+          }
+        } else {
+          for (int c0 = 32 * par; c0 < cols; c0 += 64) {
+            const int left = cols - c0;
+            uint4 res[4] = {};
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (rrow && valid && 8 * h < left) res[h] = *reinterpret_cast<const uint4*>(rrow + c0 + 8 * h);
+            float v[16], w[16];
+            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(c0 + 16), v, w);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (8 * h < left) linear_affine8<kEight>(g.lin, xs, n0 + c0 + 8 * h, (h < 2 ? v : w) + 8 * (h & 1));
+            uint32_t z[16];
+            if (g.lin.pre) {
+              pack16(v, z);
+              pack16(w, z + 8);
+              store_32x32(g.lin.pre + (size_t)(m - lane) * p.N + n0 + c0, p.N, z, rows, left, lane);
+            }
+            linear_values(g.lin.act, v);
+            linear_values(g.lin.act, w);
+            if (rrow) {
+              add_bf16x8(v, res[0]);
+              add_bf16x8(v + 8, res[1]);
+              add_bf16x8(w, res[2]);
+              add_bf16x8(w + 8, res[3]);
+            }
+            pack16(v, z);
+            pack16(w, z + 8);
+            store_32x32(orow + c0 - (size_t)lane * p.N, p.N, z, rows, left, lane);
           }
         }
       } else if (EPI == kEpiDact && tl.pi == 0) {
@@ -1015,7 +1113,9 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
       const int q = warp & 3, par = (warp - 2) >> 2, row = 32 * q + lane;
       const Tile tl = tile_at<false>(g, unit);
       const Problem& p = g.p[tl.pi];
-      const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn, shares = tn / 8, each = EPI == kEpiGlu ? 16 : 8;
+      const int tn = p.pair ? p.tn >> 1 : p.tn, n0 = tl.n * tn, shares = tn / 8;
+      const bool pairs = EPI == kEpiGlu || (is_linear(EPI) && p.pair);
+      const int each = pairs ? 16 : 8;
       const float* ex = reinterpret_cast<const float*>(smem + kStages * kStageBytes) + row;
       const int u0 = shares * part / parts, u1 = shares * (part + 1) / parts;
       for (int u = u0 + par; u < u1; u += 2) {
@@ -1026,7 +1126,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             v[i] += x[i * kBM];
-            if (EPI == kEpiGlu) w[i] += x[(8 + i) * kBM];
+            if (pairs) w[i] += x[(8 + i) * kBM];
           }
         }
         finish8<EPI>(g, p, tl.m, row, n0 + 8 * u, v, w);
@@ -1556,6 +1656,121 @@ cudaError_t launch_glu_backward(const GluParams& w, const uint16_t* x, const uin
   if (dwd && !b.down_first) product(w.d, w.ff, T, dy, nullptr, true, sv.h, nullptr, b.parts, dwd);
   if (!ok) return cudaErrorInvalidValue;
   if (!g.n_problems) return cudaSuccess;
+  g.partial = reinterpret_cast<float4*>(split.partial);
+  g.arrived = split.arrived;
+  return launch<kEpiStore>(g, Way{b.cg, 1, b.tn}, s);
+}
+
+// ---------------------------------------------------------------- the linear layer
+cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const void* weights, uint16_t* y,
+                               const LinearEpi& epi, uint32_t* status, cudaStream_t s) {
+  GemmParams g;
+  std::memset(&g, 0, sizeof(g));
+  g.n_problems = 1;
+  // e4m3 values are moved two at a time: to TMA both formats are rows of n_in bytes or 2 n_in
+  const int k = l.eight ? l.n_in / 2 : l.n_in, per = epi.glu ? 2 : 1;
+  const uint16_t *a = static_cast<const uint16_t*>(x), *b = static_cast<const uint16_t*>(weights);
+  Problem& p = g.p[0];
+  p.M = T;
+  p.N = l.n_out;
+  p.nkc = cdiv(k, kBK);
+  p.segs = 1;
+  p.pair = epi.glu;
+  p.parts = 1;
+  const Way way = pick_way(T, l.n_out, p.nkc, per, 0);
+  p.tn = way.tn;
+  p.mt = cdiv(T, kBM * way.cg);
+  p.nt = cdiv(l.n_out, p.tn / per);
+  p.wide = l.n_out % 16 == 0 && aligned32(y);
+  p.out = y;
+  const int brows = epi.glu ? p.tn / 2 : p.tn / way.cg;
+  if (!map_bf16(&p.a[0], a, T, k, kBM) || !map_bf16(&p.b[0], b, l.n_out, k, brows) ||
+      (epi.glu && !map_bf16(&p.b[1], b + (size_t)l.n_out * k, l.n_out, k, brows)))
+    return cudaErrorInvalidValue;
+  g.lin = epi;
+  g.status = status;
+  g.clear_status = 1;
+  return l.eight ? launch<kEpiLinear8>(g, way, s) : launch<kEpiLinear>(g, way, s);
+}
+
+namespace {
+
+// How the two products of a linear layer's backward pass are laid out, as Backward above.
+struct LinearBackward {
+  Way dx;
+  int cg, parts, tn;
+  bool dx_alone;
+};
+
+LinearBackward plan_linear_backward(int n_in, int n_out, int T, bool dx, bool dw) {
+  constexpr int kSpace = Lay<kEpiStore>::kStageSpace;
+  const ClusterCounts counts = cluster_counts();
+  const int k = cdiv(T, kBK), ko = cdiv(n_out, kBK);
+  auto tiles = [&](int M, int N, int cg, int tn) { return (int)std::min<long long>((long long)cdiv(M, kBM * cg) * cdiv(N, tn), 1 << 28); };
+  LinearBackward b{};
+  long long least = -1, alone_dx = 0;
+  if (dx) b.dx = pick_way(T, n_in, ko, 1, kSpace, &alone_dx);
+  const int most = linear_split_tiles(n_in, n_out, T);
+  Alike a[2];
+  auto consider = [&](int cg, int tn, int parts) {
+    for (int alone = 0; alone <= (dx && (!dw || b.dx.parts > 1) ? 1 : 0); ++alone) {
+      const int each = tiles(n_out, n_in, cg, tn);
+      if (parts > 1 && (!dw || (long long)each * parts > most)) continue;
+      int n = 0;
+      if (dx && !alone) a[n++] = Alike{tiles(T, n_in, cg, tn), tile_clocks(ko, 1, cg, tn, kSpace)};
+      if (dw) a[n++] = Alike{each * parts, tile_clocks(k, parts, cg, tn, kSpace)};
+      long long clocks = alone ? alone_dx + kLaunchClocks : 0;
+      if (n) clocks += span(counts[cg], a, n) + kLaunchClocks + (cg == 2 ? kPairClocks : 0);
+      if (least < 0 || clocks < least) {
+        least = clocks;
+        b.cg = cg;
+        b.parts = parts;
+        b.tn = tn;
+        b.dx_alone = alone == 1;
+      }
+    }
+  };
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int tn = kMaxN; tn >= 128; tn >>= 1) consider(cg, tn, 1);
+  for (int parts = 2; parts <= kMaxParts && k >= 4 * parts; ++parts) consider(2, kMaxN, parts);
+  return b;
+}
+
+}  // namespace
+
+int linear_split_tiles(int n_in, int n_out, int T) {
+  const long long tiles = (long long)cdiv(n_out, 2 * kBM) * cdiv(n_in, kMaxN);
+  if (T < 8 * kBK || 2 * tiles > kMaxSplit) return 0;
+  return (int)std::min<long long>(kMaxParts * tiles, kMaxSplit);
+}
+
+bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw) {
+  return dw && plan_linear_backward(l.n_in, l.n_out, T, dx, dw).parts > 1;
+}
+
+cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
+                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, uint32_t* status, cudaStream_t s) {
+  const LinearBackward b = plan_linear_backward(l.n_in, l.n_out, T, dx, dw);
+  GemmParams g;
+  std::memset(&g, 0, sizeof(g));
+  g.status = status;
+  g.clear_status = 1;
+  if (b.dx_alone) {
+    if (!set_problem(g.p[g.n_problems++], b.dx.cg, b.dx.tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))
+      return cudaErrorInvalidValue;
+    const cudaError_t e = launch<kEpiStore>(g, b.dx, s);
+    if (e != cudaSuccess || !dw) return e;
+    g.n_problems = g.clear_status = 0;
+    dx = nullptr;
+  }
+  if (dx && !set_problem(g.p[g.n_problems++], b.cg, b.tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))
+    return cudaErrorInvalidValue;
+  if (dw) {
+    Problem& p = g.p[g.n_problems++];
+    if (!set_problem(p, b.cg, b.tn, l.n_out, l.n_in, T, dv, nullptr, true, x, nullptr, true, dw)) return cudaErrorInvalidValue;
+    p.parts = b.parts;
+    p.base = 0;
+  }
   g.partial = reinterpret_cast<float4*>(split.partial);
   g.arrived = split.arrived;
   return launch<kEpiStore>(g, Way{b.cg, 1, b.tn}, s);

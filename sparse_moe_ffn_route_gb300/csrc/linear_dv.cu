@@ -1,0 +1,114 @@
+// Backward pass of the linear layer before its products: dv = dy act'(pre) in bf16, and the
+// bias's gradient, the sum of dv's rows.
+//
+// Bound by memory: reads dy and pre, writes dv (6 bytes per element; without an activation
+// dy alone, for the bias).  A CTA takes 256 columns, 8 to a lane, and a run of rows, one per
+// warp at a time; each lane adds its columns up in registers, the warps add theirs in order, and
+// a second kernel adds the CTAs' partial sums in order.
+#include "block.h"
+#include "common.cuh"
+#include "linear_act.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8, kCols = 256, kAhead = 4;
+
+int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+template <int ACT>
+__global__ void __launch_bounds__(kWarps * 32) linear_dv_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ pre,
+                                                                int T, int n, uint16_t* dv, float* parts, uint32_t* status,
+                                                                uint32_t* clear, int zeros) {
+  __shared__ float sums[kWarps][kCols];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * kCols + 8 * lane;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0u;
+  const long long first = blockIdx.y * gridDim.x + blockIdx.x;
+  for (long long i = first * blockDim.x + threadIdx.x; i < zeros; i += (long long)gridDim.x * gridDim.y * blockDim.x) clear[i] = 0u;
+  const int r0 = (int)((long long)T * blockIdx.y / gridDim.y), r1 = (int)((long long)T * (blockIdx.y + 1) / gridDim.y);
+  float sum[8] = {};
+  if (col < n)
+    for (int r = r0 + warp; r < r1; r += kWarps * kAhead) {
+      uint4 a[kAhead], z[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (r + i * kWarps < r1) {
+          const size_t at = (size_t)(r + i * kWarps) * n + col;
+          a[i] = __ldg(reinterpret_cast<const uint4*>(dy + at));
+          if (ACT != MOE_LINEAR_NONE) z[i] = __ldg(reinterpret_cast<const uint4*>(pre + at));
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (r + i * kWarps < r1) {
+          float v[8];
+          unpack_bf16x8(a[i], v);
+          if (ACT != MOE_LINEAR_NONE) {
+            float p[8];
+            unpack_bf16x8(z[i], p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], linear_slope<ACT>(p[e]));   // one value, kept or not
+            if (dv)
+              *reinterpret_cast<uint4*>(dv + (size_t)(r + i * kWarps) * n + col) =
+                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        }
+    }
+  if (parts) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[warp][8 * lane + e] = sum[e];
+    __syncthreads();
+    const int c = blockIdx.x * kCols + threadIdx.x;   // a thread to a column
+    if (c < n) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += sums[w][threadIdx.x];
+      parts[(size_t)blockIdx.y * n + c] = s;
+    }
+  }
+  pdl_trigger();
+}
+
+// 32 columns per CTA, 8 rows of threads that take every eighth partial row, added in order.
+__global__ void __launch_bounds__(256) linear_dbias_kernel(const float* parts, int rows, int n, uint16_t* dbias) {
+  __shared__ float s[8][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (col < n)
+    for (int i = r; i < rows; i += 8) v += parts[(size_t)i * n + col];
+  s[r][lane] = v;
+  __syncthreads();
+  if (r == 0 && col < n) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += s[i][lane];
+    dbias[col] = f32_to_bf16(v);
+  }
+  pdl_trigger();
+}
+
+}  // namespace
+
+int linear_bias_parts(int n, int T) {
+  const int columns = cdiv(n, kCols), most = cdiv(4 * sm_count(), columns), least = cdiv(T, kWarps * kAhead);
+  return least < most ? least : most;
+}
+
+cudaError_t launch_linear_dv(int act, const uint16_t* dy, const uint16_t* pre, int T, int n, uint16_t* dv, uint16_t* dbias,
+                             float* parts, uint32_t* status, uint32_t* clear, int zeros, cudaStream_t s) {
+  const int rows = linear_bias_parts(n, T);
+  auto run = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(cdiv(n, kCols), rows), dim3(kWarps * 32), 0, s, dy, pre, T, n, dv, dbias ? parts : nullptr,
+                      status, clear, zeros);
+  };
+  const cudaError_t e = act == MOE_LINEAR_SILU   ? run(linear_dv_kernel<MOE_LINEAR_SILU>)
+                        : act == MOE_LINEAR_GELU ? run(linear_dv_kernel<MOE_LINEAR_GELU>)
+                        : act == MOE_LINEAR_GELU_TANH ? run(linear_dv_kernel<MOE_LINEAR_GELU_TANH>)
+                                                      : run(linear_dv_kernel<MOE_LINEAR_NONE>);
+  if (e != cudaSuccess || !dbias) return e;
+  return launch_pdl(linear_dbias_kernel, dim3(cdiv(n, 32)), dim3(256), 0, s, static_cast<const float*>(parts), rows, n, dbias);
+}
+
+}  // namespace moe
