@@ -194,10 +194,10 @@ __device__ __forceinline__ void cta_sum_max(float& sum, float& most, float* buf)
   }
 }
 
-// 8 values times m as e4m3 (to nearest even; past 448 the largest value, NaN stays NaN).
-// EXACT: m is 1 / scale, and the quotient is corrected by its remainder, which rounds as the
-// division itself does (Markstein): rows of bf16 values have many quotients just halfway between
-// two codes, and 2 in 1000 fell on the other side.
+// 8 values times m = 1 / scale as e4m3 (to nearest even; past 448 the largest value, NaN stays
+// NaN).  EXACT: the quotient is corrected by its remainder, which rounds as the division itself
+// does (Markstein): rows of bf16 values have many quotients just halfway between two codes, and
+// 2 in 1000 fell on the other side.
 template <bool EXACT>
 __device__ __forceinline__ uint2 pack_e4m3x8(const F2 (&v)[4], F2 m, F2 minus_scale) {
   uint32_t u[4];
@@ -216,8 +216,8 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const F2 (&v)[4], F2 m, F2 minus_sc
 
 // Z: there is a branch; POST: with a norm; PRE: with the next block's norm (a); EIGHT: a in
 // e4m3 with its row's scale.  There a row's scale is r max|y pre_w| / 448, r the row's 1 / rms:
-// the maximum is taken beside the sum of y^2, in the same exchange, and one factor per row
-// takes y pre_w to the codes.
+// the maximum is taken beside the sum of y^2, in the same exchange.  (r and 1 / scale are two
+// factors, since their product leaves fp32's range where the scale is at its least.)
 template <int V, int DEPTH, bool Z, bool POST, bool PRE, bool EIGHT>
 __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __grid_constant__ NormArgs g) {
   extern __shared__ uint4 rows[];
@@ -303,7 +303,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       const float r = PRE ? inv_rms(ss, inv_d, eps) : 1.f;
       const float scale = fmaxf(__fdiv_rn(r * most, 448.f), 0x1p-126f);
       if (threadIdx.x == 0) g.scale[t] = scale;
-      const F2 m = f2(__fdiv_rn(r, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+      const F2 m = f2(__fdiv_rn(1.f, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+      if (PRE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[i][j] = mul2(y[i][j], f2(r));
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d) *reinterpret_cast<uint2*>(g.q + base + ahead.elem(i)) = pack_e4m3x8<!PRE>(y[i], m, minus_scale);

@@ -47,7 +47,9 @@ def w8_quantize(w: torch.Tensor):
     if w.dim() != 2:
         raise ValueError(f"w must have two dimensions, not {w.dim()}")
     v = w.float()
-    scale = (v.abs().amax(1) / E4M3_MAX).clamp(min=LEAST_SCALE) if w.shape[1] else v.new_full((w.shape[0],), LEAST_SCALE)
+    # (torch would multiply by the rounded reciprocal of a plain number)
+    top = v.abs().amax(1) if w.shape[1] else v.new_zeros(w.shape[0])
+    scale = (top / torch.full_like(top, E4M3_MAX)).clamp(min=LEAST_SCALE)
     return (v / scale[:, None]).to(torch.float8_e4m3fn), scale
 
 
