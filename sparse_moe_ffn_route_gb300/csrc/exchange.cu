@@ -4,57 +4,111 @@
 //
 // Everything here is bound by memory, and goes by token, not by sorted row: a token's row
 // is read (or written) once and its k sorted rows are written (or read) once.
+#include <algorithm>
+
 #include "../../include/moe_exchange.h"
 #include "abi_check.h"
-#include "common.cuh"
+#include "block.h"
+#include "f32x2.cuh"
 
 namespace moe {
 namespace {
 
-// ---------------------------------------------------------------- the sort
-// The slots are cut into chunks, one CTA each.  First every chunk counts its slots of each
-// expert; then each CTA knows where its chunk's slots of an expert begin (all slots of the
-// experts before, and the expert's slots in the chunks before), and places them in order:
-// 1024 slots at a time, a warp 32 of them, a slot's place among those of its warp by
-// match_any, and the warps' counts added up in a table.
-constexpr int kSortThreads = 1024, kChunk = 2048, kMostChunks = 128;
+// ---------------------------------------------------------------- out: sort and copy
+// Each CTA takes a run of tokens, finds where its slots go and copies its tokens' rows there.
+// A slot's row is (all slots of the experts before) + (its expert's slots before this
+// run) + (those before it in the run).  The first two come from counts: of all ids themselves
+// where these are few (one launch), else of chunks of slots, which a launch before has counted,
+// and of the ids between the chunk's start and the run's.  The third comes tile by tile, a
+// thread to a slot: the slot's place among those of its warp by match_any, and the warps'
+// counts added up in a table.
+constexpr int kCountThreads = 1024, kMostChunks = 128;
+// Slots up to which every CTA counts all ids, and slots of a chunk beyond.  (Every CTA reads
+// kDirect ids at most, or a chunk and the chunks' counts.)
+constexpr int kDirect = 8192, kChunk = 2048;
 
 struct SortArgs {
   const int32_t* ids;
-  int S, E, chunks, chunk;   // slots, experts; chunks of so many slots
-  int32_t *hist;             // [chunks][E]
+  int T, k, S, E;            // S = T k slots
+  int chunks, chunk;         // 0: count all ids
+  int32_t* hist;             // [chunks][E]
   int32_t *offsets, *rows;
+  int vecs;                  // 16-byte vectors of a row; 0: sort alone
+  const uint4* x;
+  uint4* xs;
+  const float* x_scale;
+  float* xs_scale;
 };
 
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArgs a) {
   __shared__ int count[kMaxExperts];
   pdl_wait();
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) count[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kCountThreads) count[e] = 0;
   __syncthreads();
   const int s0 = blockIdx.x * a.chunk, s1 = min(a.S, s0 + a.chunk);
-  for (int s = s0 + threadIdx.x; s < s1; s += kSortThreads) {
+  for (int s = s0 + threadIdx.x; s < s1; s += kCountThreads) {
     const int e = a.ids[s];
     if (e >= 0 && e < a.E) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.hist[(size_t)blockIdx.x * a.E + e] = count[e];
+  for (int e = threadIdx.x; e < a.E; e += kCountThreads) a.hist[(size_t)blockIdx.x * a.E + e] = count[e];
   pdl_trigger();
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs a) {
-  __shared__ int cursor[kMaxExperts], warp_sum[32];
-  __shared__ __align__(16) uint8_t table[kMaxExperts][32];   // an expert's slots in each warp
-  pdl_wait();
+// Sum of four bytes of counts.
+__device__ __forceinline__ uint32_t add_bytes(uint32_t w, uint32_t sum) { return __dp4a(w, 0x01010101u, sum); }
+
+// NT threads, W = NT / 32 warps.
+template <int NT>
+__global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
+  constexpr int W = NT / 32, PER = kMaxExperts / NT;   // experts of a thread in the scan
+  __shared__ int all[kMaxExperts], cursor[kMaxExperts], warp_sum[W], tile_rows[NT];
+  __shared__ __align__(16) uint8_t table[kMaxExperts][W];   // an expert's slots in each warp of a tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // thread e: expert e's slots in all chunks, and in those before this one
-  int all = 0, before = 0;
-  if (tid < a.E)
-    for (int c = 0; c < a.chunks; ++c) {
-      const int n = a.hist[(size_t)c * a.E + tid];
-      all += n;
-      before += c < (int)blockIdx.x ? n : 0;
+  const int t0 = (int)((long long)a.T * blockIdx.x / gridDim.x), t1 = (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
+  const int s0 = t0 * a.k;
+  for (int e = tid; e < a.E; e += NT) all[e] = cursor[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  int from = 0, to = a.S;   // ids to count here
+  if (a.chunks) {
+    const int mine = s0 / a.chunk;
+    from = mine * a.chunk;
+    to = s0;
+    for (int e = tid; e < a.E; e += NT) {
+      int sum = 0, before = 0;
+      for (int c0 = 0; c0 < a.chunks; c0 += 8) {
+        int n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = c0 + i < a.chunks ? a.hist[(size_t)(c0 + i) * a.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum += n[i];
+          before += c0 + i < mine ? n[i] : 0;
+        }
+      }
+      all[e] = sum;
+      cursor[e] = before;
     }
-  int inc = all;
+    __syncthreads();
+  }
+  for (int s = from + tid; s < to; s += NT) {
+    const int e = a.ids[s];
+    if (e >= 0 && e < a.E) {
+      if (!a.chunks) atomicAdd(&all[e], 1);
+      if (s < s0) atomicAdd(&cursor[e], 1);
+    }
+  }
+  __syncthreads();
+  // where each expert's rows begin: an exclusive scan, PER experts to a thread
+  int mine[PER], run = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * tid + i;
+    mine[i] = run;
+    run += e < a.E ? all[e] : 0;
+  }
+  int inc = run;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -62,201 +116,296 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
   }
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  int base = inc - all;
+  int base = inc - run;
   for (int w = 0; w < warp; ++w) base += warp_sum[w];
-  if (tid < a.E) {
-    cursor[tid] = base + before;
-    if (blockIdx.x == 0) {
-      a.offsets[tid] = base;
-      if (tid == a.E - 1) a.offsets[a.E] = base + all;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * tid + i;
+    if (e < a.E) {
+      cursor[e] += base + mine[i];
+      if (blockIdx.x == 0) {
+        a.offsets[e] = base + mine[i];
+        if (e == a.E - 1) a.offsets[a.E] = base + run;
+      }
     }
   }
-  const int s0 = blockIdx.x * a.chunk, s1 = min(a.S, s0 + a.chunk);
-  for (int from = s0; from < s1; from += kSortThreads) {
-    for (int i = tid; i < a.E * 8; i += kSortThreads) reinterpret_cast<uint32_t*>(table)[i] = 0u;
-    const int s = from + tid;
-    int e = s < s1 ? a.ids[s] : -1;
+  // tiles of whole tokens
+  const int per_tile = NT / a.k;
+  for (int t = t0; t < t1; t += per_tile) {
+    const int tokens = min(per_tile, t1 - t), slots = tokens * a.k;
+    for (int i = tid; i < a.E * (W / 4); i += NT) reinterpret_cast<uint32_t*>(table)[i] = 0u;
+    const int s = t * a.k + tid;
+    int e = tid < slots ? a.ids[s] : -1;
     if (e < 0 || e >= a.E) e = -1;
     const uint32_t peers = __match_any_sync(0xffffffffu, e);
     const int rank = __popc(peers & ((1u << lane) - 1u));
     __syncthreads();
     if (e >= 0 && rank == 0) table[e][warp] = (uint8_t)__popc(peers);
     __syncthreads();
-    if (s < s1) {
-      int row = -1;
-      if (e >= 0) {
-        const uint32_t* t = reinterpret_cast<const uint32_t*>(table[e]);
-        uint32_t earlier = 0;
-        for (int q = 0; q < (warp >> 2); ++q) earlier = __dp4a(t[q], 0x01010101u, earlier);
-        if (warp & 3) earlier = __dp4a(t[warp >> 2] & ((1u << (8 * (warp & 3))) - 1u), 0x01010101u, earlier);
-        row = cursor[e] + (int)earlier + rank;
-      }
-      a.rows[s] = row;
+    int row = -1;
+    if (e >= 0) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(table[e]);
+      uint32_t earlier = 0;
+      for (int q = 0; q < (warp >> 2); ++q) earlier = add_bytes(w[q], earlier);
+      if (warp & 3) earlier = add_bytes(w[warp >> 2] & ((1u << (8 * (warp & 3))) - 1u), earlier);
+      row = cursor[e] + (int)earlier + rank;
     }
+    if (tid < slots) a.rows[s] = tile_rows[tid] = row;
     __syncthreads();
-    for (int i = tid; i < a.E; i += kSortThreads) {   // the next slots come behind
-      const uint32_t* t = reinterpret_cast<const uint32_t*>(table[i]);
-      uint32_t n = 0;
+    if (t + per_tile < t1)
+      for (int i = tid; i < a.E; i += NT) {   // the next tile's slots come behind
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(table[i]);
+        uint32_t n = 0;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) n = __dp4a(t[q], 0x01010101u, n);
-      cursor[i] += (int)n;
+        for (int q = 0; q < W / 4; ++q) n = add_bytes(w[q], n);
+        cursor[i] += (int)n;
+      }
+    if (a.vecs) {
+      // a warp copies up to 4 x 32 vectors of a token at a time
+      const int pieces = (a.vecs + 127) / 128;
+      for (int u = warp; u < tokens * pieces; u += W) {
+        const int i = u / pieces, v0 = (u - i * pieces) * 128 + lane;
+        const uint4* src = a.x + (size_t)(t + i) * a.vecs;
+        uint4 q[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (v0 + 32 * h < a.vecs) q[h] = __ldg(src + v0 + 32 * h);
+        for (int j = 0; j < a.k; ++j) {
+          const int r = tile_rows[i * a.k + j];
+          if (r < 0) continue;
+          uint4* dst = a.xs + (size_t)r * a.vecs;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (v0 + 32 * h < a.vecs) dst[v0 + 32 * h] = q[h];
+        }
+      }
+      if (a.xs_scale && row >= 0) a.xs_scale[row] = a.x_scale[t + tid / a.k];
     }
     __syncthreads();
   }
   pdl_trigger();
 }
 
-// ---------------------------------------------------------------- rows
-// A token's row is cut over `parts` warps, so that few tokens still fill the GPU; warp w of all
-// takes part w % parts of token w / parts, then those behind.
+// ---------------------------------------------------------------- back: rows to their tokens
+// Rows come through shared memory: every thread copies its own vectors ahead of time
+// (cp.async; a thread reads only what it copied, so no barrier is needed), which keeps 100 KiB
+// and more per SM in flight without registers.
 struct RowArgs {
   const int32_t* rows;       // [T, k]
   int T, k, S;
-  int vecs, parts;           // 16-byte vectors of a row; warps to a row
+  int vecs, groups;          // 16-byte vectors of a row; groups of 32 of them
+  int depth;                 // units ahead
 };
 
-constexpr int kRowWarps = 8;
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last n (at most 7) groups of this thread's copies are there.
+__device__ __forceinline__ void copies_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
 
-// xs[rows[t, j]] = x[t]
-__global__ void __launch_bounds__(kRowWarps * 32) dispatch_rows_kernel(const RowArgs a, const uint4* __restrict__ x,
-                                                                       const float* __restrict__ x_scale, uint4* xs,
-                                                                       float* xs_scale) {
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long units = (long long)a.T * a.parts, step = (long long)gridDim.x * kRowWarps;
-  for (long long u = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
-    const int t = (int)(u / a.parts), part = (int)(u - (long long)t * a.parts);
-    const int mine = lane < a.k ? a.rows[(size_t)t * a.k + lane] : -1;   // k is 32 at most
-    for (int v0 = part * 32; v0 < a.vecs; v0 += 128 * a.parts) {
-      uint4 q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = v0 + 32 * i * a.parts + lane;
-        if (v < a.vecs) q[i] = __ldg(x + (size_t)t * a.vecs + v);
-      }
-      for (int j = 0; j < a.k; ++j) {
-        const int r = __shfl_sync(0xffffffffu, mine, j);
-        if ((unsigned)r >= (unsigned)a.S) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int v = v0 + 32 * i * a.parts + lane;
-          if (v < a.vecs) xs[(size_t)r * a.vecs + v] = q[i];
-        }
-      }
+// y[t] = residual[t] + sum_j w[t, j] z[rows[t, j]].  A unit of a warp is 32 vectors of a token:
+// k rows' pieces and the residual's.  KT: k rounded up to a power of two.
+template <int KT>
+__global__ void __launch_bounds__(512) combine_kernel(const RowArgs a, const uint4* __restrict__ z, const float* __restrict__ w,
+                                                      const uint4* residual, uint4* y) {
+  extern __shared__ uint4 ring[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  uint4* mine = ring + (size_t)warp * a.depth * (a.k + 1) * 32 + lane;   // [slot][k + 1][lane]
+  // units first, first + step, ... of [token][group], without a division for each
+  const int step = gridDim.x * W, step_t = step / a.groups, step_g = step - step_t * a.groups;
+  const int first = blockIdx.x * W + warp;
+  int t = first / a.groups, g = first - t * a.groups, at = t, ag = g;   // this unit; the next to ask for
+  auto next = [&](int& tt, int& gg) {
+    tt += step_t;
+    if ((gg += step_g) >= a.groups) {
+      gg -= a.groups;
+      ++tt;
     }
-    if (xs_scale && part == 0 && (unsigned)mine < (unsigned)a.S) xs_scale[mine] = x_scale[t];
-  }
-  pdl_trigger();
-}
-
-__device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(u[i]);
-    f[2 * i + 1] = bf16_hi(u[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-
-// y[t] = residual[t] + sum_j w[t, j] z[rows[t, j]]
-__global__ void __launch_bounds__(kRowWarps * 32) combine_rows_kernel(const RowArgs a, const uint4* __restrict__ z,
-                                                                      const float* __restrict__ w, const uint4* residual,
-                                                                      uint4* y) {
+  };
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long units = (long long)a.T * a.parts, step = (long long)gridDim.x * kRowWarps;
-  for (long long u = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
-    const int t = (int)(u / a.parts), part = (int)(u - (long long)t * a.parts);
-    const int mine = lane < a.k ? a.rows[(size_t)t * a.k + lane] : -1;
-    const float weight = w && lane < a.k ? w[(size_t)t * a.k + lane] : 1.f;
-    for (int v = part * 32 + lane; v - lane < a.vecs; v += 32 * a.parts) {
+  // what lane j asks for: choice j of the next unit to ask for
+  int row = -1;
+  auto look = [&]() {
+    row = -1;
+    if (at < a.T && lane < a.k) row = a.rows[(size_t)at * a.k + lane];
+  };
+  look();
+  int in_slot = 0, out_slot = 0;
+  auto ask = [&]() {
+    if (at < a.T) {
+      const int v = ag * 32 + lane;
       const bool in = v < a.vecs;
-      float sum[8] = {};
-      if (residual && in) unpack8(residual[(size_t)t * a.vecs + v], sum);
-      for (int j0 = 0; j0 < a.k; j0 += 4) {
-        uint4 q[4];
-        bool has[4];
+      const uint32_t dst = shared_at(mine + in_slot * (a.k + 1) * 32);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = __shfl_sync(0xffffffffu, mine, (j0 + i) & 31);
-          has[i] = in && j0 + i < a.k && (unsigned)r < (unsigned)a.S;
-          if (has[i]) q[i] = __ldg(z + (size_t)r * a.vecs + v);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float c = __shfl_sync(0xffffffffu, weight, (j0 + i) & 31);
-          if (has[i]) {
-            float f[8];
-            unpack8(q[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] = fmaf(c, f[e], sum[e]);
-          }
-        }
+      for (int j = 0; j < KT; ++j) {   // (row is -1 from k on)
+        const int r = __shfl_sync(0xffffffffu, row, j);
+        if ((unsigned)r < (unsigned)a.S && in) copy16(dst + 512u * j, z + (size_t)r * a.vecs + v);
       }
-      if (in) y[(size_t)t * a.vecs + v] = pack8(sum);
+      if (residual && in) copy16(dst + 512u * a.k, residual + (size_t)at * a.vecs + v);
     }
+    copies_asked();
+    if (++in_slot == a.depth) in_slot = 0;
+    next(at, ag);
+    look();
+  };
+  for (int i = 0; i < a.depth; ++i) ask();
+  for (; t < a.T; next(t, g)) {
+    const int v = g * 32 + lane;
+    int r = -1;
+    float c = 1.f;
+    if (lane < a.k) {
+      r = a.rows[(size_t)t * a.k + lane];
+      if (w) c = w[(size_t)t * a.k + lane];
+    }
+    const uint32_t live = __ballot_sync(0xffffffffu, (unsigned)r < (unsigned)a.S);
+    copies_wait(a.depth - 1);
+    const uint4* slot = mine + out_slot * (a.k + 1) * 32;
+    F2 sum[4] = {};
+    if (residual) unpack8(slot[a.k * 32], sum);
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+      const F2 by = f2(__shfl_sync(0xffffffffu, c, j));
+      if (!(live >> j & 1)) continue;
+      F2 f[4];
+      unpack8(slot[j * 32], f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = fma2(by, f[e], sum[e]);
+    }
+    if (v < a.vecs) y[(size_t)t * a.vecs + v] = pack8(sum);
+    if (++out_slot == a.depth) out_slot = 0;
+    ask();
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   pdl_trigger();
 }
 
-// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA of parts warps takes
-// a token at a time.
-__global__ void __launch_bounds__(kRowWarps * 32) combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy,
-                                                                          const uint4* __restrict__ z,
-                                                                          const float* __restrict__ w, uint4* dz, float* dw) {
-  __shared__ float part_sum[2][kRowWarps][kMaxTopK];
+// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA takes a token at a
+// time, its warps the groups of 32 vectors in turn; each adds its part of the dot products up
+// over its groups, and they meet once per token.  KT: k rounded up to a power of two.
+template <int KT>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy,
+                                                               const uint4* __restrict__ z, const float* __restrict__ w,
+                                                               uint4* dz, float* dw) {
+  extern __shared__ uint4 ring[];
+  __shared__ float part_sum[2][8][kMaxTopK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  uint4* mine = ring + (size_t)warp * a.depth * (a.k + 1) * 32 + lane;
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int turn = 0;
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    const int mine = lane < a.k ? a.rows[(size_t)t * a.k + lane] : -1;
-    const float weight = lane < a.k ? w[(size_t)t * a.k + lane] : 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const int r = __shfl_sync(0xffffffffu, mine, j);
-      const float c = __shfl_sync(0xffffffffu, weight, j);
-      float sum = 0.f;
-      if ((unsigned)r < (unsigned)a.S)
-        for (int v = warp * 32 + lane; v < a.vecs; v += 32 * a.parts) {
-          float g[8];
-          unpack8(__ldg(dy + (size_t)t * a.vecs + v), g);
-          if (dw) {
-            float f[8];
-            unpack8(__ldg(z + (size_t)r * a.vecs + v), f);
+  // the next unit to ask for: token `at`, group `ag`
+  int at = blockIdx.x, ag = warp, row = -1;
+  auto look = [&]() {
+    row = -1;
+    if (at < a.T && lane < a.k) row = a.rows[(size_t)at * a.k + lane];
+  };
+  look();
+  int in_slot = 0, out_slot = 0;
+  auto ask = [&]() {
+    if (at < a.T) {
+      const int v = ag * 32 + lane;
+      const bool in = v < a.vecs;
+      const uint32_t dst = shared_at(mine + in_slot * (a.k + 1) * 32);
+      if (in) copy16(dst + 512u * a.k, dy + (size_t)at * a.vecs + v);
+      if (dw)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(g[e], f[e], sum);
-          }
-          if (dz) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] *= c;
-            dz[(size_t)r * a.vecs + v] = pack8(g);
-          }
+        for (int j = 0; j < KT; ++j) {
+          const int r = __shfl_sync(0xffffffffu, row, j);
+          if ((unsigned)r < (unsigned)a.S && in) copy16(dst + 512u * j, z + (size_t)r * a.vecs + v);
         }
-      if (dw) {
+    }
+    copies_asked();
+    if (++in_slot == a.depth) in_slot = 0;
+    if ((ag += W) >= a.groups) {
+      ag = warp;
+      at += gridDim.x;
+      look();
+    }
+  };
+  for (int i = 0; i < a.depth; ++i) ask();
+  int turn = 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {   // (T + the grid stay below 2^31)
+    int r = -1;
+    float c = 0.f;
+    if (lane < a.k) {
+      r = a.rows[(size_t)t * a.k + lane];
+      c = w[(size_t)t * a.k + lane];
+    }
+    const uint32_t live = __ballot_sync(0xffffffffu, (unsigned)r < (unsigned)a.S);
+    F2 acc[KT] = {};
+    for (int g = warp; g < a.groups; g += W) {
+      const int v = g * 32 + lane;
+      copies_wait(a.depth - 1);
+      const uint4* slot = mine + out_slot * (a.k + 1) * 32;
+      const bool in = v < a.vecs;
+      F2 d[4];
+      unpack8(slot[a.k * 32], d);   // lanes past the row's end hold anything, and keep it
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) part_sum[turn][warp][j] = sum;
+      for (int j = 0; j < KT; ++j) {
+        const F2 by = f2(__shfl_sync(0xffffffffu, c, j));
+        const int to = __shfl_sync(0xffffffffu, r, j);
+        if (!(live >> j & 1) || !in) continue;   // (live: j < k)
+        if (dw) {
+          F2 f[4];
+          unpack8(slot[j * 32], f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j] = fma2(d[e], f[e], acc[j]);
+        }
+        if (dz) {
+          F2 o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = mul2(by, d[e]);
+          dz[(size_t)to * a.vecs + v] = pack8(o);
+        }
       }
+      if (++out_slot == a.depth) out_slot = 0;
+      ask();
     }
     if (dw) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (j < a.k) {
+          float v = both(acc[j]);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) part_sum[turn][warp][j] = v;
+        }
       __syncthreads();
       if (warp == 0 && lane < a.k) {
         float s = 0.f;
-        for (int p = 0; p < a.parts; ++p) s += part_sum[turn][p][lane];
+        for (int p = 0; p < W; ++p) s += part_sum[turn][p][lane];
         dw[(size_t)t * a.k + lane] = s;
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   pdl_trigger();
 }
 
 // ---------------------------------------------------------------- host
 int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
 
-int chunk_slots(int S) { return S <= kChunk * kMostChunks ? kChunk : cdiv(cdiv(S, kMostChunks), kSortThreads) * kSortThreads; }
-int chunk_count(int S) { return S ? cdiv(S, chunk_slots(S)) : 1; }
+int chunk_slots(int S) { return S <= kChunk * kMostChunks ? kChunk : cdiv(S, kMostChunks); }
+int chunk_count(int S) { return S <= kDirect ? 0 : cdiv(S, chunk_slots(S)); }
+
+// How the way back runs: warps to a CTA, CTAs, shared memory.
+struct RowPlan {
+  RowArgs a;
+  int warps, ctas, smem;
+};
+
+constexpr int kRingBytes = 200 * 1024, kMostDepth = 8;
 
 RowArgs row_args(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
   RowArgs a{};
@@ -264,15 +413,43 @@ RowArgs row_args(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
   a.T = T;
   a.k = c.top_k;
   a.S = T * c.top_k;
-  a.vecs = c.d_model * (c.format == MOE_ROWS_E4M3 ? 1 : 2) / 16;
-  const int most = cdiv(a.vecs, 32), want = cdiv(48LL * sm_count(), T);
-  a.parts = want < most ? (want > 1 ? want : 1) : most;
+  a.vecs = c.d_model / 8;
+  a.groups = cdiv(a.vecs, 32);
   return a;
 }
 
-int row_grid(const RowArgs& a) {
-  const long long blocks = ((long long)a.T * a.parts + kRowWarps - 1) / kRowWarps, most = 64LL * sm_count();
-  return (int)(blocks < most ? blocks : most);
+// One CTA per SM, of as many warps as have two units in its ring at least; less where there are
+// few units.
+RowPlan plan_combine(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
+  RowPlan p;
+  p.a = row_args(c, rows, T);
+  const int sms = sm_count(), unit = (p.a.k + 1) * 512;
+  const long long units = (long long)T * p.a.groups;
+  p.warps = 16;
+  while (p.warps > 4 && kRingBytes / (p.warps * unit) < 2) p.warps >>= 1;
+  while (p.warps > 1 && units < (long long)p.warps * sms) p.warps >>= 1;
+  const long long ctas = (units + p.warps - 1) / p.warps;
+  p.ctas = (int)(ctas < sms ? ctas : sms);
+  p.a.depth = std::min(kMostDepth, kRingBytes / (p.warps * unit));
+  const long long each = (units + (long long)p.ctas * p.warps - 1) / ((long long)p.ctas * p.warps);
+  if (p.a.depth > each) p.a.depth = (int)each;
+  p.smem = p.a.depth * p.warps * unit;
+  return p;
+}
+
+// Up to 8 warps, as even a share of the groups each as can be; two CTAs per SM.
+RowPlan plan_backward(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
+  RowPlan p;
+  p.a = row_args(c, rows, T);
+  const int unit = (p.a.k + 1) * 512;
+  p.warps = cdiv(p.a.groups, cdiv(p.a.groups, 8));
+  while (p.warps > 1 && kRingBytes / 2 / (p.warps * unit) < 1) --p.warps;
+  p.ctas = std::min(T, 2 * sm_count());
+  p.a.depth = std::min(kMostDepth, kRingBytes / 2 / (p.warps * unit));
+  const long long each = (long long)cdiv(T, p.ctas) * cdiv(p.a.groups, p.warps);
+  if (p.a.depth > each) p.a.depth = (int)each;
+  p.smem = p.a.depth * p.warps * unit;
+  return p;
 }
 
 int check_cfg(const moe_exchange_cfg_t* c, int T, bool bf16) {
@@ -301,9 +478,18 @@ int sum_rows(const moe_exchange_cfg_t* cfg, const void* z, const int32_t* rows, 
   const Span out[] = {{y, T * row}};
   const Span in[] = {{z, S * row}, {rows, S * 4}, {w, S * 4}, {residual == y ? nullptr : residual, T * row}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
-  const RowArgs a = row_args(*cfg, rows, T);
-  EXCHANGE_CUDA(launch_pdl(combine_rows_kernel, dim3(row_grid(a)), dim3(kRowWarps * 32), 0, static_cast<cudaStream_t>(stream), a,
-                           static_cast<const uint4*>(z), w, static_cast<const uint4*>(residual), static_cast<uint4*>(y)));
+  const RowPlan p = plan_combine(*cfg, rows, T);
+  auto run = [&](auto kernel, cudaError_t allowed) {
+    if (allowed != cudaSuccess) return allowed;
+    return launch_pdl(kernel, dim3(p.ctas), dim3(p.warps * 32), p.smem, static_cast<cudaStream_t>(stream), p.a,
+                      static_cast<const uint4*>(z), w, static_cast<const uint4*>(residual), static_cast<uint4*>(y));
+  };
+  const int k = cfg->top_k;
+  EXCHANGE_CUDA(k <= 2   ? run(combine_kernel<2>, allow_smem<combine_kernel<2>>(kRingBytes))
+                : k <= 4 ? run(combine_kernel<4>, allow_smem<combine_kernel<4>>(kRingBytes))
+                : k <= 8 ? run(combine_kernel<8>, allow_smem<combine_kernel<8>>(kRingBytes))
+                : k <= 16 ? run(combine_kernel<16>, allow_smem<combine_kernel<16>>(kRingBytes))
+                          : run(combine_kernel<32>, allow_smem<combine_kernel<32>>(kRingBytes)));
   return MOE_OK;
 }
 
@@ -316,7 +502,7 @@ extern "C" {
 
 size_t moe_dispatch_workspace_bytes(const moe_exchange_cfg_t* cfg, int32_t T) {
   if (check_cfg(cfg, T, false) != MOE_OK) return 0;
-  return align_up((size_t)chunk_count(T * cfg->top_k) * cfg->n_experts * 4);
+  return 256 + align_up((size_t)chunk_count(T * cfg->top_k) * cfg->n_experts * 4);
 }
 
 int moe_dispatch_forward(const moe_exchange_cfg_t* cfg, const int32_t* topk_ids, const void* x, const float* x_scale,
@@ -344,20 +530,23 @@ int moe_dispatch_forward(const moe_exchange_cfg_t* cfg, const int32_t* topk_ids,
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   SortArgs a{};
   a.ids = topk_ids;
+  a.T = T;
+  a.k = cfg->top_k;
   a.S = (int)S;
   a.E = cfg->n_experts;
-  a.chunk = chunk_slots(a.S);
   a.chunks = chunk_count(a.S);
-  a.hist = static_cast<int32_t*>(ws);
+  a.chunk = chunk_slots(a.S);
+  a.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256);
   a.offsets = offsets;
   a.rows = rows;
-  EXCHANGE_CUDA(launch_pdl(sort_count_kernel, dim3(a.chunks), dim3(kSortThreads), 0, s, a));
-  EXCHANGE_CUDA(launch_pdl(sort_place_kernel, dim3(a.chunks), dim3(kSortThreads), 0, s, a));
-  if (xs) {
-    const RowArgs r = row_args(*cfg, rows, T);
-    EXCHANGE_CUDA(launch_pdl(dispatch_rows_kernel, dim3(row_grid(r)), dim3(kRowWarps * 32), 0, s, r, static_cast<const uint4*>(x),
-                             x_scale, static_cast<uint4*>(xs), xs_scale));
-  }
+  a.vecs = xs ? (int)(row / 16) : 0;
+  a.x = static_cast<const uint4*>(x);
+  a.xs = static_cast<uint4*>(xs);
+  a.x_scale = x_scale;
+  a.xs_scale = xs_scale;
+  if (a.chunks) EXCHANGE_CUDA(launch_pdl(sort_count_kernel, dim3(a.chunks), dim3(kCountThreads), 0, s, a));
+  const int most = sm_count();
+  EXCHANGE_CUDA(launch_pdl(dispatch_kernel<1024>, dim3(T < most ? T : most), dim3(1024), 0, s, a));
   return MOE_OK;
 }
 
@@ -381,12 +570,18 @@ int moe_combine_backward(const moe_exchange_cfg_t* cfg, const void* dy, const vo
   const Span out[] = {{dz, S * row}, {dw, S * 4}};
   const Span in[] = {{dy, T * row}, {dw ? z : nullptr, S * row}, {rows, S * 4}, {w, S * 4}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
-  RowArgs a = row_args(*cfg, rows, T);
-  a.parts = cdiv(a.vecs, 64) < kRowWarps ? cdiv(a.vecs, 64) : kRowWarps;
-  const int most = 16 * sm_count();
-  EXCHANGE_CUDA(launch_pdl(combine_backward_kernel, dim3(T < most ? T : most), dim3(a.parts * 32), 0,
-                           static_cast<cudaStream_t>(stream), a, static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w,
-                           static_cast<uint4*>(dz), dw));
+  const RowPlan p = plan_backward(*cfg, rows, T);
+  auto run = [&](auto kernel, cudaError_t allowed) {
+    if (allowed != cudaSuccess) return allowed;
+    return launch_pdl(kernel, dim3(p.ctas), dim3(p.warps * 32), p.smem, static_cast<cudaStream_t>(stream), p.a,
+                      static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w, static_cast<uint4*>(dz), dw);
+  };
+  const int k = cfg->top_k;
+  EXCHANGE_CUDA(k <= 2   ? run(combine_backward_kernel<2>, allow_smem<combine_backward_kernel<2>>(kRingBytes / 2))
+                : k <= 4 ? run(combine_backward_kernel<4>, allow_smem<combine_backward_kernel<4>>(kRingBytes / 2))
+                : k <= 8 ? run(combine_backward_kernel<8>, allow_smem<combine_backward_kernel<8>>(kRingBytes / 2))
+                : k <= 16 ? run(combine_backward_kernel<16>, allow_smem<combine_backward_kernel<16>>(kRingBytes / 2))
+                          : run(combine_backward_kernel<32>, allow_smem<combine_backward_kernel<32>>(kRingBytes / 2)));
   return MOE_OK;
 }
 
