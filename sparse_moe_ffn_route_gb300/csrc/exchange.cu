@@ -43,6 +43,7 @@ struct SortArgs {
 __global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArgs a) {
   __shared__ int count[kMaxExperts];
   pdl_wait();
+  pdl_trigger();   // what does not need the counts may start
   for (int e = threadIdx.x; e < a.E; e += kCountThreads) count[e] = 0;
   __syncthreads();
   const int s0 = blockIdx.x * a.chunk, s1 = min(a.S, s0 + a.chunk);
@@ -52,7 +53,6 @@ __global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArg
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kCountThreads) a.hist[(size_t)blockIdx.x * a.E + e] = count[e];
-  pdl_trigger();
 }
 
 // Sum of four bytes of counts.
@@ -69,30 +69,25 @@ __global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
   const int s0 = t0 * a.k;
   for (int e = tid; e < a.E; e += NT) all[e] = cursor[e] = 0;
   __syncthreads();
-  pdl_wait();
-  int from = 0, to = a.S;   // ids to count here
-  if (a.chunks) {
-    const int mine = s0 / a.chunk;
-    from = mine * a.chunk;
-    to = s0;
-    for (int e = tid; e < a.E; e += NT) {
-      int sum = 0, before = 0;
-      for (int c0 = 0; c0 < a.chunks; c0 += 8) {
-        int n[8];
+  // With counts to come, only these have to be waited for: the launch that makes them has itself
+  // waited for what is before it on the stream.
+  if (!a.chunks) pdl_wait();
+  // A warp copies up to 4 x 32 vectors of a token at a time; its first ones are asked for now.
+  const int pieces = (a.vecs + 127) / 128, piece = pieces ? (a.vecs + 32 * pieces - 1) / (32 * pieces) * 32 : 0;
+  uint4 q[4];
+  auto load = [&](int u) {   // unit u of the run
+    const int i = u / pieces, v0 = (u - i * pieces) * piece;
+    const uint4* src = a.x + (size_t)(t0 + i) * a.vecs;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = c0 + i < a.chunks ? a.hist[(size_t)(c0 + i) * a.E + e] : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum += n[i];
-          before += c0 + i < mine ? n[i] : 0;
-        }
-      }
-      all[e] = sum;
-      cursor[e] = before;
+    for (int h = 0; h < 4; ++h) {
+      const int v = v0 + 32 * h + lane;
+      if (32 * h < piece && v < a.vecs) q[h] = __ldg(src + v);
     }
-    __syncthreads();
-  }
-  for (int s = from + tid; s < to; s += NT) {
+  };
+  int unit = warp;
+  if (a.vecs && unit < (t1 - t0) * pieces) load(unit);
+  const int chunk = a.chunks ? s0 / a.chunk : 0;
+  for (int s = (a.chunks ? chunk * a.chunk : 0) + tid, end = a.chunks ? s0 : a.S; s < end; s += NT) {
     const int e = a.ids[s];
     if (e >= 0 && e < a.E) {
       if (!a.chunks) atomicAdd(&all[e], 1);
@@ -100,6 +95,25 @@ __global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
     }
   }
   __syncthreads();
+  if (a.chunks) {
+    pdl_wait();
+    for (int e = tid; e < a.E; e += NT) {
+      int sum = 0, before = 0;
+      for (int c0 = 0; c0 < a.chunks; c0 += 16) {
+        int n[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n[i] = c0 + i < a.chunks ? a.hist[(size_t)(c0 + i) * a.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          sum += n[i];
+          before += c0 + i < chunk ? n[i] : 0;
+        }
+      }
+      all[e] = sum;
+      cursor[e] += before;
+    }
+    __syncthreads();
+  }
   // where each expert's rows begin: an exclusive scan, PER experts to a thread
   int mine[PER], run = 0;
 #pragma unroll
@@ -161,22 +175,22 @@ __global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
         cursor[i] += (int)n;
       }
     if (a.vecs) {
-      // a warp copies up to 4 x 32 vectors of a token at a time
-      const int pieces = (a.vecs + 127) / 128;
-      for (int u = warp; u < tokens * pieces; u += W) {
-        const int i = u / pieces, v0 = (u - i * pieces) * 128 + lane;
-        const uint4* src = a.x + (size_t)(t + i) * a.vecs;
-        uint4 q[4];
+      for (; unit < (t + tokens - t0) * pieces; unit += W) {
+        const int i = unit / pieces, v0 = (unit - i * pieces) * piece;
+        uint4 p[4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (v0 + 32 * h < a.vecs) q[h] = __ldg(src + v0 + 32 * h);
+        for (int h = 0; h < 4; ++h) p[h] = q[h];
+        if (unit + W < (t1 - t0) * pieces) load(unit + W);
+        const int* to = tile_rows + (t0 + i - t) * a.k;
         for (int j = 0; j < a.k; ++j) {
-          const int r = tile_rows[i * a.k + j];
+          const int r = to[j];
           if (r < 0) continue;
           uint4* dst = a.xs + (size_t)r * a.vecs;
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (v0 + 32 * h < a.vecs) dst[v0 + 32 * h] = q[h];
+          for (int h = 0; h < 4; ++h) {
+            const int v = v0 + 32 * h + lane;
+            if (32 * h < piece && v < a.vecs) dst[v] = p[h];
+          }
         }
       }
       if (a.xs_scale && row >= 0) a.xs_scale[row] = a.x_scale[t + tid / a.k];
@@ -275,14 +289,20 @@ __global__ void __launch_bounds__(512) combine_kernel(const RowArgs a, const uin
     const uint4* slot = mine + out_slot * (a.k + 1) * 32;
     F2 sum[4] = {};
     if (residual) unpack8(slot[a.k * 32], sum);
-#pragma unroll
-    for (int j = 0; j < KT; ++j) {
+    auto add = [&](int j) {
       const F2 by = f2(__shfl_sync(0xffffffffu, c, j));
-      if (!(live >> j & 1)) continue;
       F2 f[4];
       unpack8(slot[j * 32], f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = fma2(by, f[e], sum[e]);
+    };
+    if (live == (KT == 32 ? ~0u : (1u << (KT & 31)) - 1u)) {   // no branch per row
+#pragma unroll
+      for (int j = 0; j < KT; ++j) add(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (live >> j & 1) add(j);
     }
     if (v < a.vecs) y[(size_t)t * a.vecs + v] = pack8(sum);
     if (++out_slot == a.depth) out_slot = 0;
@@ -292,104 +312,76 @@ __global__ void __launch_bounds__(512) combine_kernel(const RowArgs a, const uin
   pdl_trigger();
 }
 
-// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA takes a token at a
-// time, its warps the groups of 32 vectors in turn; each adds its part of the dot products up
-// over its groups, and they meet once per token.  KT: k rounded up to a power of two.
-template <int KT>
-__global__ void __launch_bounds__(256) combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy,
-                                                               const uint4* __restrict__ z, const float* __restrict__ w,
-                                                               uint4* dz, float* dw) {
-  extern __shared__ uint4 ring[];
-  __shared__ float part_sum[2][8][kMaxTopK];
+// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA to a token, its
+// warps the groups of 32 vectors in turn, KB rows at a time in registers; the warps add their parts
+// of the dot products up at the end.  Half of the bytes are writes, and many CTAs per SM keep
+// both ways busy: 4096 x 2048 with 8 rows a token takes 50 us, 1001 x 2880 with 4 11 us; through
+// a ring as above 51 to 59 us and 15 to 19.
+constexpr int kBackWarps = 8;
+template <int KB>
+__global__ void __launch_bounds__(kBackWarps * 32, KB == 8 ? 3 : 4)
+combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy, const uint4* __restrict__ z, const float* __restrict__ w,
+                        uint4* dz, float* dw) {
+  __shared__ float part_sum[kBackWarps][kMaxTopK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  uint4* mine = ring + (size_t)warp * a.depth * (a.k + 1) * 32 + lane;
   pdl_wait();
-  // the next unit to ask for: token `at`, group `ag`
-  int at = blockIdx.x, ag = warp, row = -1;
-  auto look = [&]() {
-    row = -1;
-    if (at < a.T && lane < a.k) row = a.rows[(size_t)at * a.k + lane];
-  };
-  look();
-  int in_slot = 0, out_slot = 0;
-  auto ask = [&]() {
-    if (at < a.T) {
-      const int v = ag * 32 + lane;
-      const bool in = v < a.vecs;
-      const uint32_t dst = shared_at(mine + in_slot * (a.k + 1) * 32);
-      if (in) copy16(dst + 512u * a.k, dy + (size_t)at * a.vecs + v);
-      if (dw)
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          const int r = __shfl_sync(0xffffffffu, row, j);
-          if ((unsigned)r < (unsigned)a.S && in) copy16(dst + 512u * j, z + (size_t)r * a.vecs + v);
-        }
-    }
-    copies_asked();
-    if (++in_slot == a.depth) in_slot = 0;
-    if ((ag += W) >= a.groups) {
-      ag = warp;
-      at += gridDim.x;
-      look();
-    }
-  };
-  for (int i = 0; i < a.depth; ++i) ask();
-  int turn = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {   // (T + the grid stay below 2^31)
-    int r = -1;
-    float c = 0.f;
-    if (lane < a.k) {
-      r = a.rows[(size_t)t * a.k + lane];
-      c = w[(size_t)t * a.k + lane];
-    }
-    const uint32_t live = __ballot_sync(0xffffffffu, (unsigned)r < (unsigned)a.S);
-    F2 acc[KT] = {};
+  const int t = blockIdx.x;
+  int r = -1;
+  float c = 0.f;
+  if (lane < a.k) {
+    r = a.rows[(size_t)t * a.k + lane];
+    c = w[(size_t)t * a.k + lane];
+    if ((unsigned)r >= (unsigned)a.S) r = -1;
+  }
+  for (int j0 = 0; j0 < a.k; j0 += KB) {
+    F2 acc[KB] = {};
     for (int g = warp; g < a.groups; g += W) {
       const int v = g * 32 + lane;
-      copies_wait(a.depth - 1);
-      const uint4* slot = mine + out_slot * (a.k + 1) * 32;
       const bool in = v < a.vecs;
+      uint4 q[KB], own = make_uint4(0u, 0u, 0u, 0u);
+      if (in) own = __ldg(dy + (size_t)t * a.vecs + v);
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        const int from = __shfl_sync(0xffffffffu, r, (j0 + i) & 31);
+        q[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (dw && in && j0 + i < a.k && from >= 0) q[i] = __ldg(z + (size_t)from * a.vecs + v);
+      }
       F2 d[4];
-      unpack8(slot[a.k * 32], d);   // lanes past the row's end hold anything, and keep it
+      unpack8(own, d);
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const F2 by = f2(__shfl_sync(0xffffffffu, c, j));
-        const int to = __shfl_sync(0xffffffffu, r, j);
-        if (!(live >> j & 1) || !in) continue;   // (live: j < k)
-        if (dw) {
-          F2 f[4];
-          unpack8(slot[j * 32], f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j] = fma2(d[e], f[e], acc[j]);
-        }
-        if (dz) {
+      for (int i = 0; i < KB; ++i) {
+        const F2 by = f2(__shfl_sync(0xffffffffu, c, (j0 + i) & 31));
+        const int to = __shfl_sync(0xffffffffu, r, (j0 + i) & 31);
+        if (dz && in && j0 + i < a.k && to >= 0) {
           F2 o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = mul2(by, d[e]);
           dz[(size_t)to * a.vecs + v] = pack8(o);
         }
+        F2 f[4];
+        unpack8(q[i], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i] = fma2(d[e], f[e], acc[i]);
       }
-      if (++out_slot == a.depth) out_slot = 0;
-      ask();
     }
     if (dw) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
-        if (j < a.k) {
-          float v = both(acc[j]);
+      for (int i = 0; i < KB; ++i) {
+        float v = both(acc[i]);
 #pragma unroll
-          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == 0) part_sum[turn][warp][j] = v;
-        }
-      __syncthreads();
-      if (warp == 0 && lane < a.k) {
-        float s = 0.f;
-        for (int p = 0; p < W; ++p) s += part_sum[turn][p][lane];
-        dw[(size_t)t * a.k + lane] = s;
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0 && j0 + i < a.k) part_sum[warp][j0 + i] = v;
       }
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (dw) {
+    __syncthreads();
+    if (warp == 0 && lane < a.k) {
+      float s = 0.f;
+      for (int p = 0; p < W; ++p) s += part_sum[p][lane];
+      dw[(size_t)t * a.k + lane] = r >= 0 ? s : 0.f;   // (without a row: 0 times what dy holds)
+    }
+  }
   pdl_trigger();
 }
 
@@ -432,21 +424,6 @@ RowPlan plan_combine(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
   p.ctas = (int)(ctas < sms ? ctas : sms);
   p.a.depth = std::min(kMostDepth, kRingBytes / (p.warps * unit));
   const long long each = (units + (long long)p.ctas * p.warps - 1) / ((long long)p.ctas * p.warps);
-  if (p.a.depth > each) p.a.depth = (int)each;
-  p.smem = p.a.depth * p.warps * unit;
-  return p;
-}
-
-// Up to 8 warps, as even a share of the groups each as can be; two CTAs per SM.
-RowPlan plan_backward(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
-  RowPlan p;
-  p.a = row_args(c, rows, T);
-  const int unit = (p.a.k + 1) * 512;
-  p.warps = cdiv(p.a.groups, cdiv(p.a.groups, 8));
-  while (p.warps > 1 && kRingBytes / 2 / (p.warps * unit) < 1) --p.warps;
-  p.ctas = std::min(T, 2 * sm_count());
-  p.a.depth = std::min(kMostDepth, kRingBytes / 2 / (p.warps * unit));
-  const long long each = (long long)cdiv(T, p.ctas) * cdiv(p.a.groups, p.warps);
   if (p.a.depth > each) p.a.depth = (int)each;
   p.smem = p.a.depth * p.warps * unit;
   return p;
@@ -546,7 +523,12 @@ int moe_dispatch_forward(const moe_exchange_cfg_t* cfg, const int32_t* topk_ids,
   a.xs_scale = xs_scale;
   if (a.chunks) EXCHANGE_CUDA(launch_pdl(sort_count_kernel, dim3(a.chunks), dim3(kCountThreads), 0, s, a));
   const int most = sm_count();
-  EXCHANGE_CUDA(launch_pdl(dispatch_kernel<1024>, dim3(T < most ? T : most), dim3(1024), 0, s, a));
+  // a token or two to a CTA: small CTAs start and meet sooner (8 tokens of 2048: 3.6 us, of
+  // 1024 threads 4.2; 512 tokens: 6.3, 6.3; 1000: 13.3, 10.4)
+  if (T <= 2 * most)
+    EXCHANGE_CUDA(launch_pdl(dispatch_kernel<256>, dim3(T < most ? T : most), dim3(256), 0, s, a));
+  else
+    EXCHANGE_CUDA(launch_pdl(dispatch_kernel<1024>, dim3(most), dim3(1024), 0, s, a));
   return MOE_OK;
 }
 
@@ -570,18 +552,11 @@ int moe_combine_backward(const moe_exchange_cfg_t* cfg, const void* dy, const vo
   const Span out[] = {{dz, S * row}, {dw, S * 4}};
   const Span in[] = {{dy, T * row}, {dw ? z : nullptr, S * row}, {rows, S * 4}, {w, S * 4}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
-  const RowPlan p = plan_backward(*cfg, rows, T);
-  auto run = [&](auto kernel, cudaError_t allowed) {
-    if (allowed != cudaSuccess) return allowed;
-    return launch_pdl(kernel, dim3(p.ctas), dim3(p.warps * 32), p.smem, static_cast<cudaStream_t>(stream), p.a,
-                      static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w, static_cast<uint4*>(dz), dw);
-  };
-  const int k = cfg->top_k;
-  EXCHANGE_CUDA(k <= 2   ? run(combine_backward_kernel<2>, allow_smem<combine_backward_kernel<2>>(kRingBytes / 2))
-                : k <= 4 ? run(combine_backward_kernel<4>, allow_smem<combine_backward_kernel<4>>(kRingBytes / 2))
-                : k <= 8 ? run(combine_backward_kernel<8>, allow_smem<combine_backward_kernel<8>>(kRingBytes / 2))
-                : k <= 16 ? run(combine_backward_kernel<16>, allow_smem<combine_backward_kernel<16>>(kRingBytes / 2))
-                          : run(combine_backward_kernel<32>, allow_smem<combine_backward_kernel<32>>(kRingBytes / 2)));
+  const RowArgs a = row_args(*cfg, rows, T);
+  const int warps = cdiv(a.groups, cdiv(a.groups, kBackWarps));
+  EXCHANGE_CUDA(launch_pdl(cfg->top_k <= 4 ? combine_backward_kernel<4> : combine_backward_kernel<8>, dim3(T), dim3(warps * 32), 0,
+                           static_cast<cudaStream_t>(stream), a, static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w,
+                           static_cast<uint4*>(dz), dw));
   return MOE_OK;
 }
 
