@@ -73,6 +73,8 @@ constexpr int kEpiWarps = 8, kProducer1 = 3 + kEpiWarps;
 enum : int { kEpiGlu = 0, kEpiStore = 1, kEpiDact = 2, kEpiLinear = 3, kEpiLinear8 = 4 };
 __host__ __device__ constexpr bool is_linear(int epi) { return epi >= kEpiLinear; }
 
+constexpr int kLinearCols = 128 * 8;   // bias and scale of 128 columns in fp32
+
 constexpr int kMaxStages = 10;
 constexpr int kInfos = 4;   // tiles worked out ahead
 
@@ -84,8 +86,9 @@ struct Lay {
   static constexpr int kSlots = EPI == kEpiDact ? 4 : 0;
   static constexpr int kRing = kSlots ? kSlots : 1;
   static constexpr int kSlotBytes = 2 * 128 * 16 * 4;
-  static constexpr int kStageSpace = 225 * 1024 - kSlots * kSlotBytes;
-  static constexpr int kSmemBytes = kStageSpace + kSlots * kSlotBytes + 1024;
+  // the linear layer's epilogue warps keep their columns' bias and scale behind the stages
+  static constexpr int kStageSpace = is_linear(EPI) ? 216 * 1024 : 225 * 1024 - kSlots * kSlotBytes;
+  static constexpr int kSmemBytes = kStageSpace + (is_linear(EPI) ? kEpiWarps * kLinearCols : kSlots * kSlotBytes) + 1024;
   static constexpr int kThreads = 32 * (4 + kEpiWarps + (EPI == kEpiDact ? 1 : 0));
 };
 
@@ -183,6 +186,17 @@ __device__ __forceinline__ int nth_tile(const GemmParams& g, int unit, int units
   }
   const long long t = unit + (long long)units * i;
   return t < g.tiles ? (int)t : -1;
+}
+
+// Four fp32 of shared memory as two pairs.
+struct alignas(16) F2x2 {
+  F2 a, b;
+};
+
+__device__ __forceinline__ uint32_t pack_pair(F2 v) {
+  float lo, hi;
+  split(v, lo, hi);
+  return pack_bf16x2(lo, hi);
 }
 
 // Descriptor of an MN-major tile of 128-byte-swizzled boxes [64 k][64 mn]: 8 k rows are
@@ -551,22 +565,29 @@ __device__ __forceinline__ void finish8(const GemmParams& g, const Problem& p, i
     *reinterpret_cast<uint4*>(g.out2 + (size_t)m * p.N + n) =
         make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
   }
-  if (is_linear(EPI)) {
+  if constexpr (is_linear(EPI)) {
     if (!valid) return;
     constexpr bool kEight = EPI == kEpiLinear8;
     const float xs = kEight ? g.lin.x_scale[m] : 1.f;
-    linear_affine8<kEight>(g.lin, xs, n, v);
+    const size_t at = (size_t)m * p.N + n;
+    F2 a[4] = {f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])};
+    linear_affine8<kEight>(g.lin, xs, n, a);
     if (p.pair) {
-      linear_affine8<kEight>(g.lin, xs, p.N + n, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = glu_value(g.lin.gated, v[i], w[i]);
+      F2 u[4] = {f2(w[0], w[1]), f2(w[2], w[3]), f2(w[4], w[5]), f2(w[6], w[7])};
+      linear_affine8<kEight>(g.lin, xs, p.N + n, u);
+      gated_values(g.lin.gated, a, u);
     } else {
-      if (g.lin.pre)
-        *reinterpret_cast<uint4*>(g.lin.pre + (size_t)m * p.N + n) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      linear_values(g.lin.act, v);
+      if (g.lin.pre) *reinterpret_cast<uint4*>(g.lin.pre + at) = pack8(a);
+      linear_values(g.lin.act, a);
     }
-    if (g.lin.residual) add_bf16x8(v, *reinterpret_cast<const uint4*>(g.lin.residual + (size_t)m * p.N + n));
+    if (g.lin.residual) {
+      F2 r[4];
+      unpack8(*reinterpret_cast<const uint4*>(g.lin.residual + at), r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = add2(a[i], r[i]);
+    }
+    *reinterpret_cast<uint4*>(p.out + at) = pack8(a);
+    return;
   }
   if (valid)
     *reinterpret_cast<uint4*>(p.out + (size_t)m * p.N + n) =
@@ -873,6 +894,33 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           wn[k] = n < 3.0e38f ? n : 0.f;
         }
       }
+      // Linear layer, asked for under the tile's MMAs as well: bias and scale of this warp's
+      // columns, 4 to a lane in the order of its chunks (gated: the gate's, then the up's); the
+      // row's scale; and the residual of the first chunk (then always the next one's).
+      uint2 lin_bias = make_uint2(0u, 0u);
+      float4 lin_scale = make_float4(0.f, 0.f, 0.f, 0.f);
+      float xs = 1.f;
+      uint4 res[4] = {};
+      const uint16_t* rrow = is_linear(EPI) && !SPLIT && g.lin.residual ? g.lin.residual + (size_t)m * p.N + n0 : nullptr;
+      auto ask = [&](int c0) {
+        if (!rrow || !valid) return;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if ((h < 2 || !p.pair) && c0 + 8 * h < cols) res[h] = *reinterpret_cast<const uint4*>(rrow + c0 + 8 * h);
+      };
+      F2* mine_cols = nullptr;
+      if (is_linear(EPI) && !SPLIT) {
+        mine_cols = reinterpret_cast<F2*>(smem + L::kStageSpace + (warp - 2) * kLinearCols);
+        const int l = lane & 15;
+        const int c = p.pair ? 32 * (l >> 2) + 16 * par + 4 * (l & 3) : 64 * (lane >> 3) + 32 * par + 4 * (lane & 7);
+        const int wr = n0 + c + (p.pair && lane >= 16 ? p.N : 0);
+        if (c < cols) {
+          if (g.lin.bias) lin_bias = __ldg(reinterpret_cast<const uint2*>(g.lin.bias + wr));
+          if (EPI == kEpiLinear8) lin_scale = __ldg(reinterpret_cast<const float4*>(g.lin.w_scale + wr));
+        }
+        if (EPI == kEpiLinear8 && valid) xs = g.lin.x_scale[m];
+        ask((p.pair ? 16 : 32) * par);
+      }
       if (!warp_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
       if (SPLIT) {
@@ -940,68 +988,89 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
             store_bf16x16(orow + c0, v, left, wide);
           }
         }
-      } else if (is_linear(EPI)) {
+      } else if constexpr (is_linear(EPI)) {
         constexpr bool kEight = EPI == kEpiLinear8;
-        const float xs = kEight && valid ? g.lin.x_scale[m] : 1.f;
+        __syncwarp();
+        mine_cols[2 * lane] = f2(bf16_lo(lin_bias.x), bf16_hi(lin_bias.x));
+        mine_cols[2 * lane + 1] = f2(bf16_lo(lin_bias.y), bf16_hi(lin_bias.y));
+        if (kEight) *reinterpret_cast<float4*>(mine_cols + 64 + 2 * lane) = lin_scale;
+        __syncwarp();
         const int rows = p.M - (m - lane);
-        const uint16_t* rrow = g.lin.residual ? g.lin.residual + (size_t)m * p.N + n0 : nullptr;
-        if (p.pair) {
-          for (int c0 = 16 * par; c0 < cols; c0 += 32) {
-            const int left = cols - c0;
-            uint4 res[2] = {};
+        // 2 N columns of the parameters' place i on
+        auto affine = [&](int i, auto& v) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (rrow && valid && 8 * h < left) res[h] = *reinterpret_cast<const uint4*>(rrow + c0 + 8 * h);
-            float v[16], w[16];
-            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), v, w);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (8 * h < left) {
-                linear_affine8<kEight>(g.lin, xs, n0 + c0 + 8 * h, v + 8 * h);
-                linear_affine8<kEight>(g.lin, xs, p.N + n0 + c0 + 8 * h, w + 8 * h);
-              }
-            if (g.lin.gated.act == MOE_ACT_CLAMPED_GLU) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = glu_value<true>(g.lin.gated, v[i], w[i]);
+          for (int j = 0; j < (int)(sizeof(v) / sizeof(F2)); j += 2) {
+            const F2x2 bias = *reinterpret_cast<const F2x2*>(mine_cols + (i >> 1) + j);
+            if (kEight) {
+              const F2x2 scale = *reinterpret_cast<const F2x2*>(mine_cols + 64 + (i >> 1) + j);
+              v[j] = fma2(mul2(v[j], f2(xs)), scale.a, bias.a);   // (the scales' product could underflow)
+              v[j + 1] = fma2(mul2(v[j + 1], f2(xs)), scale.b, bias.b);
             } else {
+              v[j] = add2(v[j], bias.a);
+              v[j + 1] = add2(v[j + 1], bias.b);
+            }
+          }
+        };
+        if (p.pair) {
+          for (int c0 = 16 * par, i = 0; c0 < cols; c0 += 32, i += 16) {
+            const uint4 now[2] = {res[0], res[1]};
+            ask(c0 + 32);
+            float x[16], y[16];
+            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(tn + c0), x, y);
+            F2 v[8], u[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = glu_value<false>(g.lin.gated, v[i], w[i]);
+            for (int j = 0; j < 8; ++j) {
+              v[j] = f2(x[2 * j], x[2 * j + 1]);
+              u[j] = f2(y[2 * j], y[2 * j + 1]);
             }
+            affine(i, v);
+            affine(64 + i, u);
+            gated_values(g.lin.gated, v, u);
             if (rrow) {
-              add_bf16x8(v, res[0]);
-              add_bf16x8(v + 8, res[1]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                F2 r[4];
+                unpack8(now[h], r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * h + j] = add2(v[4 * h + j], r[j]);
+              }
             }
-            if (valid) store_bf16x16(orow + c0, v, left, wide);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split(v[j], x[2 * j], x[2 * j + 1]);
+            if (valid) store_bf16x16(orow + c0, x, cols - c0, wide);
           }
         } else {
-          for (int c0 = 32 * par; c0 < cols; c0 += 64) {
-            const int left = cols - c0;
-            uint4 res[4] = {};
+          for (int c0 = 32 * par, i = 0; c0 < cols; c0 += 64, i += 32) {
+            const uint4 now[4] = {res[0], res[1], res[2], res[3]};
+            ask(c0 + 64);
+            float x[16], y[16];
+            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(c0 + 16), x, y);
+            F2 v[16];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (rrow && valid && 8 * h < left) res[h] = *reinterpret_cast<const uint4*>(rrow + c0 + 8 * h);
-            float v[16], w[16];
-            tmem_ld_2x16(taddr + (uint32_t)c0, taddr + (uint32_t)(c0 + 16), v, w);
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (8 * h < left) linear_affine8<kEight>(g.lin, xs, n0 + c0 + 8 * h, (h < 2 ? v : w) + 8 * (h & 1));
+            for (int j = 0; j < 8; ++j) {
+              v[j] = f2(x[2 * j], x[2 * j + 1]);
+              v[8 + j] = f2(y[2 * j], y[2 * j + 1]);
+            }
+            affine(i, v);
             uint32_t z[16];
             if (g.lin.pre) {
-              pack16(v, z);
-              pack16(w, z + 8);
-              store_32x32(g.lin.pre + (size_t)(m - lane) * p.N + n0 + c0, p.N, z, rows, left, lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) z[j] = pack_pair(v[j]);
+              store_32x32(g.lin.pre + (size_t)(m - lane) * p.N + n0 + c0, p.N, z, rows, cols - c0, lane);
             }
             linear_values(g.lin.act, v);
-            linear_values(g.lin.act, w);
             if (rrow) {
-              add_bf16x8(v, res[0]);
-              add_bf16x8(v + 8, res[1]);
-              add_bf16x8(w, res[2]);
-              add_bf16x8(w + 8, res[3]);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                F2 r[4];
+                unpack8(now[h], r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * h + j] = add2(v[4 * h + j], r[j]);
+              }
             }
-            pack16(v, z);
-            pack16(w, z + 8);
-            store_32x32(orow + c0 - (size_t)lane * p.N, p.N, z, rows, left, lane);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = pack_pair(v[j]);
+            store_32x32(orow + c0 - (size_t)lane * p.N, p.N, z, rows, cols - c0, lane);
           }
         }
       } else if (EPI == kEpiDact && tl.pi == 0) {

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dv_kernel(const uint16_t* 
   const long long first = blockIdx.y * gridDim.x + blockIdx.x;
   for (long long i = first * blockDim.x + threadIdx.x; i < zeros; i += (long long)gridDim.x * gridDim.y * blockDim.x) clear[i] = 0u;
   const int r0 = (int)((long long)T * blockIdx.y / gridDim.y), r1 = (int)((long long)T * (blockIdx.y + 1) / gridDim.y);
-  float sum[8] = {};
+  F2 sum[4] = {};
   if (col < n)
     for (int r = r0 + warp; r < r1; r += kWarps * kAhead) {
       uint4 a[kAhead], z[kAhead];
@@ -41,24 +41,22 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dv_kernel(const uint16_t* 
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (r + i * kWarps < r1) {
-          float v[8];
-          unpack_bf16x8(a[i], v);
+          F2 v[4];
+          unpack8(a[i], v);
           if (ACT != MOE_LINEAR_NONE) {
-            float p[8];
-            unpack_bf16x8(z[i], p);
+            F2 p[4];
+            unpack8(z[i], p);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], linear_slope<ACT>(p[e]));   // one value, kept or not
-            if (dv)
-              *reinterpret_cast<uint4*>(dv + (size_t)(r + i * kWarps) * n + col) =
-                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], linear_slope<ACT>(p[e]));
+            if (dv) *reinterpret_cast<uint4*>(dv + (size_t)(r + i * kWarps) * n + col) = pack8(v);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += v[e];
+          for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], v[e]);
         }
     }
   if (parts) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[warp][8 * lane + e] = sum[e];
+    for (int e = 0; e < 4; ++e) split(sum[e], sums[warp][8 * lane + 2 * e], sums[warp][8 * lane + 2 * e + 1]);
     __syncthreads();
     const int c = blockIdx.x * kCols + threadIdx.x;   // a thread to a column
     if (c < n) {

@@ -487,9 +487,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n
           o = lane < 16 ? f0 : n_out;
         } else {
           if (act.pre && in) act.pre[at] = f32_to_bf16(s);
-          float one[1] = {s};
+          F2 one[1] = {f2(s)};
           linear_values(act.act, one);
-          s = one[0];
+          float same;
+          split(one[0], s, same);
         }
         if (act.residual && in && o < n_out) s += bf16_to_f32(act.residual[at]);
       } else if (GLU) {
