@@ -181,6 +181,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
   const uint16_t* const src[2] = {g.x, Z ? g.z : nullptr};
 #pragma unroll
   for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
+  // EIGHT: fewer bytes a row, so that the weights' way from L1 shows; they stay in registers
+  constexpr bool kKeep = EIGHT && V <= 2;
+  uint4 post_w[kKeep ? V : 1], pre_w[kKeep ? V : 1];
+  if (kKeep) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ahead.elem(i) < d) {
+        if (POST) post_w[i] = ld8(g.post_w, ahead.elem(i));
+        if (PRE) pre_w[i] = ld8(g.pre_w, ahead.elem(i));
+      }
+  }
   int slot = 0, par = 0;
   for (int t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
     const size_t base = (size_t)t * d;
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
           unpack8(ahead.get(slot, 1, i), z);
           if (POST) {
             F2 w[4];
-            unpack8(ld8(g.post_w, ahead.elem(i)), w);
+            unpack8(kKeep ? post_w[kKeep ? i : 0] : ld8(g.post_w, ahead.elem(i)), w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[j] = mul2(z[j], w[j]);
           }
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       for (int i = 0; i < V; ++i)
         if (ahead.elem(i) < d) {
           F2 w[4];
-          if (PRE) unpack8(ld8(g.pre_w, ahead.elem(i)), w);
+          if (PRE) unpack8(kKeep ? pre_w[kKeep ? i : 0] : ld8(g.pre_w, ahead.elem(i)), w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (PRE) {
@@ -249,9 +260,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       float ss = both(sum);
       cta_sum_max(ss, most, buf[par][1]);
       const float r = PRE ? inv_rms(ss, inv_d, eps) : 1.f;
-      const float scale = fmaxf(__fdiv_rn(r * most, 448.f), 0x1p-126f);
+      // (a's own errors are larger than those of the faster quotients)
+      const float scale = fmaxf(PRE ? r * most * (1.f / 448.f) : __fdiv_rn(most, 448.f), 0x1p-126f);
       if (threadIdx.x == 0) g.scale[t] = scale;
-      const F2 m = f2(__fdiv_rn(1.f, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+      const F2 m = f2(PRE ? __fdividef(1.f, scale) : __fdiv_rn(1.f, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
       if (PRE) {
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -920,6 +920,9 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         }
         if (EPI == kEpiLinear8 && valid) xs = g.lin.x_scale[m];
         ask((p.pair ? 16 : 32) * par);
+        if (rrow && valid)   // the later chunks' into L2
+          for (int c0 = (p.pair ? 48 : 96) - (p.pair ? 16 : 32) * (1 - par); c0 < cols; c0 += p.pair ? 32 : 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rrow + c0));
       }
       if (!warp_wait(tc::smem_u32(&tfull_bar[b]), aph, abort, g.status)) break;
       tc::tc_fence_after();
