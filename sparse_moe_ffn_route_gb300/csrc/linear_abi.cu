@@ -109,7 +109,7 @@ int moe_linear_forward(const moe_linear_cfg_t* cfg, const void* x, const float* 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* status = static_cast<uint32_t*>(ws);
   if (T <= kSkinnyTokens)
-    LINEAR_CUDA(launch_linear_skinny(shape(*cfg), x, T, w->w, static_cast<uint16_t*>(y), e, status, s));
+    LINEAR_CUDA(launch_linear_stream(shape(*cfg), x, T, w->w, static_cast<uint16_t*>(y), e, status, s));
   else
     LINEAR_CUDA(launch_linear_gemm(shape(*cfg), x, T, w->w, static_cast<uint16_t*>(y), e, status, s));
   return MOE_OK;

@@ -32,10 +32,7 @@
 #include "block.h"
 #include "common.cuh"
 #include "glu_act.cuh"
-#include "linear_act.cuh"
 #include "tc.cuh"
-
-#include <type_traits>
 
 namespace moe {
 namespace {
@@ -126,43 +123,6 @@ struct Bf16 {
       for (int b = 0; b < 2; ++b) {
         mma_bf16_16816(acc[b][n], w[b][0].x, w[b][1].x, w[b][0].y, w[b][1].y, x.x, x.y);
         mma_bf16_16816(acc[b][n], w[b][0].z, w[b][1].z, w[b][0].w, w[b][1].w, x.z, x.w);
-      }
-    }
-  }
-};
-
-// ---------------------------------------------------------------- e4m3 weights
-// Moved as pairs, a step is 32 of them; x is e4m3 as well.  Both become f16, which holds every
-// e4m3 value, so that the products are exact and the sums fp32 as with bf16.
-struct E4m3 : Bf16 {
-  static __device__ __forceinline__ void halves(uint32_t q, uint32_t& a, uint32_t& b) {
-    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-        : "=r"(a), "=r"(b)
-        : "r"(q));
-  }
-  template <int NC>
-  __device__ __forceinline__ void multiply(const uint8_t* slot, const Scales&, int, const uint8_t* xs, int pitch,
-                                           float (&acc)[2][NC][4], int lane) const {
-    const int gq = lane >> 2, piece = ((lane & 3) ^ twist(gq)) * 16;
-    uint4 x[NC];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) x[n] = *reinterpret_cast<const uint4*>(xs + 8 * n * pitch + 16 * (lane & 3));
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint4 r0 = *reinterpret_cast<const uint4*>(slot + (16 * b + gq) * 64 + piece);
-      const uint4 r1 = *reinterpret_cast<const uint4*>(slot + (16 * b + 8 + gq) * 64 + piece);
-      const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a0, a1, a2, a3;
-        halves(w0[i], a0, a2);
-        halves(w1[i], a1, a3);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          uint32_t b0, b1;
-          halves(i == 0 ? x[n].x : i == 1 ? x[n].y : i == 2 ? x[n].z : x[n].w, b0, b1);
-          mma_f16_16816(acc[b][n], a0, a1, a2, a3, b0, b1);
-        }
       }
     }
   }
@@ -330,13 +290,11 @@ struct W4 {
 // early: what precedes on the stream is this file's gate/up kernel, which lets the next
 // start only after everything before it is done; so the weights may be read before the
 // wait for it.
-// Act: GluAct, or the linear layer's epilogue.
-template <class F, bool GLU, int NC, class Act>
+template <class F, bool GLU, int NC>
 __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n_out, const Tokens tk, const Cut cut,
-                                                                const Act act, uint16_t* y, uint16_t* y_lo,
+                                                                const GluAct act, uint16_t* y, uint16_t* y_lo,
                                                                 uint32_t* clear_status, bool early) {
   constexpr int TOK = 8 * NC, DEPTH = Mem<NC>::kDepth;
-  constexpr bool kLinear = std::is_same_v<Act, LinearEpi>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem);        // over the rings, once their steps are done with
   uint8_t* xs = smem + Mem<NC>::kRingBytes;           // [token column][k of the phase | pad]
@@ -474,26 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n
         if (isfinite(s)) s += l;
       }
       int o = u * kUnitRows + lane;
-      if constexpr (kLinear) {
-        // this lane's weight row, for scale and bias
-        const int f0 = GLU ? u * 16 + (lane & 15) : o, wr = GLU && lane >= 16 ? n_out + f0 : f0;
-        const bool in = f0 < n_out && t0 + t < tk.T;
-        if (std::is_same_v<F, E4m3> && in) s = s * act.x_scale[t0 + t] * act.w_scale[wr];
-        if (act.bias && in) s += bf16_to_f32(act.bias[wr]);
-        const size_t at = (size_t)(t0 + t) * n_out + f0;
-        if (GLU) {
-          const float up = __shfl_down_sync(0xffffffffu, s, 16);
-          s = glu_value(act.gated, s, up);
-          o = lane < 16 ? f0 : n_out;
-        } else {
-          if (act.pre && in) act.pre[at] = f32_to_bf16(s);
-          F2 one[1] = {f2(s)};
-          linear_values(act.act, one);
-          float same;
-          split(one[0], s, same);
-        }
-        if (act.residual && in && o < n_out) s += bf16_to_f32(act.residual[at]);
-      } else if (GLU) {
+      if (GLU) {
         const float up = __shfl_down_sync(0xffffffffu, s, 16);
         s = glu_value(act, s, up);
         o = lane < 16 ? u * 16 + lane : n_out;
@@ -513,8 +452,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) skinny_kernel(const F f, int n
 }
 
 // ---------------------------------------------------------------- host
-template <class F, bool GLU, int NC, class Act>
-cudaError_t launch_one(const F& f, int n_out, const Tokens& tk, const Act& act, uint16_t* y, uint16_t* y_lo,
+template <class F, bool GLU, int NC>
+cudaError_t launch_one(const F& f, int n_out, const Tokens& tk, const GluAct& act, uint16_t* y, uint16_t* y_lo,
                        uint32_t* clear_status, bool early, cudaStream_t s) {
   Cut c;
   c.units = GLU ? (n_out + 15) / 16 : (n_out + kUnitRows - 1) / kUnitRows;
@@ -533,14 +472,14 @@ cudaError_t launch_one(const F& f, int n_out, const Tokens& tk, const Act& act, 
   const int most = (Mem<NC>::kPhaseBytes / (8 * NC) - 256) / (F::kStep * 2) / kWarps * kWarps;
   c.phase_steps = c.steps <= most ? (c.steps + c.ws - 1) / c.ws * c.ws : most;
   const int smem = Mem<NC>::kRingBytes + 8 * NC * (c.phase_steps * F::kStep * 2 / 128 * 128 + 128 + F::kPad);
-  const cudaError_t e = allow_smem<skinny_kernel<F, GLU, NC, Act>>(227 * 1024);
+  const cudaError_t e = allow_smem<skinny_kernel<F, GLU, NC>>(227 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(skinny_kernel<F, GLU, NC, Act>, dim3(ctas, passes), dim3(kWarps * 32), smem, s, f, n_out, tk, c, act, y, y_lo, clear_status,
+  return launch_pdl(skinny_kernel<F, GLU, NC>, dim3(ctas, passes), dim3(kWarps * 32), smem, s, f, n_out, tk, c, act, y, y_lo, clear_status,
                     early);
 }
 
-template <class F, class Act>
-cudaError_t launch_format(const F& f, bool glu, int n_out, const Tokens& tk, const Act& act, uint16_t* y,
+template <class F>
+cudaError_t launch_format(const F& f, bool glu, int n_out, const Tokens& tk, const GluAct& act, uint16_t* y,
                           uint16_t* y_lo, uint32_t* clear_status, bool early, cudaStream_t s) {
   if (tk.T > 8 || tk.lo)
     return glu ? launch_one<F, true, 2>(f, n_out, tk, act, y, y_lo, clear_status, early, s)
@@ -556,16 +495,6 @@ cudaError_t launch_skinny_bf16(const uint16_t* w0, const uint16_t* w1, int n_out
                                uint32_t* clear_status, bool early, cudaStream_t s) {
   const GluAct act = g ? GluAct{g->act, g->limit, g->alpha} : GluAct{0, 0.f, 0.f};
   return launch_format(Bf16{w0, w1}, g != nullptr, n_out, Tokens{x, x_lo, T, n_in}, act, y, y_lo, clear_status, early, s);
-}
-
-cudaError_t launch_linear_skinny(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
-                                 uint32_t* clear_status, cudaStream_t s) {
-  const int k = l.eight ? l.n_in / 2 : l.n_in;
-  const uint16_t* w0 = static_cast<const uint16_t*>(w);
-  const Bf16 f{w0, epi.glu ? w0 + (size_t)l.n_out * k : nullptr};
-  const Tokens tk{static_cast<const uint16_t*>(x), nullptr, T, k};
-  if (l.eight) return launch_format(E4m3{f}, epi.glu, l.n_out, tk, epi, y, nullptr, clear_status, false, s);
-  return launch_format(f, epi.glu, l.n_out, tk, epi, y, nullptr, clear_status, false, s);
 }
 
 cudaError_t launch_skinny_w4(const moe_w4_cfg_t& c, const moe_w4_weights_t& w, const uint16_t* x, int T, uint16_t* y,
