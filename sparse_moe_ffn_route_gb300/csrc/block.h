@@ -91,14 +91,24 @@ cudaError_t launch_linear_stream(const LinearShape& l, const void* x, int T, con
 // backward pass does share them (split.arrived has to be zero before it).
 int linear_split_tiles(int n_in, int n_out, int T);
 bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw);
-// dx = dv W, dW = dv^T x, each where its pointer is non-null (one of them is).
+// Partial sums of a bias's gradient, [rows][n] floats (parts null: none), and where it goes.
+struct BiasParts {
+  const float* parts;
+  int rows, n;
+  uint16_t* out;
+};
+// dx = dv W, dW = dv^T x, each where its pointer is non-null (one of them is); the bias's gradient
+// on the way.
 cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
-                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, uint32_t* status, cudaStream_t s);
-// dv = dy act'(pre) (dv null: not written), dbias = the sum of its rows (null: not computed;
-// parts: linear_bias_parts(n, T) x n floats); clears *status and `zeros` words at `clear`.
+                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, const BiasParts& bias, uint32_t* status,
+                                   cudaStream_t s);
+// dv = dy act'(pre) (dv null: not written) and partial sums of its rows, linear_bias_parts(n, T)
+// x n floats (parts null: none), which the products' launch or the function after adds up; clears
+// *status and `zeros` words at `clear`.
 int linear_bias_parts(int n, int T);
-cudaError_t launch_linear_dv(int act, const uint16_t* dy, const uint16_t* pre, int T, int n, uint16_t* dv, uint16_t* dbias,
-                             float* parts, uint32_t* status, uint32_t* clear, int zeros, cudaStream_t s);
+cudaError_t launch_linear_dbias(const BiasParts& bias, cudaStream_t s);
+cudaError_t launch_linear_dv(int act, const uint16_t* dy, const uint16_t* pre, int T, int n, uint16_t* dv, float* parts,
+                             uint32_t* status, uint32_t* clear, int zeros, cudaStream_t s);
 
 // Norms (block_norm.cu).
 cudaError_t launch_block_norm_fwd(const moe_norm_cfg_t& c, const moe_norm_inputs_t& in, int T, uint16_t* y,

@@ -130,6 +130,7 @@ struct GemmParams {
   const float* norm;    // [M] | [N] | [N]; null where nothing is settled
   float gap;
   LinearEpi lin;        // kEpiLinear, kEpiLinear8
+  BiasParts bias;       // kEpiStore: partial sums to add up on the way, or none
   uint32_t* status;
   int clear_status;     // this is the call's first kernel
 };
@@ -865,6 +866,11 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
     const bool clamped = g.act.act == MOE_ACT_CLAMPED_GLU;
     int b = 0, sl = 0;                      // sl: dact, chunks seen (slot sl % kSlots)
     uint32_t aph = 0;
+    if (EPI == kEpiStore && g.bias.parts) {
+      // a linear layer's bias gradient, under the first tile's MMAs
+      pdl_wait();
+      bias_sums(g.bias, blockIdx.x * kEpiWarps + warp - 2, gridDim.x * kEpiWarps, lane);
+    }
     for (int nth = 0, t; (t = nth_tile(g, unit, units, nth)) >= 0 && __all_sync(0xffffffffu, !*abort); ++nth) {
       const Tile tl = tile_at<EPI == kEpiStore && !SPLIT>(g, t);
       const Problem& p = g.p[tl.pi];
@@ -1821,18 +1827,21 @@ bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw) {
 }
 
 cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
-                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, uint32_t* status, cudaStream_t s) {
+                                   uint16_t* dx, uint16_t* dw, const GluSplit& split, const BiasParts& bias, uint32_t* status,
+                                   cudaStream_t s) {
   const LinearBackward b = plan_linear_backward(l.n_in, l.n_out, T, dx, dw);
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.status = status;
   g.clear_status = 1;
+  g.bias = bias;
   if (b.dx_alone) {
     if (!set_problem(g.p[g.n_problems++], b.dx.cg, b.dx.tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))
       return cudaErrorInvalidValue;
     const cudaError_t e = launch<kEpiStore>(g, b.dx, s);
     if (e != cudaSuccess || !dw) return e;
     g.n_problems = g.clear_status = 0;
+    g.bias.parts = nullptr;
     dx = nullptr;
   }
   if (dx && !set_problem(g.p[g.n_problems++], b.cg, b.tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))

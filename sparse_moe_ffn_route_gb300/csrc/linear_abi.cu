@@ -146,10 +146,12 @@ int moe_linear_backward(const moe_linear_cfg_t* cfg, const void* x, int32_t T, c
   const bool products = dx || g.w, splits = linear_backward_splits(shape(*cfg), T, dx, g.w);
   const int zeros = splits ? (int)(kGluArrivedBytes / 4) : 0;
   const uint16_t* dv = static_cast<const uint16_t*>(dy);
+  float* parts = reinterpret_cast<float*>(base + L.bias);
+  const BiasParts sums{g.bias ? parts : nullptr, linear_bias_parts(cfg->n_out, T), cfg->n_out, static_cast<uint16_t*>(g.bias)};
   if (g.bias || (act && products)) {
     uint16_t* out_dv = act && products ? reinterpret_cast<uint16_t*>(base + L.dv) : nullptr;
     LINEAR_CUDA(launch_linear_dv(cfg->act, dv, static_cast<const uint16_t*>(pre), T, cfg->n_out, out_dv,
-                                 static_cast<uint16_t*>(g.bias), reinterpret_cast<float*>(base + L.bias), status, arrived, zeros, s));
+                                 g.bias ? parts : nullptr, status, arrived, zeros, s));
     if (out_dv) dv = out_dv;
   } else if (zeros) {
     LINEAR_CUDA(cudaMemsetAsync(arrived, 0, kGluArrivedBytes, s));
@@ -157,7 +159,9 @@ int moe_linear_backward(const moe_linear_cfg_t* cfg, const void* x, int32_t T, c
   if (products)
     LINEAR_CUDA(launch_linear_backward(shape(*cfg), static_cast<const uint16_t*>(x), T, static_cast<const uint16_t*>(w->w), dv,
                                        static_cast<uint16_t*>(dx), static_cast<uint16_t*>(g.w),
-                                       GluSplit{reinterpret_cast<float*>(base + L.partial), arrived}, status, s));
+                                       GluSplit{reinterpret_cast<float*>(base + L.partial), arrived}, sums, status, s));
+  else if (g.bias)
+    LINEAR_CUDA(launch_linear_dbias(sums, s));
   return MOE_OK;
 }
 

@@ -1,7 +1,7 @@
 // The linear layer's epilogue: what becomes of a sum on its way to y.
 #pragma once
 
-#include "../../include/moe_linear.h"
+#include "block.h"
 #include "f32x2.cuh"
 #include "glu_act.cuh"
 
@@ -157,6 +157,18 @@ __device__ __forceinline__ void linear_affine8(const LinearEpi& e, float xs, int
     unpack8(__ldg(reinterpret_cast<const uint4*>(e.bias + o)), b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = add2(v[i], b[i]);
+  }
+}
+
+// Columns first, first + step, ... of a bias's gradient: a warp to a column, its lanes in turn
+// down the rows of partial sums, in one order wherever this runs.
+__device__ __forceinline__ void bias_sums(const BiasParts& b, int first, int step, int lane) {
+  for (int c = first; c < b.n; c += step) {
+    float s = 0.f;
+    for (int r = lane; r < b.rows; r += 32) s += b.parts[(size_t)r * b.n + c];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) b.out[c] = f32_to_bf16(s);
   }
 }
 
