@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
 #pragma unroll
   for (int s = 0; s < DEPTH; ++s) ahead.start(s, src, blockIdx.x + s * gridDim.x, T, d);
   // EIGHT: fewer bytes a row, so that the weights' way from L1 shows; they stay in registers
-  constexpr bool kKeep = EIGHT && V <= 2;
+  constexpr bool kKeep = EIGHT && DEPTH > 1;
   uint4 post_w[kKeep ? V : 1], pre_w[kKeep ? V : 1];
   if (kKeep) {
 #pragma unroll
@@ -627,6 +627,19 @@ cudaError_t pick_fwd(const NormArgs& g, cudaStream_t s) {
 
 template <bool EIGHT>
 cudaError_t pick_fwd_width(const NormArgs& g, cudaStream_t s) {
+  if constexpr (EIGHT) {
+    // With 7 bytes an element the work per row and thread shows, and more elements to a thread
+    // share it.  8192 rows: of 1024 13.7 us with one vector, 13.9 with two; 2048 25.0, 23.9; 2880
+    // 33.6 with two, 31.8 with three (CTAs of 128 threads); 4096 44.3, 51.8; 8192 118 with
+    // two, 88 with four.
+    const int vecs = g.d / 8;
+    if (vecs <= 128) return pick_fwd<1, 3, true>(g, s);
+    if (vecs <= 256) return pick_fwd<2, 3, true>(g, s);
+    if (vecs <= 3 * 128) return pick_fwd<3, 2, true>(g, s);
+    if (vecs <= 512) return pick_fwd<2, 2, true>(g, s);
+    if (vecs <= 1024) return pick_fwd<4, 2, true>(g, s);
+    return pick_fwd<4, 1, true>(g, s);
+  }
   if (g.d <= 2048) return pick_fwd<1, 3, EIGHT>(g, s);
   if (g.d <= 8192) return pick_fwd<2, 2, EIGHT>(g, s);
   return pick_fwd<4, 1, EIGHT>(g, s);

@@ -312,8 +312,10 @@ def test_norm_quant(T, d, parts):
     if y is not None:
         close(y.t, *out["y"], "y")
         y.check()
-        want = moe.moe_block_norm_forward(cfg, x, **kw)
-        assert torch.equal(y.t, want[0])
+        # moe_block_norm_forward's y: a row's squares may be added in another order there (a thread has
+        # other elements), so that both are within the bound of the exact value, and of each other by
+        # twice that
+        close(moe.moe_block_norm_forward(cfg, x, **kw)[0], y.t.double(), 2 * out["y"][1], "y of the bf16 form")
     if full["pre_w"] is not None:
         a, ea = out["a"]
         ea = ea - H * a.abs()        # a is not rounded to bf16
