@@ -84,7 +84,8 @@ struct LinearShape {
 // Many tokens (glu_gemm.cu): y = act(x W^T ...) as epi says.
 cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
                                uint32_t* status, cudaStream_t s);
-// At most 16 tokens at a time (linear_stream.cu): the same.
+// The same for few tokens (linear_stream.cu), and whether that is the faster way.
+bool linear_streams(const LinearShape& l, int T, bool glu);
 cudaError_t launch_linear_stream(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
                                  uint32_t* clear_status, cudaStream_t s);
 // Room for a weight gradient whose tokens several units share, as glu_split_tiles; whether a

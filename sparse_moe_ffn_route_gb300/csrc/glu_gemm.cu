@@ -75,7 +75,7 @@ __host__ __device__ constexpr bool is_linear(int epi) { return epi >= kEpiLinear
 
 constexpr int kLinearCols = 128 * 8;   // bias and scale of 128 columns in fp32
 
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 20;
 constexpr int kInfos = 4;   // tiles worked out ahead
 
 // Shared memory: the ring of operand stages (A 16 KiB | B rows of this CTA, as many as the
@@ -130,6 +130,7 @@ struct GemmParams {
   const float* norm;    // [M] | [N] | [N]; null where nothing is settled
   float gap;
   LinearEpi lin;        // kEpiLinear, kEpiLinear8
+  int tile_a;           // and the bytes of a stage's rows of x: as many as there are, where fewer than 128
   BiasParts bias;       // kEpiStore: partial sums to add up on the way, or none
   uint32_t* status;
   int clear_status;     // this is the call's first kernel
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
                 ok = false;
                 break;
               }
-              const uint32_t fb = lead0 + 8u * s, sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + kTileA;
+              const uint32_t fb = lead0 + 8u * s, sa = stage0 + (uint32_t)s * kStageBytes, sb = sa + (is_linear(EPI) ? (uint32_t)g.tile_a : kTileA);
               const bool now = issued != withheld;
               if (now && rank == 0) tc::mbar_arrive_expect_tx(full0 + 8u * s, bytes);   // the peer's loads count here too
               const bool wraps = s + 2 >= kStages;
@@ -743,7 +744,8 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
         if (chunks == 0) break;
         const uint32_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;   // 16 k, in 16-byte units
         const uint64_t ad0 = a_mn ? sdesc_mn_sw128(stage0) : tc::sdesc_sw128(stage0);
-        const uint64_t bd0 = b_mn ? sdesc_mn_sw128(stage0 + kTileA) : tc::sdesc_sw128(stage0 + kTileA);
+        const uint32_t stage_b = stage0 + (is_linear(EPI) ? (uint32_t)g.tile_a : kTileA);
+        const uint64_t bd0 = b_mn ? sdesc_mn_sw128(stage_b) : tc::sdesc_sw128(stage_b);
         if (!tc::mbar_wait(tc::smem_u32(&tempty_bar[b]), aph ^ 1, abort, g.status)) break;
         tc::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)b * 256u;
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(Lay<EPI>::kThreads, 1) glu_gemm_kernel(const _
           in.b_blocks = p.b_blocks;
           in.two_b = CG == 1 && p.pair;
           in.boxes = in.b_mn ? (brows + 63) / 64 : 0;
-          in.bytes = CG * ((uint32_t)kTileA + (in.b_mn ? (uint32_t)in.boxes * 8192u : (uint32_t)brows * 128u));
+          in.bytes = CG * ((is_linear(EPI) ? (uint32_t)g.tile_a : (uint32_t)kTileA) + (in.b_mn ? (uint32_t)in.boxes * 8192u : (uint32_t)brows * 128u));
           in.idesc = (EPI == kEpiLinear8 ? tc::idesc_e4m3_f32(kBM * CG, p.tn) : tc::idesc_bf16_f32(kBM * CG, p.tn)) | ((uint32_t)in.a_mn << 15) | ((uint32_t)in.b_mn << 16);
           in.nkc = p.nkc;
           const int all = p.nkc * p.segs;
@@ -1360,10 +1362,7 @@ int stage_bytes(int cg, int tn, bool b_mn) {
   return kTileA + (b_mn ? cdiv(tn / cg, 64) * 8192 : tn / cg * 128);
 }
 
-int stages_for(int bytes, int space) {
-  const int n = space / bytes;
-  return n < kMaxStages ? n : kMaxStages;
-}
+int stages_for(int bytes, int space, int most = 10) { return std::min(most, space / bytes); }
 
 // Clocks of one chunk of 64 k with tn columns of B: the MMAs (2 per column for the 128
 // rows of an SM, and 1 in 22 more), its operands' way into shared memory (86 bytes a clock),
@@ -1485,7 +1484,14 @@ cudaError_t launch(GemmParams& g, const Way& w, cudaStream_t s) {
   for (int i = 0; i < g.n_problems; ++i) g.stage_bytes = std::max(g.stage_bytes, stage_bytes(w.cg, g.p[i].tn, g.p[i].b_mn));
   g.stage_bytes = (g.stage_bytes + 1023) / 1024 * 1024;
   // a split tile's exchange takes the partial sums of 128 rows x its columns
-  g.stages = stages_for(g.stage_bytes, Lay<EPI>::kStageSpace - (w.parts > 1 ? kBM * w.tn * 4 : 0));
+  int space = Lay<EPI>::kStageSpace - (w.parts > 1 ? kBM * w.tn * 4 : 0), most = 10;
+  if (is_linear(EPI) && g.tile_a < kTileA) {
+    // the MMAs read 128 rows all the same: what comes behind the last stage's has to be there
+    g.stage_bytes -= kTileA - g.tile_a;
+    space -= std::max(0, kTileA - g.stage_bytes);
+    most = kMaxStages;
+  }
+  g.stages = stages_for(g.stage_bytes, space, most);
   list_tiles(g, w.cg);
   if (w.parts > 1) return launch_as<1, EPI, true>(g, w, s);
   return w.cg == 2 ? launch_as<2, EPI, false>(g, w, s) : launch_as<1, EPI, false>(g, w, s);
@@ -1740,6 +1746,39 @@ cudaError_t launch_glu_backward(const GluParams& w, const uint16_t* x, const uin
 }
 
 // ---------------------------------------------------------------- the linear layer
+namespace {
+
+// The way for T <= 128 tokens, one row of tiles: the weights' stream bounds what pick_way's
+// clocks do not, epilogues and exchanges take the rows that there are, 32 to a warp, and x no
+// more of a stage than its rows (a_bytes), so that more weights are under way: 32 tokens, 8192 x
+// 8192, bf16 33.0 us with stages of 128 rows of x, 28.6 with 32, 27.4 in the way that this picks;
+// e4m3 21.1, 18.8 and 16.0; 8192 x 1024 10.7 and 8.6.
+Way pick_few(int T, int N, int chunks, int per, int a_bytes) {
+  constexpr long long kStream = 3370;   // bytes a clock from memory: 6.4 TB/s
+  Way best{1, 1, kMaxN};
+  long long least = -1;
+  const ClusterCounts counts = cluster_counts();
+  const int warps = cdiv(T, 32);
+  auto consider = [&](int parts, int tn) {
+    const int units = counts[parts], feed = (a_bytes + tn * 128) / 86;
+    const long long waves = (cdiv(N, tn / per) + units - 1) / units;
+    const int chunk = std::max(std::max(2 * tn * 23 / 22, feed), 330);
+    const int exchange = parts > 1 ? 1500 + 29 * tn * warps / 4 + 500 * (parts - 2) : 0;
+    const long long work = waves * cdiv(chunks, parts) * chunk, stream = (long long)N * per * chunks * 128 / kStream;
+    const long long cost = std::max(work, stream) + waves * (1000 + 2 * tn * warps + exchange);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = Way{1, parts, tn};
+    }
+  };
+  for (int tn = 256; tn >= 32 * per; tn -= 32) consider(1, tn);
+  for (int parts = 2; parts <= 8 && parts <= chunks; parts <<= 1)
+    for (int tn = 128; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(parts, tn);
+  return best;
+}
+
+}  // namespace
+
 cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const void* weights, uint16_t* y,
                                const LinearEpi& epi, uint32_t* status, cudaStream_t s) {
   GemmParams g;
@@ -1755,14 +1794,16 @@ cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const
   p.segs = 1;
   p.pair = epi.glu;
   p.parts = 1;
-  const Way way = pick_way(T, l.n_out, p.nkc, per, 0);
+  const int arows = std::min(kBM, (T + 7) / 8 * 8);
+  g.tile_a = arows * kBK * 2;
+  const Way way = T <= kBM ? pick_few(T, l.n_out, p.nkc, per, g.tile_a) : pick_way(T, l.n_out, p.nkc, per, 0);
   p.tn = way.tn;
   p.mt = cdiv(T, kBM * way.cg);
   p.nt = cdiv(l.n_out, p.tn / per);
   p.wide = l.n_out % 16 == 0 && aligned32(y);
   p.out = y;
   const int brows = epi.glu ? p.tn / 2 : p.tn / way.cg;
-  if (!map_bf16(&p.a[0], a, T, k, kBM) || !map_bf16(&p.b[0], b, l.n_out, k, brows) ||
+  if (!map_bf16(&p.a[0], a, T, k, arows) || !map_bf16(&p.b[0], b, l.n_out, k, brows) ||
       (epi.glu && !map_bf16(&p.b[1], b + (size_t)l.n_out * k, l.n_out, k, brows)))
     return cudaErrorInvalidValue;
   g.lin = epi;

@@ -10,10 +10,6 @@ using namespace moe;
 
 namespace {
 
-// Tokens up to which the weights stream through warp MMAs instead of tcgen05 tiles of 128
-// token rows.
-constexpr int kSkinnyTokens = 16;
-
 #define LINEAR_CUDA(call)                           \
   do {                                              \
     if ((call) != cudaSuccess) return MOE_ERR_CUDA; \
@@ -108,7 +104,7 @@ int moe_linear_forward(const moe_linear_cfg_t* cfg, const void* x, const float* 
   e.w_scale = w->scale;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* status = static_cast<uint32_t*>(ws);
-  if (T <= kSkinnyTokens)
+  if (linear_streams(shape(*cfg), T, cfg->glu))
     LINEAR_CUDA(launch_linear_stream(shape(*cfg), x, T, w->w, static_cast<uint16_t*>(y), e, status, s));
   else
     LINEAR_CUDA(launch_linear_gemm(shape(*cfg), x, T, w->w, static_cast<uint16_t*>(y), e, status, s));

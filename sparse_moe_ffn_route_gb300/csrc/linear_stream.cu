@@ -281,6 +281,16 @@ cudaError_t launch_format(StreamArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Up to 8 tokens always.  Up to 16, where the MMAs' second half of columns and x cost more,
+// unless the weights are many or x has to come in phases (16 tokens here, and 17 in tiles: 4096 x
+// 12288 gated, 8 bits 23.6 us and 20.0, bf16 37.4 and 34.1; 8192 x 1024 bf16 11.6 and 8.6; 4096 x
+// 4096 bf16 9.0 and 12.5; 2880 x 2880 7.2 and 8.5).
+bool linear_streams(const LinearShape& l, int T, bool glu) {
+  const long long row = l.eight ? l.n_in : 2LL * l.n_in;
+  if (T <= 8) return true;
+  return T <= 16 && row * l.n_out * (glu ? 2 : 1) < (64LL << 20) && T * (row + kXPad) + 2 * kWarps * kSlotBytes <= kSpace;
+}
+
 cudaError_t launch_linear_stream(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
                                  uint32_t* status, cudaStream_t s) {
   StreamArgs a{};
