@@ -75,7 +75,8 @@ size_t moe_linear_workspace_bytes(const moe_linear_cfg_t* cfg, int32_t T);
 
 /* y [T, n_out] bf16 from x [T, n_in] (x_scale fp32 [T] with MOE_LINEAR_E4M3, else NULL).
  * residual bf16 [T, n_out] or NULL; it may be y's buffer.  pre: NULL, or bf16 [T, n_out]
- * (glu = 0) that receives v rounded, for moe_linear_backward.  Otherwise no output may share
+ * (glu = 0) that receives v rounded, for moe_linear_backward.  x_scale need only be aligned to
+ * 4 bytes, so that a run of sorted rows (moe_exchange.h) can be passed.  Otherwise no output may share
  * memory with an input or another output (MOE_ERR_INVALID_ARG). */
 int moe_linear_forward(const moe_linear_cfg_t* cfg, const void* x, const float* x_scale, int32_t T,
                        const moe_linear_weights_t* w, const void* residual, void* y, void* pre, void* ws,

@@ -86,7 +86,8 @@ int moe_linear_forward(const moe_linear_cfg_t* cfg, const void* x, const float* 
   const bool eight = cfg->format == MOE_LINEAR_E4M3;
   if (!x || !w || !w->w || !y || !ws || (eight != (x_scale != nullptr)) || (eight != (w->scale != nullptr)) || (pre && cfg->glu))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x, x_scale, w->w, w->scale, w->bias, residual, y, pre, ws)) return MOE_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(x_scale) & 3u) return MOE_ERR_ALIGNMENT;
+  if (!aligned16(x, w->w, w->scale, w->bias, residual, y, pre, ws)) return MOE_ERR_ALIGNMENT;
   if (ws_bytes < 256) return MOE_ERR_WORKSPACE;
   const size_t rows = (size_t)cfg->n_out * (cfg->glu ? 2 : 1), each = eight ? 1 : 2, outs = (size_t)T * cfg->n_out * 2;
   const Span out[] = {{y, outs}, {pre, outs}, {ws, 256}};

@@ -251,6 +251,18 @@ def test_scales_at_the_ends_of_their_range():
         assert torch.isinf(y[~small]).all() or (v[~small].abs() < 2.0 ** 128).any()
 
 
+@pytest.mark.parametrize("T", [3, 16, 40, 300])
+def test_scales_of_a_run_of_rows(T):
+    """x_scale may start on any fp32."""
+    x, xs, w, r, _ = inputs(T, 128, 96, moe.LINEAR_E4M3, seed=60)
+    cfg = moe.linear_cfg(128, 96, fmt=moe.LINEAR_E4M3)
+    want = moe.moe_linear_forward(cfg, x, w, x_scale=xs, residual=r)
+    for shift in (1, 2, 3):
+        room = torch.full((T + 8,), float("nan"), device="cuda")
+        room[shift:shift + T] = xs
+        assert torch.equal(moe.moe_linear_forward(cfg, x, w, x_scale=room[shift:shift + T], residual=r), want)
+
+
 def test_no_tokens():
     x, _, w, _, _ = inputs(4, 64, 48)
     cfg = moe.linear_cfg(64, 48)

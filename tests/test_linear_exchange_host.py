@@ -67,7 +67,7 @@ def test_linear_arguments_refused():
     for kw in (dict(x=A + 8), dict(w=(B + 2, None, C)), dict(w=(B, None, C + 4)), dict(res=D + 8), dict(y=E + 8), dict(pre=I + 8),
                dict(ws=G + 8)):
         assert forward(c, **kw) == ALIGNMENT, kw
-    assert forward(e, xs=I + 4, w=(B, J, C)) == ALIGNMENT and forward(e, xs=I, w=(B, J + 4, C)) == ALIGNMENT
+    assert forward(e, xs=I + 2, w=(B, J, C)) == ALIGNMENT and forward(e, xs=I, w=(B, J + 4, C)) == ALIGNMENT
     assert forward(c, wb=255) == WORKSPACE
     # shared memory: y with x, the weights, the bias, half of the residual, pre and the workspace
     for kw in (dict(y=A + 16), dict(y=B), dict(y=C), dict(y=D + 64), dict(pre=E + 16), dict(pre=D), dict(y=G + 16), dict(pre=A)):
