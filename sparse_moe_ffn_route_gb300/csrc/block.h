@@ -88,10 +88,17 @@ cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const
 bool linear_streams(const LinearShape& l, int T, bool glu);
 cudaError_t launch_linear_stream(const LinearShape& l, const void* x, int T, const void* w, uint16_t* y, const LinearEpi& epi,
                                  uint32_t* clear_status, cudaStream_t s);
-// Room for a weight gradient whose tokens several units share, as glu_split_tiles; whether a
-// backward pass does share them (split.arrived has to be zero before it).
+// Room for a weight gradient whose tokens several units share, as glu_split_tiles.
 int linear_split_tiles(int n_in, int n_out, int T);
-bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw);
+// How the two products of a backward pass are laid out: dx in a launch of its own (where it is the
+// only product, or its long sum over few tiles is split) or beside dW, and over how many
+// units the tokens of a tile of dW (parts > 1: split.arrived has to be zero before).
+struct LinearPlan {
+  int dx_cg, dx_parts, dx_tn;
+  int cg, parts, tn;
+  bool dx_alone;
+};
+LinearPlan plan_linear_backward(const LinearShape& l, int T, bool dx, bool dw);
 // Partial sums of a bias's gradient, [rows][n] floats (parts null: none), and where it goes.
 struct BiasParts {
   const float* parts;
@@ -100,7 +107,7 @@ struct BiasParts {
 };
 // dx = dv W, dW = dv^T x, each where its pointer is non-null (one of them is); the bias's gradient
 // on the way.
-cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
+cudaError_t launch_linear_backward(const LinearShape& l, const LinearPlan& plan, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
                                    uint16_t* dx, uint16_t* dw, const GluSplit& split, const BiasParts& bias, uint32_t* status,
                                    cudaStream_t s);
 // dv = dy act'(pre) (dv null: not written) and partial sums of its rows, linear_bias_parts(n, T)

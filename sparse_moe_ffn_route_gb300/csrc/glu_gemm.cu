@@ -1812,27 +1812,23 @@ cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const
   return l.eight ? launch<kEpiLinear8>(g, way, s) : launch<kEpiLinear>(g, way, s);
 }
 
-namespace {
-
-// How the two products of a linear layer's backward pass are laid out, as Backward above.
-struct LinearBackward {
-  Way dx;
-  int cg, parts, tn;
-  bool dx_alone;
-};
-
-LinearBackward plan_linear_backward(int n_in, int n_out, int T, bool dx, bool dw) {
+LinearPlan plan_linear_backward(const LinearShape& l, int T, bool dx, bool dw) {
+  const int n_in = l.n_in, n_out = l.n_out;
   constexpr int kSpace = Lay<kEpiStore>::kStageSpace;
   const ClusterCounts counts = cluster_counts();
   const int k = cdiv(T, kBK), ko = cdiv(n_out, kBK);
   auto tiles = [&](int M, int N, int cg, int tn) { return (int)std::min<long long>((long long)cdiv(M, kBM * cg) * cdiv(N, tn), 1 << 28); };
-  LinearBackward b{};
+  LinearPlan b{};
   long long least = -1, alone_dx = 0;
-  if (dx) b.dx = pick_way(T, n_in, ko, 1, kSpace, &alone_dx);
+  Way own{1, 1, kMaxN};
+  if (dx) own = pick_way(T, n_in, ko, 1, kSpace, &alone_dx);
+  b.dx_cg = own.cg;
+  b.dx_parts = own.parts;
+  b.dx_tn = own.tn;
   const int most = linear_split_tiles(n_in, n_out, T);
   Alike a[2];
   auto consider = [&](int cg, int tn, int parts) {
-    for (int alone = 0; alone <= (dx && (!dw || b.dx.parts > 1) ? 1 : 0); ++alone) {
+    for (int alone = 0; alone <= (dx && (!dw || own.parts > 1) ? 1 : 0); ++alone) {
       const int each = tiles(n_out, n_in, cg, tn);
       if (parts > 1 && (!dw || (long long)each * parts > most)) continue;
       int n = 0;
@@ -1855,31 +1851,24 @@ LinearBackward plan_linear_backward(int n_in, int n_out, int T, bool dx, bool dw
   return b;
 }
 
-}  // namespace
-
 int linear_split_tiles(int n_in, int n_out, int T) {
   const long long tiles = (long long)cdiv(n_out, 2 * kBM) * cdiv(n_in, kMaxN);
   if (T < 8 * kBK || 2 * tiles > kMaxSplit) return 0;
   return (int)std::min<long long>(kMaxParts * tiles, kMaxSplit);
 }
 
-bool linear_backward_splits(const LinearShape& l, int T, bool dx, bool dw) {
-  return dw && plan_linear_backward(l.n_in, l.n_out, T, dx, dw).parts > 1;
-}
-
-cudaError_t launch_linear_backward(const LinearShape& l, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
+cudaError_t launch_linear_backward(const LinearShape& l, const LinearPlan& b, const uint16_t* x, int T, const uint16_t* w, const uint16_t* dv,
                                    uint16_t* dx, uint16_t* dw, const GluSplit& split, const BiasParts& bias, uint32_t* status,
                                    cudaStream_t s) {
-  const LinearBackward b = plan_linear_backward(l.n_in, l.n_out, T, dx, dw);
   GemmParams g;
   std::memset(&g, 0, sizeof(g));
   g.status = status;
   g.clear_status = 1;
   g.bias = bias;
   if (b.dx_alone) {
-    if (!set_problem(g.p[g.n_problems++], b.dx.cg, b.dx.tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))
+    if (!set_problem(g.p[g.n_problems++], b.dx_cg, b.dx_tn, T, l.n_in, l.n_out, dv, nullptr, false, w, nullptr, true, dx))
       return cudaErrorInvalidValue;
-    const cudaError_t e = launch<kEpiStore>(g, b.dx, s);
+    const cudaError_t e = launch<kEpiStore>(g, Way{b.dx_cg, b.dx_parts, b.dx_tn}, s);
     if (e != cudaSuccess || !dw) return e;
     g.n_problems = g.clear_status = 0;
     g.bias.parts = nullptr;

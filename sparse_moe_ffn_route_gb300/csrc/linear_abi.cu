@@ -140,8 +140,9 @@ int moe_linear_backward(const moe_linear_cfg_t* cfg, const void* x, int32_t T, c
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   char* base = static_cast<char*>(ws);
   uint32_t *status = reinterpret_cast<uint32_t*>(base), *arrived = reinterpret_cast<uint32_t*>(base + L.arrived);
-  const bool products = dx || g.w, splits = linear_backward_splits(shape(*cfg), T, dx, g.w);
-  const int zeros = splits ? (int)(kGluArrivedBytes / 4) : 0;
+  const bool products = dx || g.w;
+  const LinearPlan plan = products ? plan_linear_backward(shape(*cfg), T, dx, g.w) : LinearPlan{};
+  const int zeros = plan.parts > 1 ? (int)(kGluArrivedBytes / 4) : 0;
   const uint16_t* dv = static_cast<const uint16_t*>(dy);
   float* parts = reinterpret_cast<float*>(base + L.bias);
   const BiasParts sums{g.bias ? parts : nullptr, linear_bias_parts(cfg->n_out, T), cfg->n_out, static_cast<uint16_t*>(g.bias)};
@@ -154,7 +155,7 @@ int moe_linear_backward(const moe_linear_cfg_t* cfg, const void* x, int32_t T, c
     LINEAR_CUDA(cudaMemsetAsync(arrived, 0, kGluArrivedBytes, s));
   }
   if (products)
-    LINEAR_CUDA(launch_linear_backward(shape(*cfg), static_cast<const uint16_t*>(x), T, static_cast<const uint16_t*>(w->w), dv,
+    LINEAR_CUDA(launch_linear_backward(shape(*cfg), plan, static_cast<const uint16_t*>(x), T, static_cast<const uint16_t*>(w->w), dv,
                                        static_cast<uint16_t*>(dx), static_cast<uint16_t*>(g.w),
                                        GluSplit{reinterpret_cast<float*>(base + L.partial), arrived}, sums, status, s));
   else if (g.bias)
