@@ -1394,7 +1394,9 @@ constexpr int kMaxParts = 8, kMaxSplit = 152;
 // waves: 493 us; no more apart than two boxes are, so the rule is a weak one).  A part of a split tile pays for the exchange (two parts of 128 columns 2.7 us,
 // of 32 columns 1.3 us).
 constexpr long long kLongClocks = 200000;
-Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = nullptr) {
+// finer: widths between 128 and 256 columns in steps of 16 (the linear layer's; 4096 x 2048 x
+// 2048 takes 144 tiles of 240 columns instead of 128 of 256 on 76 pairs, 25.0 us instead of 27.4).
+Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = nullptr, bool finer = false) {
   Way best{1, 1, kMaxN};
   long long least = -1;
   const ClusterCounts counts = cluster_counts();
@@ -1414,7 +1416,7 @@ Way pick_way(int M, int N, int chunks, int per, int space, long long* clocks = n
   for (int cg = 1; cg <= 2; ++cg)
     // boxes of 16 rows of gate and of up are too small for few tokens (16 x 1080 x 1520:
     // 18.6 us, of 32 rows 15.6; 126 x 376 x 1216: 9.9, 10.4)
-    for (int tn = 256; tn >= 32 * per; tn -= 32) consider(cg, 1, tn);
+    for (int tn = 256; tn >= 32 * per; tn -= finer && tn > 128 ? 16 : 32) consider(cg, 1, tn);
   for (int parts = 2; parts <= 8 && parts <= chunks; parts <<= 1)
     // up to 128 columns: the exchange's space leaves the ring three stages at least
     for (int tn = 128; tn >= 8 * per * parts && tn >= 32; tn >>= 1) consider(1, parts, tn);
@@ -1796,7 +1798,7 @@ cudaError_t launch_linear_gemm(const LinearShape& l, const void* x, int T, const
   p.parts = 1;
   const int arows = std::min(kBM, (T + 7) / 8 * 8);
   g.tile_a = arows * kBK * 2;
-  const Way way = T <= kBM ? pick_few(T, l.n_out, p.nkc, per, g.tile_a) : pick_way(T, l.n_out, p.nkc, per, 0);
+  const Way way = T <= kBM ? pick_few(T, l.n_out, p.nkc, per, g.tile_a) : pick_way(T, l.n_out, p.nkc, per, 0, nullptr, per == 1);
   p.tn = way.tn;
   p.mt = cdiv(T, kBM * way.cg);
   p.nt = cdiv(l.n_out, p.tn / per);
