@@ -27,7 +27,9 @@
 //
 // Measured: forward 8192 x 2880 29.7 us in the kernel, 33.3 a call (189 MB, 83% of a copy's
 // rate); backward 8192 x 2048 47.7 us (201 MB, 4.2 TB/s), bound by issue: about 3500
-// instructions a row.
+// instructions a row.  With its output in 8 bits (EIGHT: a's row is then held until its largest
+// element is known, one more exchange) 8192 x 2880 takes 31.5 us (165 MB, 78% of a copy's rate, half
+// of the issue slots), 8 x 2048 3.9 us a call, the host's launch.
 #include "block.h"
 #include "f32x2.cuh"
 

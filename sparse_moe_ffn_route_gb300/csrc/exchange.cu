@@ -4,6 +4,12 @@
 //
 // Everything here is bound by memory, and goes by token, not by sorted row: a token's row
 // is read (or written) once and its k sorted rows are written (or read) once.
+//
+// Measured, 4096 tokens of 2048 in bf16, 8 experts each of 256 (151 MB a kernel, the combine's
+// gradient 285; a copy's rate is 6.8 TB/s): sort and copy 29.1 us with the count's launch, rows
+// back 27.9 (168 MB with the residual: 6.0 TB/s), their gradient 50.0 (6.0 TB/s with the
+// weights and dy), the first's gradient 25.4 (5.9).  1001 tokens of 2880, 4 experts each of 32, where
+// the launches show: 7.9, 9.2, 11.1 and 6.0 us.  A few tokens take one launch's 3.3 to 3.6 us.
 #include <algorithm>
 
 #include "../../include/moe_exchange.h"

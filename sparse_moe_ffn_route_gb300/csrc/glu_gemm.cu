@@ -1,6 +1,7 @@
-// The dense gated FFN on the 5th-generation tensor cores: its two forward products and
-// the six of its backward pass, all D[M x N] = A[M x K] . B[N x K]^T tiles with fp32
-// accumulators in TMEM, fed by TMA through an mbarrier ring.
+// The dense gated FFN on the 5th-generation tensor cores, its two forward products and
+// the six of its backward pass, and the linear layer (moe_linear.h), all
+// D[M x N] = A[M x K] . B[N x K]^T tiles with fp32 accumulators in TMEM, fed by TMA through an
+// mbarrier ring.
 //
 //   gate/up:  g = x Wg^T, u = x Wu^T in one tile (the B tile holds tn / 2 rows of each), so
 //             that the epilogue has both and writes h = act(g, u) (and, in training, g, u;
@@ -13,6 +14,10 @@
 //   grads:    dx = dg Wg + du Wu (one sum over two runs of k), dWg = dg^T x and
 //             dWu = du^T x in one launch, so that the tiles of the small products fill the
 //             SMs that the large ones leave
+//   linear:   act(x W^T + bias) + residual, or a gated layer's two halves as gate/up; bf16, or
+//             e4m3 with a scale per row of x and of W (kind::f8f6f4; two values are moved as one
+//             of 16 bits, so that a chunk is 128 of k in the same 128 bytes)
+//   its gradients: dx = dv W and dW = dv^T x in one launch, with dv from linear_dv.cu
 //
 // An operand's k runs along its rows ("K-major": x Wg^T) or down its columns
 // ("MN-major": both operands of dg^T x).  Both are read as they lie: a K-major tile is
@@ -48,7 +53,12 @@
 // bf16 product reaches 1.87 PFLOP/s): gate/up 280 us (1.96 PFLOP/s; 325 with g and u kept,
 // 0.5 GB), down 165 us (1.67: 256 tiles on 76 pairs), dact 211 us, grads with dWd 724 us
 // (1.90).  At 4096, 2048, 512 the four launches take 20, 14, 19 and 32 us: one wave each,
-// bound by the first loads' latency and the open epilogue.
+// bound by the first loads' latency and the open epilogue.  Linear: 4096 x 2048 x 2048 25 us
+// with its bias (1.37 PFLOP/s, one wave), 30 with SiLU, residual and v kept, its gradients 42.5
+// (1.62); 8192 x 4096 x 4096 144 us (1.91), in 8 bits 79 (3.5); 8192 x 2880 x 8192 gated in 8 bits
+// 220 to 245 us by the power limit (3.5 to 3.2 PFLOP/s).  16 epilogue warps with 16 columns
+// at a time in place of 8 with 32 took 26.5 instead of 27.2 us with an activation, but 29.1
+// instead of 27.9 with a residual, since a row's pieces are then 32 bytes.
 #include <cuda.h>
 
 #include <algorithm>

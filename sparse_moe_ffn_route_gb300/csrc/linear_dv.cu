@@ -6,7 +6,8 @@
 // warp at a time (pieces of 512 bytes; of 128 bytes, with the sums meeting in a cluster, a step of
 // 4096 x 2048 x 2048 took 65 us instead of 57); each lane adds its columns up in registers, the
 // warps add theirs in order, and the launch of the products, or where there is none a second
-// kernel, adds the CTAs' partial sums in order.
+// kernel, adds the CTAs' partial sums in order.  4096 x 2048: 13 us (50 MB, 3.9 TB/s; half of the
+// issue slots), dv then lies in L2 for the products.
 #include "block.h"
 #include "common.cuh"
 #include "linear_act.cuh"
