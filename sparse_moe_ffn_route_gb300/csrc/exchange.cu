@@ -7,9 +7,9 @@
 //
 // Measured, 4096 tokens of 2048 in bf16, 8 experts each of 256 (151 MB a kernel, the combine's
 // gradient 285; a copy's rate is 6.8 TB/s): sort and copy 29.1 us with the count's launch, rows
-// back 27.9 (168 MB with the residual: 6.0 TB/s), their gradient 50.0 (6.0 TB/s with the
-// weights and dy), the first's gradient 25.4 (5.9).  1001 tokens of 2880, 4 experts each of 32, where
-// the launches show: 7.9, 9.2, 11.1 and 6.0 us.  A few tokens take one launch's 3.3 to 3.6 us.
+// back 29.3 (168 MB with the residual: 5.7 TB/s), their gradient 50.0 (6.0 TB/s with the
+// weights and dy), the first's gradient 25.2 (6.0).  1001 tokens of 2880, 4 experts each of 32, where
+// the launches show: 7.5, 4.6, 9.8 and 4.3 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
 #include <algorithm>
 
 #include "../../include/moe_exchange.h"
@@ -207,125 +207,71 @@ __global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
 }
 
 // ---------------------------------------------------------------- back: rows to their tokens
-// Rows come through shared memory: every thread copies its own vectors ahead of time
-// (cp.async; a thread reads only what it copied, so no barrier is needed), which keeps 100 KiB
-// and more per SM in flight without registers.
 struct RowArgs {
   const int32_t* rows;       // [T, k]
   int T, k, S;
   int vecs, groups;          // 16-byte vectors of a row; groups of 32 of them
-  int depth;                 // units ahead
 };
 
-__device__ __forceinline__ uint32_t shared_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the last n (at most 7) groups of this thread's copies are there.
-__device__ __forceinline__ void copies_wait(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
-}
-
-// y[t] = residual[t] + sum_j w[t, j] z[rows[t, j]].  A unit of a warp is 32 vectors of a token:
-// k rows' pieces and the residual's.  KT: k rounded up to a power of two.
-template <int KT>
-__global__ void __launch_bounds__(512) combine_kernel(const RowArgs a, const uint4* __restrict__ z, const float* __restrict__ w,
-                                                      const uint4* residual, uint4* y) {
-  extern __shared__ uint4 ring[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  uint4* mine = ring + (size_t)warp * a.depth * (a.k + 1) * 32 + lane;   // [slot][k + 1][lane]
-  // units first, first + step, ... of [token][group], without a division for each
-  const int step = gridDim.x * W, step_t = step / a.groups, step_g = step - step_t * a.groups;
-  const int first = blockIdx.x * W + warp;
-  int t = first / a.groups, g = first - t * a.groups, at = t, ag = g;   // this unit; the next to ask for
-  auto next = [&](int& tt, int& gg) {
-    tt += step_t;
-    if ((gg += step_g) >= a.groups) {
-      gg -= a.groups;
-      ++tt;
-    }
-  };
+// y[t] = residual[t] + sum_j w[t, j] z[rows[t, j]].  threadIdx.y: tokens of a CTA (whole warps
+// each); threadIdx.x and blockIdx.y: vectors of the row.  A thread has the vectors of KT rows
+// in flight, of more than 8 four at a time (2000 x 4096, 12 rows: 39 us, eight at a time 45), and
+// as many CTAs as their registers allow hide the way to a row, its number first.
+// Persistent warps that copied units of 32 vectors ahead through shared memory took 28 us instead
+// of 29 at 4096 x 2048 with 8 rows a token, but 54 instead of 34 at 8192 x 4096 with one and
+// 6.8 instead of 4.6 at 1001 x 2880 with 4: each unit then waits for its row's number.  Row
+// numbers and weights by shuffles from a lane's register: 50 us at the first of these sizes, the loads
+// wait for one another.
+template <int KT, bool MORE>
+__global__ void __launch_bounds__(256, MORE ? 5 : KT == 8 ? 4 : KT == 4 ? 5 : 8)
+combine_kernel(const RowArgs a, const uint4* __restrict__ z, const float* __restrict__ w, const uint4* residual, uint4* y) {
   pdl_wait();
-  // what lane j asks for: choice j of the next unit to ask for
-  int row = -1;
-  auto look = [&]() {
-    row = -1;
-    if (at < a.T && lane < a.k) row = a.rows[(size_t)at * a.k + lane];
-  };
-  look();
-  int in_slot = 0, out_slot = 0;
-  auto ask = [&]() {
-    if (at < a.T) {
-      const int v = ag * 32 + lane;
-      const bool in = v < a.vecs;
-      const uint32_t dst = shared_at(mine + in_slot * (a.k + 1) * 32);
+  const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.T) return;
+  int r[KT];
+  float c[KT];
+  auto look = [&](int j0) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {   // (row is -1 from k on)
-        const int r = __shfl_sync(0xffffffffu, row, j);
-        if ((unsigned)r < (unsigned)a.S && in) copy16(dst + 512u * j, z + (size_t)r * a.vecs + v);
-      }
-      if (residual && in) copy16(dst + 512u * a.k, residual + (size_t)at * a.vecs + v);
+    for (int j = 0; j < KT; ++j) {
+      r[j] = j0 + j < a.k ? a.rows[t * a.k + j0 + j] : -1;
+      if (KT <= 4) c[j] = w && j0 + j < a.k ? w[t * a.k + j0 + j] : 1.f;
+      if ((unsigned)r[j] >= (unsigned)a.S) r[j] = -1;
     }
-    copies_asked();
-    if (++in_slot == a.depth) in_slot = 0;
-    next(at, ag);
-    look();
   };
-  for (int i = 0; i < a.depth; ++i) ask();
-  for (; t < a.T; next(t, g)) {
-    const int v = g * 32 + lane;
-    int r = -1;
-    float c = 1.f;
-    if (lane < a.k) {
-      r = a.rows[(size_t)t * a.k + lane];
-      if (w) c = w[(size_t)t * a.k + lane];
-    }
-    const uint32_t live = __ballot_sync(0xffffffffu, (unsigned)r < (unsigned)a.S);
-    copies_wait(a.depth - 1);
-    const uint4* slot = mine + out_slot * (a.k + 1) * 32;
+  if (!MORE) look(0);
+  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < a.vecs; v += blockDim.x * gridDim.y) {
     F2 sum[4] = {};
-    if (residual) unpack8(slot[a.k * 32], sum);
-    auto add = [&](int j) {
-      const F2 by = f2(__shfl_sync(0xffffffffu, c, j));
-      F2 f[4];
-      unpack8(slot[j * 32], f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = fma2(by, f[e], sum[e]);
-    };
-    if (live == (KT == 32 ? ~0u : (1u << (KT & 31)) - 1u)) {   // no branch per row
-#pragma unroll
-      for (int j = 0; j < KT; ++j) add(j);
-    } else {
+    if (residual) unpack8(residual[t * a.vecs + v], sum);
+    for (int j0 = 0; j0 < (MORE ? a.k : 1); j0 += KT) {
+      if (MORE) look(j0);
+      uint4 q[KT];
 #pragma unroll
       for (int j = 0; j < KT; ++j)
-        if (live >> j & 1) add(j);
+        if (r[j] >= 0) q[j] = __ldg(z + (size_t)r[j] * a.vecs + v);
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+        if (r[j] >= 0) {
+          F2 f[4];
+          const F2 by = f2(KT <= 4 ? c[j] : w ? __ldg(w + t * a.k + j0 + j) : 1.f);   // (8 would spill)
+          unpack8(q[j], f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = fma2(by, f[e], sum[e]);
+        }
     }
-    if (v < a.vecs) y[(size_t)t * a.vecs + v] = pack8(sum);
-    if (++out_slot == a.depth) out_slot = 0;
-    ask();
+    y[t * a.vecs + v] = pack8(sum);
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
   pdl_trigger();
 }
 
 // dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA to a token, its
 // warps the groups of 32 vectors in turn, KB rows at a time in registers; the warps add their parts
 // of the dot products up at the end.  Half of the bytes are writes, and many CTAs per SM keep
-// both ways busy: 4096 x 2048 with 8 rows a token takes 50 us, 1001 x 2880 with 4 11 us; through
-// a ring as above 51 to 59 us and 15 to 19.
+// both ways busy: 4096 x 2048 with 8 rows a token takes 50 us, 1001 x 2880 with 4 10 us; through
+// rings in shared memory 51 to 59 us and 15 to 19.  One row a token, 8192 x 4096: 36 us, 52 with the
+// registers of four.
 constexpr int kBackWarps = 8;
 template <int KB>
-__global__ void __launch_bounds__(kBackWarps * 32, KB == 8 ? 3 : 4)
+__global__ void __launch_bounds__(kBackWarps * 32, KB == 8 ? 3 : KB == 4 ? 4 : KB == 2 ? 5 : 6)
 combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy, const uint4* __restrict__ z, const float* __restrict__ w,
                         uint4* dz, float* dw) {
   __shared__ float part_sum[kBackWarps][kMaxTopK];
@@ -397,14 +343,6 @@ int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
 int chunk_slots(int S) { return S <= kChunk * kMostChunks ? kChunk : cdiv(S, kMostChunks); }
 int chunk_count(int S) { return S <= kDirect ? 0 : cdiv(S, chunk_slots(S)); }
 
-// How the way back runs: warps to a CTA, CTAs, shared memory.
-struct RowPlan {
-  RowArgs a;
-  int warps, ctas, smem;
-};
-
-constexpr int kRingBytes = 200 * 1024, kMostDepth = 8;
-
 RowArgs row_args(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
   RowArgs a{};
   a.rows = rows;
@@ -414,25 +352,6 @@ RowArgs row_args(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
   a.vecs = c.d_model / 8;
   a.groups = cdiv(a.vecs, 32);
   return a;
-}
-
-// One CTA per SM, of as many warps as have two units in its ring at least; less where there are
-// few units.
-RowPlan plan_combine(const moe_exchange_cfg_t& c, const int32_t* rows, int T) {
-  RowPlan p;
-  p.a = row_args(c, rows, T);
-  const int sms = sm_count(), unit = (p.a.k + 1) * 512;
-  const long long units = (long long)T * p.a.groups;
-  p.warps = 16;
-  while (p.warps > 4 && kRingBytes / (p.warps * unit) < 2) p.warps >>= 1;
-  while (p.warps > 1 && units < (long long)p.warps * sms) p.warps >>= 1;
-  const long long ctas = (units + p.warps - 1) / p.warps;
-  p.ctas = (int)(ctas < sms ? ctas : sms);
-  p.a.depth = std::min(kMostDepth, kRingBytes / (p.warps * unit));
-  const long long each = (units + (long long)p.ctas * p.warps - 1) / ((long long)p.ctas * p.warps);
-  if (p.a.depth > each) p.a.depth = (int)each;
-  p.smem = p.a.depth * p.warps * unit;
-  return p;
 }
 
 int check_cfg(const moe_exchange_cfg_t* c, int T, bool bf16) {
@@ -461,18 +380,17 @@ int sum_rows(const moe_exchange_cfg_t* cfg, const void* z, const int32_t* rows, 
   const Span out[] = {{y, T * row}};
   const Span in[] = {{z, S * row}, {rows, S * 4}, {w, S * 4}, {residual == y ? nullptr : residual, T * row}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
-  const RowPlan p = plan_combine(*cfg, rows, T);
-  auto run = [&](auto kernel, cudaError_t allowed) {
-    if (allowed != cudaSuccess) return allowed;
-    return launch_pdl(kernel, dim3(p.ctas), dim3(p.warps * 32), p.smem, static_cast<cudaStream_t>(stream), p.a,
-                      static_cast<const uint4*>(z), w, static_cast<const uint4*>(residual), static_cast<uint4*>(y));
-  };
-  const int k = cfg->top_k;
-  EXCHANGE_CUDA(k <= 2   ? run(combine_kernel<2>, allow_smem<combine_kernel<2>>(kRingBytes))
-                : k <= 4 ? run(combine_kernel<4>, allow_smem<combine_kernel<4>>(kRingBytes))
-                : k <= 8 ? run(combine_kernel<8>, allow_smem<combine_kernel<8>>(kRingBytes))
-                : k <= 16 ? run(combine_kernel<16>, allow_smem<combine_kernel<16>>(kRingBytes))
-                          : run(combine_kernel<32>, allow_smem<combine_kernel<32>>(kRingBytes)));
+  const RowArgs a = row_args(*cfg, rows, T);
+  // 256 threads: short rows' CTAs take several tokens; with few tokens several take a row
+  const int x = std::min(256, a.groups * 32), ty = 256 / x, ctas = cdiv(T, ty), k = cfg->top_k;
+  const int pieces = std::max(1, std::min(cdiv(a.vecs, x), 4 * sm_count() / ctas));
+  auto* kernel = k == 1   ? combine_kernel<1, false>
+                 : k == 2 ? combine_kernel<2, false>
+                 : k <= 4 ? combine_kernel<4, false>
+                 : k <= 8 ? combine_kernel<8, false>
+                          : combine_kernel<4, true>;
+  EXCHANGE_CUDA(launch_pdl(kernel, dim3(ctas, pieces), dim3(x, ty), 0, static_cast<cudaStream_t>(stream), a,
+                           static_cast<const uint4*>(z), w, static_cast<const uint4*>(residual), static_cast<uint4*>(y)));
   return MOE_OK;
 }
 
@@ -560,8 +478,12 @@ int moe_combine_backward(const moe_exchange_cfg_t* cfg, const void* dy, const vo
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   const RowArgs a = row_args(*cfg, rows, T);
   const int warps = cdiv(a.groups, cdiv(a.groups, kBackWarps));
-  EXCHANGE_CUDA(launch_pdl(cfg->top_k <= 4 ? combine_backward_kernel<4> : combine_backward_kernel<8>, dim3(T), dim3(warps * 32), 0,
-                           static_cast<cudaStream_t>(stream), a, static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w,
+  const int k = cfg->top_k;
+  auto* kernel = k == 1   ? combine_backward_kernel<1>
+                 : k == 2 ? combine_backward_kernel<2>
+                 : k <= 4 ? combine_backward_kernel<4>
+                          : combine_backward_kernel<8>;
+  EXCHANGE_CUDA(launch_pdl(kernel, dim3(T), dim3(warps * 32), 0, static_cast<cudaStream_t>(stream), a, static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w,
                            static_cast<uint4*>(dz), dw));
   return MOE_OK;
 }

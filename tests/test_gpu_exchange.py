@@ -154,6 +154,14 @@ def test_combine_and_gradients(T, d, E, k):
     assert torch.equal(moe.moe_combine_backward(cfg, dy, z, rows, w, need_dz=False)[1], dw.t)
 
 
+# rows a token on both sides of each number of rows in flight; several tokens to a CTA and the last
+# CTA not full (short rows), several CTAs to a row (few tokens, long rows), rows longer than a CTA
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 5, 8, 9, 12, 13])
+@pytest.mark.parametrize("T,d", [(1, 8), (77, 40), (333, 520), (3, 16392), (700, 2056)])
+def test_combine_rows_a_token(T, d, k):
+    test_combine_and_gradients(T, d, 16, k)
+
+
 def test_combine_gradient_against_differences():
     """Directional derivatives of sum(dy y) by central differences in 64 bits; y is linear in z and in
     w apart, so the quotient is exact but for a term of h^2."""
