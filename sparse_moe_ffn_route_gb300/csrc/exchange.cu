@@ -7,9 +7,9 @@
 //
 // Measured, 4096 tokens of 2048 in bf16, 8 experts each of 256 (151 MB a kernel, the combine's
 // gradient 285; a copy's rate is 6.8 TB/s): sort and copy 29.1 us with the count's launch, rows
-// back 29.3 (168 MB with the residual: 5.7 TB/s), their gradient 50.0 (6.0 TB/s with the
-// weights and dy), the first's gradient 25.2 (6.0).  1001 tokens of 2880, 4 experts each of 32, where
-// the launches show: 7.5, 4.6, 9.8 and 4.3 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
+// back 27.4 (168 MB with the residual: 6.1 TB/s), their gradient 50.0 (6.0 TB/s with the
+// weights and dy), the first's gradient 24.9 (6.1).  1001 tokens of 2880, 4 experts each of 32, where
+// the launches show: 7.5, 4.1, 9.8 and 4.0 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
 #include <algorithm>
 
 #include "../../include/moe_exchange.h"
@@ -217,13 +217,17 @@ struct RowArgs {
 // each); threadIdx.x and blockIdx.y: vectors of the row.  A thread has the vectors of KT rows
 // in flight, of more than 8 four at a time (2000 x 4096, 12 rows: 39 us, eight at a time 45), and
 // as many CTAs as their registers allow hide the way to a row, its number first.
-// Persistent warps that copied units of 32 vectors ahead through shared memory took 28 us instead
-// of 29 at 4096 x 2048 with 8 rows a token, but 54 instead of 34 at 8192 x 4096 with one and
-// 6.8 instead of 4.6 at 1001 x 2880 with 4: each unit then waits for its row's number.  Row
+// Smaller CTAs begin and end less at one time: with 128 threads instead of 256, 8 rows at
+// 1001 x 2880 take 10.6 us instead of 12.8, 3 at 4096 x 2048 14.8 instead of 15.6, but 1 at
+// 8000 x 1024, where a CTA has too little to do, 9.9 instead of 8.6.
+// Persistent warps that copied units of 32 vectors ahead through shared memory took 27.7 us
+// (here 27.4) at 4096 x 2048 with 8 rows a token, 54 (34) at 8192 x 4096 with one and 6.8 (4.1) at
+// 1001 x 2880 with 4: each unit then waits for its row's number.  Row
 // numbers and weights by shuffles from a lane's register: 50 us at the first of these sizes, the loads
 // wait for one another.
+constexpr int combine_threads(int kt, bool more) { return kt <= 2 || more ? 256 : 128; }
 template <int KT, bool MORE>
-__global__ void __launch_bounds__(256, MORE ? 5 : KT == 8 ? 4 : KT == 4 ? 5 : 8)
+__global__ void __launch_bounds__(combine_threads(KT, MORE), MORE ? 5 : KT == 8 ? 7 : KT == 4 ? 10 : 8)
 combine_kernel(const RowArgs a, const uint4* __restrict__ z, const float* __restrict__ w, const uint4* residual, uint4* y) {
   pdl_wait();
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -381,9 +385,10 @@ int sum_rows(const moe_exchange_cfg_t* cfg, const void* z, const int32_t* rows, 
   const Span in[] = {{z, S * row}, {rows, S * 4}, {w, S * 4}, {residual == y ? nullptr : residual, T * row}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   const RowArgs a = row_args(*cfg, rows, T);
-  // 256 threads: short rows' CTAs take several tokens; with few tokens several take a row
-  const int x = std::min(256, a.groups * 32), ty = 256 / x, ctas = cdiv(T, ty), k = cfg->top_k;
-  const int pieces = std::max(1, std::min(cdiv(a.vecs, x), 4 * sm_count() / ctas));
+  // short rows' CTAs take several tokens; with few tokens several take a row
+  const int k = cfg->top_k, threads = combine_threads(k, k > 8);
+  const int x = std::min(threads, a.groups * 32), ty = threads / x, ctas = cdiv(T, ty);
+  const int pieces = std::max(1, std::min(cdiv(a.vecs, x), 1024 / threads * sm_count() / ctas));
   auto* kernel = k == 1   ? combine_kernel<1, false>
                  : k == 2 ? combine_kernel<2, false>
                  : k <= 4 ? combine_kernel<4, false>
