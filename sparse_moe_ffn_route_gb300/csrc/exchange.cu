@@ -7,9 +7,9 @@
 //
 // Measured, 4096 tokens of 2048 in bf16, 8 experts each of 256 (151 MB a kernel, the combine's
 // gradient 285; a copy's rate is 6.8 TB/s): sort and copy 29.1 us with the count's launch, rows
-// back 27.4 (168 MB with the residual: 6.1 TB/s), their gradient 50.0 (6.0 TB/s with the
+// back 27.4 (168 MB with the residual: 6.1 TB/s), their gradient 49.6 (6.1 TB/s with the
 // weights and dy), the first's gradient 24.9 (6.1).  1001 tokens of 2880, 4 experts each of 32, where
-// the launches show: 7.5, 4.1, 9.8 and 4.0 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
+// the launches show: 7.5, 4.1, 9.4 and 4.0 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
 #include <algorithm>
 
 #include "../../include/moe_exchange.h"
@@ -267,58 +267,59 @@ combine_kernel(const RowArgs a, const uint4* __restrict__ z, const float* __rest
   pdl_trigger();
 }
 
-// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  A CTA to a token, its
-// warps the groups of 32 vectors in turn, KB rows at a time in registers; the warps add their parts
-// of the dot products up at the end.  Half of the bytes are writes, and many CTAs per SM keep
-// both ways busy: 4096 x 2048 with 8 rows a token takes 50 us, 1001 x 2880 with 4 10 us; through
-// rings in shared memory 51 to 59 us and 15 to 19.  One row a token, 8192 x 4096: 36 us, 52 with the
-// registers of four.
+// dz[rows[t, j]] = w[t, j] dy[t];  dw[t, j] = dy[t] . z[rows[t, j]].  threadIdx.y: tokens of
+// a CTA (short rows); a token's warps take its vectors in turn, KB rows at a time in registers, and
+// add their parts of the dot products up at the end.  Half of the bytes are writes, and many CTAs per
+// SM keep both ways busy: 4096 x 2048 with 8 rows a token takes 50 us, 1001 x 2880 with 4 9 us;
+// through rings in shared memory 51 to 59 us and 15 to 19.  One row a token, 8192 x 4096: 35 us, 52
+// with the registers of four.  Row numbers and weights by shuffles from a lane's register instead of the
+// same loads by all threads: 9.6 instead of 9.1 us at 1001 x 2880, 74 instead of 70 at 2000 x 4096
+// with 12 rows.
 constexpr int kBackWarps = 8;
 template <int KB>
-__global__ void __launch_bounds__(kBackWarps * 32, KB == 8 ? 3 : KB == 4 ? 4 : KB == 2 ? 5 : 6)
+__global__ void __launch_bounds__(kBackWarps * 32, KB == 8 ? 3 : KB == 4 ? 4 : KB == 2 ? 5 : 7)
 combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy, const uint4* __restrict__ z, const float* __restrict__ w,
                         uint4* dz, float* dw) {
   __shared__ float part_sum[kBackWarps][kMaxTopK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, W = blockDim.x >> 5, first = threadIdx.y * W, warp = first + (threadIdx.x >> 5);
   pdl_wait();
-  const int t = blockIdx.x;
-  int r = -1;
-  float c = 0.f;
-  if (lane < a.k) {
-    r = a.rows[(size_t)t * a.k + lane];
-    c = w[(size_t)t * a.k + lane];
-    if ((unsigned)r >= (unsigned)a.S) r = -1;
-  }
-  for (int j0 = 0; j0 < a.k; j0 += KB) {
+  const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const int k = t < a.T ? a.k : 0;
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    int r[KB];
+    float c[KB];
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const long long at = t * a.k + j0 + i;
+      r[i] = j0 + i < k ? a.rows[at] : -1;
+      if (KB <= 4) c[i] = j0 + i < k ? w[at] : 0.f;
+      if ((unsigned)r[i] >= (unsigned)a.S) r[i] = -1;
+    }
     F2 acc[KB] = {};
-    for (int g = warp; g < a.groups; g += W) {
-      const int v = g * 32 + lane;
-      const bool in = v < a.vecs;
-      uint4 q[KB], own = make_uint4(0u, 0u, 0u, 0u);
-      if (in) own = __ldg(dy + (size_t)t * a.vecs + v);
+    for (int v = threadIdx.x; v < a.vecs; v += blockDim.x) {
+      uint4 q[KB];
 #pragma unroll
-      for (int i = 0; i < KB; ++i) {
-        const int from = __shfl_sync(0xffffffffu, r, (j0 + i) & 31);
-        q[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (dw && in && j0 + i < a.k && from >= 0) q[i] = __ldg(z + (size_t)from * a.vecs + v);
-      }
+      for (int i = 0; i < KB; ++i)
+        if (dw && r[i] >= 0) q[i] = __ldg(z + (size_t)r[i] * a.vecs + v);
       F2 d[4];
-      unpack8(own, d);
+      unpack8(__ldg(dy + t * a.vecs + v), d);
 #pragma unroll
-      for (int i = 0; i < KB; ++i) {
-        const F2 by = f2(__shfl_sync(0xffffffffu, c, (j0 + i) & 31));
-        const int to = __shfl_sync(0xffffffffu, r, (j0 + i) & 31);
-        if (dz && in && j0 + i < a.k && to >= 0) {
-          F2 o[4];
+      for (int i = 0; i < KB; ++i)
+        if (r[i] >= 0) {
+          if (dz) {
+            const F2 by = f2(KB <= 4 ? c[i] : __ldg(w + t * a.k + j0 + i));   // (8 would spill)
+            F2 o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = mul2(by, d[e]);
-          dz[(size_t)to * a.vecs + v] = pack8(o);
+            for (int e = 0; e < 4; ++e) o[e] = mul2(by, d[e]);
+            dz[(size_t)r[i] * a.vecs + v] = pack8(o);
+          }
+          if (dw) {
+            F2 f[4];
+            unpack8(q[i], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i] = fma2(d[e], f[e], acc[i]);
+          }
         }
-        F2 f[4];
-        unpack8(q[i], f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i] = fma2(d[e], f[e], acc[i]);
-      }
     }
     if (dw) {
 #pragma unroll
@@ -326,16 +327,16 @@ combine_backward_kernel(const RowArgs a, const uint4* __restrict__ dy, const uin
         float v = both(acc[i]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0 && j0 + i < a.k) part_sum[warp][j0 + i] = v;
+        if (lane == 0 && j0 + i < k) part_sum[warp][j0 + i] = v;
       }
     }
   }
   if (dw) {
     __syncthreads();
-    if (warp == 0 && lane < a.k) {
+    if (warp == first && lane < k) {
       float s = 0.f;
-      for (int p = 0; p < W; ++p) s += part_sum[p][lane];
-      dw[(size_t)t * a.k + lane] = r >= 0 ? s : 0.f;   // (without a row: 0 times what dy holds)
+      for (int p = first; p < first + W; ++p) s += part_sum[p][lane];
+      dw[t * a.k + lane] = s;   // (without a row: 0)
     }
   }
   pdl_trigger();
@@ -482,14 +483,16 @@ int moe_combine_backward(const moe_exchange_cfg_t* cfg, const void* dy, const vo
   const Span in[] = {{dy, T * row}, {dw ? z : nullptr, S * row}, {rows, S * 4}, {w, S * 4}};
   if (overlap(out, in)) return MOE_ERR_INVALID_ARG;
   const RowArgs a = row_args(*cfg, rows, T);
-  const int warps = cdiv(a.groups, cdiv(a.groups, kBackWarps));
+  // CTAs of at least 4 warps (20000 x 256, 2 rows a token: 9.5 us, with a CTA to a token 22; 16000 x 512,
+  // 4 rows: 25.2, with 8 warps 26)
+  const int warps = cdiv(a.groups, cdiv(a.groups, kBackWarps)), tokens = std::max(1, kBackWarps / 2 / warps);
   const int k = cfg->top_k;
   auto* kernel = k == 1   ? combine_backward_kernel<1>
                  : k == 2 ? combine_backward_kernel<2>
                  : k <= 4 ? combine_backward_kernel<4>
                           : combine_backward_kernel<8>;
-  EXCHANGE_CUDA(launch_pdl(kernel, dim3(T), dim3(warps * 32), 0, static_cast<cudaStream_t>(stream), a, static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w,
-                           static_cast<uint4*>(dz), dw));
+  EXCHANGE_CUDA(launch_pdl(kernel, dim3(cdiv(T, tokens)), dim3(warps * 32, tokens), 0, static_cast<cudaStream_t>(stream), a,
+                           static_cast<const uint4*>(dy), static_cast<const uint4*>(z), w, static_cast<uint4*>(dz), dw));
   return MOE_OK;
 }
 
