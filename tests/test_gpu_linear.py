@@ -382,6 +382,31 @@ def test_norm_quant_in_place_y():
 
 
 # ----------------------------------------------------------------------------- calls
+@pytest.mark.parametrize("T,k,n", [(5, 136, 96), (100, 136, 96), (300, 264, 304), (1200, 128, 512)])
+def test_tensors_on_odd_multiples_of_16_bytes(T, k, n):
+    """Tensors that begin 16 bytes past a multiple of 32 give the bits that aligned ones give."""
+    gen = gen_for(T, n, 16)
+
+    def off(t):
+        flat = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        step = 16 // t.element_size()
+        start = step if flat.data_ptr() % 32 == 0 else 0
+        v = flat[start:start + t.numel()].view(t.shape)
+        assert v.data_ptr() % 32 == 16
+        return v.copy_(t)
+
+    x, w, b, r, dy = rnd(gen, T, k), rnd(gen, n, k, scale=k ** -0.5), rnd(gen, n), rnd(gen, T, n), rnd(gen, T, n)
+    cfg = moe.linear_cfg(k, n, act=moe.LINEAR_GELU)
+    pre, pre2, y2 = moe.linear_pre(cfg, T), off(moe.linear_pre(cfg, T)), off(dy)
+    y = moe.moe_linear_forward(cfg, x, moe.LinearWeights(w, b), residual=r, pre=pre)
+    moe.moe_linear_forward(cfg, off(x), moe.LinearWeights(off(w), off(b)), residual=off(r), pre=pre2, y=y2)
+    assert torch.equal(y, y2) and torch.equal(pre, pre2)
+    dx, g = moe.moe_linear_backward(cfg, x, moe.LinearWeights(w, b), dy, pre=pre)
+    dx2, g2 = moe.moe_linear_backward(cfg, off(x), moe.LinearWeights(off(w), off(b)), off(dy), pre=off(pre), dx=off(dx),
+                                      grads=moe.LinearGrads(off(g.w), off(g.bias)))
+    assert torch.equal(dx, dx2) and torch.equal(g.w, g2.w) and torch.equal(g.bias, g2.bias)
+
+
 def test_captured_and_replayed_beside_eager_calls():
     T, k, n = 200, 264, 520
     x, _, w, r, gen = inputs(T, k, n, seed=40)
