@@ -11,7 +11,8 @@ namespace moe {
 
 // The kernels count rows and columns in 32 bits and step a whole grid's rows (norms: 3 rows
 // ahead of up to 2432 groups of threads) or a row's bytes (skinny.cu: 2 per input) past the
-// last one before they compare.  These bounds keep every such sum below 2^31.
+// last one before they compare.  These bounds keep every such sum below 2^31.  (What a tensor
+// takes in bytes is counted in 64 bits.)
 constexpr int kMaxTokens = 1 << 30, kMaxInputs = 1 << 29, kMaxOutputs = 1 << 30;
 
 inline size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }

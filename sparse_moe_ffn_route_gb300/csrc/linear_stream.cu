@@ -23,22 +23,13 @@
 #include "block.h"
 #include "common.cuh"
 #include "linear_act.cuh"
+#include "stream_cut.h"
 #include "tc.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16, kStepBytes = 128, kSlotBytes = 16 * kStepBytes, kMostDepth = 12;
-constexpr int kSpace = 227 * 1024;
-constexpr int kXPad = 64;        // x's rows are a multiple of 128 bytes and this apart
-constexpr int kRedPitch = 17;    // floats of a token in a warp's partial sums
-
-// What of a product a CTA does at one time.  Sizes in bytes of k.
-struct Cut {
-  int slots, ws;               // tiles at one time, warps to a tile
-  int depth;                   // steps ahead
-  int steps, phase_steps;      // of k in all, and of x in shared memory at one time
-};
+constexpr int kWarps = kStreamWarps, kSpace = kStreamSpace;
 
 struct StreamArgs {
   const uint8_t *w, *x;        // rows of `row` bytes
@@ -252,25 +243,11 @@ template <bool EIGHT, bool GLU, int NC>
 cudaError_t launch(StreamArgs& a, cudaStream_t s) {
   constexpr int TOK = 8 * NC, FEATURES = GLU ? 8 : 16;
   const int ctas = std::min(sm_count(), (a.n + 3) / 4), share = (a.n + ctas - 1) / ctas;   // four features at least
-  Cut& c = a.cut;
-  c.steps = (a.row + kStepBytes - 1) / kStepBytes;
-  c.slots = std::min((share + FEATURES - 1) / FEATURES, kWarps);
-  c.ws = std::min(kWarps / c.slots, c.steps);
-  const int warps = c.slots * c.ws, per = warps * kSlotBytes;
-  auto x_bytes = [&](int steps) { return a.T * (steps * kStepBytes + kXPad); };
-  c.phase_steps = (c.steps + c.ws - 1) / c.ws * c.ws;
-  // as many steps ahead as there is room for beside x; where that is less than two, x comes in
-  // phases of k beside four
-  const int least = std::min(2, c.phase_steps / c.ws);
-  c.depth = std::min(std::min(kMostDepth, c.phase_steps / c.ws), (kSpace - x_bytes(c.phase_steps)) / per);
-  if (c.depth < least) {
-    c.depth = 4;
-    c.phase_steps = ((kSpace - c.depth * per) / a.T - kXPad) / kStepBytes / c.ws * c.ws;
-  }
-  const int smem = std::max(c.depth * per + x_bytes(c.phase_steps), warps * TOK * kRedPitch * 4);
+  int smem;
+  a.cut = stream_cut(a.T, a.row, share, FEATURES, TOK, smem);
   const cudaError_t e = allow_smem<linear_stream_kernel<EIGHT, GLU, NC>>(kSpace);
   if (e != cudaSuccess) return e;
-  return launch_pdl(linear_stream_kernel<EIGHT, GLU, NC>, dim3(ctas), dim3(warps * 32), smem, s, a);
+  return launch_pdl(linear_stream_kernel<EIGHT, GLU, NC>, dim3(ctas), dim3(a.cut.slots * a.cut.ws * 32), smem, s, a);
 }
 
 template <bool EIGHT>
