@@ -145,17 +145,16 @@ __device__ __forceinline__ void cta_sum_max(float& sum, float& most, float* buf)
 }
 
 // 8 values times m = 1 / scale as e4m3 (to nearest even; past 448 the largest value, NaN stays
-// NaN).  EXACT: the quotient is corrected by its remainder, which rounds as the division itself
+// NaN).  The product is corrected by its remainder, so that it rounds as the division itself
 // does (Markstein): rows of bf16 values have many quotients just halfway between two codes, and
-// 2 in 1000 fell on the other side.
-template <bool EXACT>
+// without it 2 in 1000 fell on the other side.
 __device__ __forceinline__ uint2 pack_e4m3x8(const F2 (&v)[4], F2 m, F2 minus_scale) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
     F2 t = mul2(v[i], m);
-    if (EXACT) t = fma2(fma2(t, minus_scale, v[i]), m, t);
+    t = fma2(fma2(t, minus_scale, v[i]), m, t);
     split(t, lo, hi);
     uint16_t p;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(hi), "f"(lo));
@@ -262,10 +261,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       float ss = both(sum);
       cta_sum_max(ss, most, buf[par][1]);
       const float r = PRE ? inv_rms(ss, inv_d, eps) : 1.f;
-      // (a's own errors are larger than those of the faster quotients)
-      const float scale = fmaxf(PRE ? r * most * (1.f / 448.f) : __fdiv_rn(most, 448.f), 0x1p-126f);
+      // r |y pre_w| grows with |y pre_w|, roundings and all: this is the largest |a|
+      const float scale = fmaxf(__fdiv_rn(PRE ? r * most : most, 448.f), 0x1p-126f);
       if (threadIdx.x == 0) g.scale[t] = scale;
-      const F2 m = f2(PRE ? __fdividef(1.f, scale) : __fdiv_rn(1.f, scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+      const F2 m = f2(__frcp_rn(scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
       if (PRE) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       }
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (ahead.elem(i) < d) *reinterpret_cast<uint2*>(g.q + base + ahead.elem(i)) = pack_e4m3x8<!PRE>(y[i], m, minus_scale);
+        if (ahead.elem(i) < d) *reinterpret_cast<uint2*>(g.q + base + ahead.elem(i)) = pack_e4m3x8(y[i], m, minus_scale);
     } else if (PRE) {
       F2 sum = f2(0.f);
 #pragma unroll
