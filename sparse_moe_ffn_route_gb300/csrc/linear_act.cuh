@@ -97,10 +97,14 @@ __device__ __forceinline__ F2 linear_slope(F2 v) {
     return fma2(mul2(v, f2(0.39894228040143268f)), e, f2(lo < 0.f ? ql : 1.f - ql, hi < 0.f ? qh : 1.f - qh));
   }
   if (ACT == MOE_LINEAR_GELU_TANH) {
+    // s(2u) + v s(2u) s(-2u) 2u'.  Past 16 one of the logistics s is 0, and v^2 held at 256 keeps the
+    // rest finite: v^3 leaves fp32's range from 1e13 on.
     constexpr float a = kTanhSlope * kLog2E;
-    const F2 s = mul2(v, v), x = mul2(v, fma2(s, f2(a * kTanhCube), f2(a)));
-    const F2 du = mul2(v, fma2(s, f2(3.f * kTanhCube * kTanhSlope), f2(kTanhSlope)));
-    return mul2(logistic(mul2(x, f2(-1.f))), fma2(du, logistic(x), f2(1.f)));
+    float lo, hi;
+    split(mul2(v, v), lo, hi);
+    const F2 sq = f2(fminf(lo, 256.f), fminf(hi, 256.f)), x = mul2(v, fma2(sq, f2(a * kTanhCube), f2(a)));
+    const F2 up = logistic(mul2(x, f2(-1.f))), down = logistic(x);
+    return fma2(mul2(mul2(up, down), v), fma2(sq, f2(3.f * kTanhCube * kTanhSlope), f2(kTanhSlope)), up);
   }
   return f2(1.f);
 }
