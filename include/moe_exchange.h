@@ -44,7 +44,8 @@ typedef struct {
 } moe_exchange_cfg_t;
 
 /* Bytes of workspace that moe_dispatch_forward needs (0 if cfg is invalid, T < 0 or
- * T k > 2^30).  Pure host function. */
+ * T k > 2^30).  Pure host function.  The workspace begins with the status word, which the
+ * call clears (moe_device_status; nothing in the dispatch sets it). */
 size_t moe_dispatch_workspace_bytes(const moe_exchange_cfg_t* cfg, int32_t T);
 
 /* Sorts the slots of topk_ids [T, k] int32 and copies the rows of x [T, d]:

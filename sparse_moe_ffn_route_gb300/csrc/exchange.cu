@@ -44,11 +44,13 @@ struct SortArgs {
   uint4* xs;
   const float* x_scale;
   float* xs_scale;
+  uint32_t* status;          // cleared by the call's first kernel
 };
 
 __global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArgs a) {
   __shared__ int count[kMaxExperts];
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
   pdl_trigger();   // what does not need the counts may start
   for (int e = threadIdx.x; e < a.E; e += kCountThreads) count[e] = 0;
   __syncthreads();
@@ -77,7 +79,10 @@ __global__ void __launch_bounds__(NT) dispatch_kernel(const SortArgs a) {
   __syncthreads();
   // With counts to come, only these have to be waited for: the launch that makes them has itself
   // waited for what is before it on the stream.
-  if (!a.chunks) pdl_wait();
+  if (!a.chunks) {
+    pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) *a.status = 0u;
+  }
   // A warp copies up to 4 x 32 vectors of a token at a time; its first ones are asked for now.
   const int pieces = (a.vecs + 127) / 128, piece = pieces ? (a.vecs + 32 * pieces - 1) / (32 * pieces) * 32 : 0;
   uint4 q[4];
@@ -443,7 +448,8 @@ int moe_dispatch_forward(const moe_exchange_cfg_t* cfg, const int32_t* topk_ids,
   a.E = cfg->n_experts;
   a.chunks = chunk_count(a.S);
   a.chunk = chunk_slots(a.S);
-  a.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256);
+  a.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256);   // behind the status word
+  a.status = static_cast<uint32_t*>(ws);
   a.offsets = offsets;
   a.rows = rows;
   a.vecs = xs ? (int)(row / 16) : 0;
