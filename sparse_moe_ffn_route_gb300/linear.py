@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 from typing import Optional
 
 import torch
@@ -43,12 +44,12 @@ EXPORTED = ("moe_block_norm_quant", "moe_linear_workspace_bytes", "moe_linear_fo
 # ----------------------------------------------------------------------------- 8 bits
 def w8_quantize(w: torch.Tensor):
     """(codes, scale): a matrix [rows, n_in] as torch.float8_e4m3fn with an fp32 scale per row.
-    Made once per weight matrix, on whichever device holds it."""
+    A NaN does not count for its row's scale.  Made once per weight matrix, on whichever device holds it."""
     if w.dim() != 2:
         raise ValueError(f"w must have two dimensions, not {w.dim()}")
     v = w.float()
     # (torch would multiply by the rounded reciprocal of a plain number)
-    top = v.abs().amax(1) if w.shape[1] else v.new_zeros(w.shape[0])
+    top = v.abs().nan_to_num(nan=0.0, posinf=math.inf).amax(1) if w.shape[1] else v.new_zeros(w.shape[0])
     scale = (top / torch.full_like(top, E4M3_MAX)).clamp(min=LEAST_SCALE)
     return (v / scale[:, None]).to(torch.float8_e4m3fn), scale
 
