@@ -144,10 +144,22 @@ __device__ __forceinline__ void cta_sum_max(float& sum, float& most, float* buf)
   }
 }
 
-// 8 values times m = 1 / scale as e4m3 (to nearest even; past 448 the largest value, NaN stays
-// NaN).  The product is corrected by its remainder, so that it rounds as the division itself
-// does (Markstein): rows of bf16 values have many quotients just halfway between two codes, and
-// without it 2 in 1000 fell on the other side.
+// p / 448 rounded to nearest (p not negative): a product with the rounded reciprocal, corrected by its
+// remainder (Markstein); equal to the division for every mantissa, down to the least scale.
+__device__ __forceinline__ float over_448(float p) {
+  constexpr float c = 1.f / 448.f;
+  const float s = p * c;
+  return p < INFINITY ? fmaf(fmaf(s, -448.f, p), c, s) : s;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+
+// 8 values times m, 1 / scale to a step of fp32, as e4m3 (to nearest even; past 448 the largest value,
+// NaN stays NaN).  The product is corrected by its remainder, which fma holds exactly and of which
+// m's error is a share of 2^-23: so it rounds as the division itself does.  Rows of bf16 values have
+// many quotients just halfway between two codes, and without it 2 in 1000 fell on the other side.
 __device__ __forceinline__ uint2 pack_e4m3x8(const F2 (&v)[4], F2 m, F2 minus_scale) {
   uint32_t u[4];
 #pragma unroll
@@ -262,9 +274,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) block_norm_fwd_kernel(const __
       cta_sum_max(ss, most, buf[par][1]);
       const float r = PRE ? inv_rms(ss, inv_d, eps) : 1.f;
       // r |y pre_w| grows with |y pre_w|, roundings and all: this is the largest |a|
-      const float scale = fmaxf(__fdiv_rn(PRE ? r * most : most, 448.f), 0x1p-126f);
+      const float scale = fmaxf(over_448(PRE ? r * most : most), 0x1p-126f);
       if (threadIdx.x == 0) g.scale[t] = scale;
-      const F2 m = f2(__frcp_rn(scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
+      const F2 m = f2(reciprocal(scale)), minus_scale = f2(scale < 3.0e38f ? -scale : 0.f);
       if (PRE) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
