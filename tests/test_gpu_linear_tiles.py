@@ -89,3 +89,29 @@ def test_backward_to_the_bit(T, k, n):
         assert want.abs().max() < 2 ** 24
         assert torch.equal(got.t, want.bfloat16()), name
         got.check()
+
+
+# the weights' gradient cut over the tokens: its counts are cleared by a memset of its own where no launch
+# comes before the products; dx in a launch of its own; one launch for all
+@pytest.mark.parametrize("T,k,n", [(8192, 256, 512), (60, 8200, 4000), (3000, 2048, 2048)])
+def test_backward_captured(T, k, n):
+    gen = gen_for(T, n, 3)
+    x, w, dy = whole(gen, T, k), moe.LinearWeights(whole(gen, n, k)), whole(gen, T, n)
+    cfg = moe.linear_cfg(k, n)
+
+    def step():
+        dx, g = moe.moe_linear_backward(cfg, x, w, dy)
+        _, only = moe.moe_linear_backward(cfg, x, w, dy, need_dx=False)
+        return dx, g.w, only.w
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        x.copy_(whole(gen, T, k))
+        dy.copy_(whole(gen, T, n))
+        graph.replay()
+        dx, dw = dy.double() @ w.w.double(), dy.double().T @ x.double()
+        assert torch.equal(out[0], dx.bfloat16()) and torch.equal(out[1], dw.bfloat16()) and torch.equal(out[2], dw.bfloat16())
