@@ -17,8 +17,8 @@
  * backward pass of the combination then leaves either gradient in that row.)  Rows behind
  * the last slot's are left as they are.
  *
- * Sums are fp32, in the order of j, rounded once to bf16; there are no atomics, so equal
- * inputs give equal bits.  No output may share memory with an input or another output,
+ * Sums are fp32, in the order of j, rounded once to bf16, and no atomic touches them (the
+ * sort's counts are whole numbers), so equal inputs give equal bits.  No output may share memory with an input or another output,
  * but for y and residual (MOE_ERR_INVALID_ARG).
  */
 #ifndef MOE_EXCHANGE_H_
@@ -70,7 +70,7 @@ int moe_combine_forward(const moe_exchange_cfg_t* cfg, const void* z, const int3
 /* Gradients of moe_combine_forward from dy [T, d] bf16 (the residual's is dy itself):
  *   dz  bf16 [S, d] or NULL: dz[rows[t, j]] = w[t, j] dy[t]
  *   dw  fp32 [T, k] or NULL: dw[t, j] = sum_i dy[t, i] z[rows[t, j], i]  (z is read only here)
- * One of them at least is given. */
+ * One of them at least is given.  w is needed: where the forward pass went without, ones. */
 int moe_combine_backward(const moe_exchange_cfg_t* cfg, const void* dy, const void* z, const int32_t* rows,
                          const float* w, int32_t T, void* dz, float* dw, void* stream);
 

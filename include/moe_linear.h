@@ -94,7 +94,8 @@ typedef struct {
  *   dv = dy act'(pre);  dx = dv W;  dW = dv^T x;  dbias = sum_t dv
  * (the residual's gradient is dy itself).  With an activation dv is rounded to bf16 for the
  * products; dbias sums it unrounded.  dx [T, n_in] bf16 or NULL; grads or any member of it
- * NULL: not computed.  Gradients are written, not added to.  With many tokens and few
+ * NULL: not computed.  x and w->w are needed whichever of them are asked for.  Gradients are
+ * written, not added to.  With many tokens and few
  * weights the sum over the tokens is cut into parts, and which cut is taken depends on the
  * outputs asked for.  No output may share memory with an input or another output
  * (MOE_ERR_INVALID_ARG). */

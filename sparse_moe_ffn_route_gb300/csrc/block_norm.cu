@@ -28,8 +28,9 @@
 // Measured: forward 8192 x 2880 29.7 us in the kernel, 33.3 a call (189 MB, 83% of a copy's
 // rate); backward 8192 x 2048 47.7 us (201 MB, 4.2 TB/s), bound by issue: about 3500
 // instructions a row.  With its output in 8 bits (EIGHT: a's row is then held until its largest
-// element is known, one more exchange) 8192 x 2880 takes 31.5 us (165 MB, 78% of a copy's rate, half
-// of the issue slots), 8 x 2048 3.9 us a call, the host's launch.
+// element is known, which comes with sum y^2; without pre_w it is an exchange of its own) 8192 x 2880
+// takes 31.7 us (165 MB, 78% of a copy's rate, 56% of the issue slots), 8 x 2048 3.3 us a call, the
+// host's launch.
 #include "block.h"
 #include "f32x2.cuh"
 
@@ -642,9 +643,15 @@ template <bool EIGHT>
 cudaError_t pick_fwd_width(const NormArgs& g, cudaStream_t s) {
   if constexpr (EIGHT) {
     // With 7 bytes an element the work per row and thread shows, and more elements to a thread
-    // share it.  8192 rows: of 1024 13.7 us with one vector, 13.9 with two; 2048 25.0, 23.9; 2880
-    // 33.6 with two, 31.8 with three (CTAs of 128 threads); 4096 44.3, 51.8; 8192 118 with
-    // two, 88 with four.
+    // share it.  8192 rows, us with one, two, three and four vectors a thread (rows ahead 3, 2, 2, 2;
+    // two with 3 ahead up to 2048 columns):
+    //   1024  13.9  14.1  14.5  14.9      4096  52.8  45.5  51.9  44.2
+    //   1536  20.0  19.4  17.8  21.1      5120        62.5  58.0  58.6
+    //   2048  25.4  24.4  24.0  24.8      6144        69.1  62.7  78.8
+    //   2880  37.2  34.5  31.4  35.2      7168       112.5 104.5  84.8
+    //   3584  48.3  44.0  39.9  42.0      8192       119.1 112.6  89.5
+    // The steps go by how many CTAs still fit; between these widths the rule is a weak one (three vectors
+    // would take 39.9 at 3584 and 62.7 at 6144, where it has two and four).
     const int vecs = g.d / 8;
     if (vecs <= 128) return pick_fwd<1, 3, true>(g, s);
     if (vecs <= 256) return pick_fwd<2, 3, true>(g, s);

@@ -7,8 +7,8 @@
 //
 // Measured, 4096 tokens of 2048 in bf16, 8 experts each of 256 (151 MB a kernel, the combine's
 // gradient 285; a copy's rate is 6.8 TB/s): sort and copy 29.1 us with the count's launch, rows
-// back 27.4 (168 MB with the residual: 6.1 TB/s), their gradient 49.6 (6.1 TB/s with the
-// weights and dy), the first's gradient 24.9 (6.1).  1001 tokens of 2880, 4 experts each of 32, where
+// back 27.4 (168 MB with the residual: 6.1 TB/s), their gradient 49.6 (5.75 TB/s),
+// the first's gradient 24.9 (6.1).  1001 tokens of 2880, 4 experts each of 32, where
 // the launches show: 7.5, 4.1, 9.4 and 4.0 us from L2.  A few tokens take one launch's 3.1 to 3.6 us.
 #include <algorithm>
 
